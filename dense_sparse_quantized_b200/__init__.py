@@ -32,10 +32,14 @@ MODE_LUT_ROW = 0
 MODE_AFFINE_G16 = 1
 MODE_BITPLANE = 2
 MODE_INTGRID = 3
+DTYPE_F16 = 0
+DTYPE_BF16 = 1
+DTYPE_F32 = 2
 
 EXPORTS = ("dsq_pack", "dsq_pack_two_axis", "dsq_pack_intgrid", "dsq_blob_desc", "dsq_create", "dsq_gemv", "dsq_gemv_launches", "dsq_decode",
            "dsq_handle_desc", "dsq_device_bytes", "dsq_check", "dsq_destroy", "dsq_status_string",
-           "dsq_gemv_noalloc", "dsq_selftest_wait_timeout", "dsq_decompose")
+           "dsq_gemv_noalloc", "dsq_selftest_wait_timeout", "dsq_decompose",
+           "dsq_kv_bytes", "dsq_kv_append", "dsq_kv_read", "dsq_kv_attend")
 
 
 class DSQError(RuntimeError):
@@ -47,6 +51,26 @@ class DSQError(RuntimeError):
 class Desc(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("bits", ctypes.c_int32),
                 ("mode", ctypes.c_int32), ("nnz", ctypes.c_int64)]
+
+
+class KVDesc(ctypes.Structure):
+    _fields_ = [("device", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("pages", ctypes.c_int32)]
+
+
+class KVRows(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_token", ctypes.c_int64),
+                ("k_head", ctypes.c_int64), ("v_token", ctypes.c_int64), ("v_head", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
+
+
+class KVQueries(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("q_token", ctypes.c_int64), ("q_head", ctypes.c_int64), ("out_token", ctypes.c_int64),
+                ("out_head", ctypes.c_int64), ("q_tokens", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("q_heads", ctypes.c_int32), ("batch", ctypes.c_int32), ("table_pages", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("window", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("page_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("q_start", ctypes.c_void_p)]
 
 
 _lib = None
@@ -78,6 +102,11 @@ def library() -> ctypes.CDLL:
         lib.dsq_gemv_noalloc.argtypes = [ctypes.POINTER(Desc), P, SZ, P, P, I, P]
         lib.dsq_selftest_wait_timeout.argtypes = [P, P]
         lib.dsq_decompose.argtypes = [ctypes.POINTER(Desc), P, P, P, P, P, P, P, P, ctypes.POINTER(SZ), P]
+        lib.dsq_kv_bytes.argtypes = [ctypes.POINTER(KVDesc), ctypes.POINTER(SZ)]
+        lib.dsq_kv_append.argtypes = [ctypes.POINTER(KVDesc), P, ctypes.POINTER(KVRows), P, ctypes.c_int64, P]
+        lib.dsq_kv_read.argtypes = [ctypes.POINTER(KVDesc), P, ctypes.POINTER(KVRows), P, ctypes.c_int64, P]
+        lib.dsq_kv_attend.argtypes = [ctypes.POINTER(KVDesc), P, ctypes.POINTER(KVQueries), P,
+                                      ctypes.POINTER(SZ), P]
         lib.dsq_status_string.argtypes = [I]
         lib.dsq_status_string.restype = ctypes.c_char_p
         for name in EXPORTS:
@@ -334,3 +363,165 @@ def decompose(w, bits: int, mode: str, nnz: int, stream=None, workspace=None):
                                    col_idx.data_ptr(), values.data_ptr(), workspace.data_ptr(),
                                    ctypes.byref(size), _stream_ptr(stream)), "dsq_decompose")
     return codes, table, zeros, row_ptr, col_idx[:nnz], values[:nnz]
+
+
+class KVCache:
+    """The keys and values of one layer in 4-bit codes, in pages (dsq_kv_*).
+
+    ``data``: cuda uint8 memory of KVCache.bytes_for(...) bytes to use (a
+    stored cache, or a host program's own pool); allocated and zeroed
+    otherwise.  A token's slot is page * page_tokens + offset.  Calls are
+    asynchronous on ``stream`` (default: the current torch stream of the
+    cache's device) and work on the cache's device, whichever is current.
+
+        kv = KVCache(kv_heads=8, head_dim=128, pages=1024)
+        kv.append(k, v, slots)                    # k, v: [tokens, kv_heads, head_dim]
+        out = kv.attend(q, page_table, kv_lens)   # q: [batch, q_heads, head_dim]
+        k, v = kv.read(slots)
+    """
+
+    def __init__(self, kv_heads: int, head_dim: int, pages: int, page_tokens: int = 64, device: int = 0,
+                 data=None):
+        import torch
+        if data is not None:
+            if data.dtype != torch.uint8 or not data.is_cuda or not data.is_contiguous():
+                raise ValueError("data must be a contiguous cuda uint8 tensor")
+            device = data.device.index
+        self.desc = KVDesc(int(device), int(kv_heads), int(head_dim), int(page_tokens), int(pages))
+        size = self.bytes_for(kv_heads, head_dim, pages, page_tokens)
+        if data is None:
+            data = torch.zeros(size, dtype=torch.uint8, device=f"cuda:{int(device)}")
+        elif data.numel() != size:
+            raise ValueError(f"data has {data.numel()} bytes, the cache takes {size}")
+        self.data = data
+        self.device = data.device
+        self.kv_heads, self.head_dim = int(kv_heads), int(head_dim)
+        self.page_tokens, self.pages = int(page_tokens), int(pages)
+        self._d = ctypes.byref(self.desc)
+        self._dtypes = {torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+
+    @staticmethod
+    def bytes_for(kv_heads: int, head_dim: int, pages: int, page_tokens: int = 64) -> int:
+        """Bytes of a cache of that shape (dsq_kv_bytes)."""
+        size = ctypes.c_size_t(0)
+        d = KVDesc(0, int(kv_heads), int(head_dim), int(page_tokens), int(pages))
+        _check(library().dsq_kv_bytes(ctypes.byref(d), ctypes.byref(size)), "dsq_kv_bytes")
+        return size.value
+
+    def _stream(self, stream):
+        import torch
+        return _stream_ptr(torch.cuda.current_stream(self.device) if stream is None else stream)
+
+    def _rows(self, t, name, heads, tokens):
+        if t.device != self.device or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.head_dim:
+            raise ValueError(f"{name} must be [tokens, {heads}, {self.head_dim}] on {self.device}")
+        if t.stride(2) != 1:
+            raise ValueError(f"{name} must be contiguous in its last dimension")
+        if tokens is not None and t.shape[0] != tokens:
+            raise ValueError(f"{name} has {t.shape[0]} rows, not {tokens}")
+        if t.dtype not in self._dtypes:
+            raise ValueError(f"{name} must be float16, bfloat16 or float32")
+
+    def _slots(self, slots):
+        import torch
+        if slots.dtype != torch.int64 or slots.device != self.device or slots.dim() != 1 or not slots.is_contiguous():
+            raise ValueError(f"slots must be a contiguous 1-D int64 tensor on {self.device}")
+
+    def append(self, k, v, slots, stream=None):
+        """Quantise k, v [tokens, kv_heads, head_dim] (float16 or bfloat16, any
+        strides that are multiples of 8) into ``slots`` (int64 [tokens]; a
+        negative slot passes its token over; no slot twice)."""
+        self._slots(slots)
+        n = slots.shape[0]
+        self._rows(k, "k", self.kv_heads, n)
+        self._rows(v, "v", self.kv_heads, n)
+        if k.dtype != v.dtype:
+            raise ValueError("k and v must have the same dtype")
+        rows = KVRows(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+                      self._dtypes[k.dtype])
+        _check(library().dsq_kv_append(self._d, self.data.data_ptr(), ctypes.byref(rows), slots.data_ptr(), n,
+                                       self._stream(stream)), "dsq_kv_append")
+
+    def read(self, slots, dtype=None, k=None, v=None, stream=None):
+        """(k, v): the values at ``slots``, [tokens, kv_heads, head_dim] in
+        ``dtype`` (default float16) or in the given k and v, whose rows of
+        negative slots stay as they are (new ones hold 0 there)."""
+        import torch
+        self._slots(slots)
+        n = slots.shape[0]
+        if k is None or v is None:
+            like = k if k is not None else v
+            dtype = dtype or (like.dtype if like is not None else torch.float16)
+            shape = (n, self.kv_heads, self.head_dim)
+            k = torch.zeros(shape, dtype=dtype, device=self.device) if k is None else k
+            v = torch.zeros(shape, dtype=dtype, device=self.device) if v is None else v
+        self._rows(k, "k", self.kv_heads, n)
+        self._rows(v, "v", self.kv_heads, n)
+        if k.dtype != v.dtype or (dtype is not None and k.dtype != dtype):
+            raise ValueError("k and v must have the same dtype, the one asked for")
+        rows = KVRows(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+                      self._dtypes[k.dtype])
+        _check(library().dsq_kv_read(self._d, self.data.data_ptr(), ctypes.byref(rows), slots.data_ptr(), n,
+                                     self._stream(stream)), "dsq_kv_read")
+        return k, v
+
+    def attend_workspace(self, q_tokens: int, q_heads: int, batch: int):
+        """Scratch for attend() calls of up to these sizes that follow one
+        another; calls that may overlap need one each."""
+        import torch
+        size = ctypes.c_size_t(0)
+        a = KVQueries(q_tokens=int(q_tokens), q_heads=int(q_heads), batch=int(batch))
+        a.q_tokens = a.q_tokens // max(a.batch, 1) * a.batch
+        rc = library().dsq_kv_attend(self._d, None, ctypes.byref(a), None, ctypes.byref(size), None)
+        if rc != DSQ_ERR_BUFFER_TOO_SMALL:
+            _check(rc, "dsq_kv_attend")
+        return torch.empty(max(size.value, 1), dtype=torch.uint8, device=self.device)
+
+    def attend(self, q, page_table, kv_lens, q_start=None, scale=None, causal=True, window=0, out=None, lse=None,
+               return_lse=False, workspace=None, stream=None):
+        """softmax(scale * q K^T) V of queries over the cache (dsq_kv_attend).
+
+        q: [q_tokens, q_heads, head_dim], float16 or bfloat16; page_table:
+        int32 [batch, pages per sequence]; kv_lens: int32 [batch], the tokens
+        of each sequence in the cache, those of its queries among them;
+        q_start: int32 [batch + 1], the first row of each sequence (default:
+        q_tokens / batch rows each); scale: default head_dim ** -0.5; window:
+        see only the last that many tokens.  Returns out (like q), and with
+        ``return_lse`` or ``lse`` also the fp32 log-sum-exp [q_tokens,
+        q_heads].  Rows of no sequence stay as they are in a given out and
+        lse, and hold 0 in new ones."""
+        import torch
+        self._rows(q, "q", q.shape[1] if q.dim() == 3 else 0, None)
+        n, heads = q.shape[0], q.shape[1]
+        if page_table.dim() != 2 or kv_lens.dim() != 1 or kv_lens.shape[0] != page_table.shape[0]:
+            raise ValueError("page_table must be [batch, pages] and kv_lens [batch]")
+        batch = kv_lens.shape[0]
+        for name, t in (("page_table", page_table), ("kv_lens", kv_lens), ("q_start", q_start)):
+            if t is not None and (t.dtype != torch.int32 or t.device != self.device or not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous int32 tensor on {self.device}")
+        if q_start is not None and tuple(q_start.shape) != (batch + 1,):
+            raise ValueError("q_start must be [batch + 1]")
+        if out is None:
+            out = (torch.empty if q_start is None else torch.zeros)(q.shape, dtype=q.dtype, device=self.device)
+        else:
+            self._rows(out, "out", heads, n)
+            if out.dtype != q.dtype:
+                raise ValueError("out must have q's dtype")
+        if lse is None:
+            if return_lse:
+                lse = torch.zeros((n, heads), dtype=torch.float32, device=self.device)
+        elif (lse.dtype != torch.float32 or lse.device != self.device or tuple(lse.shape) != (n, heads)
+              or not lse.is_contiguous()):
+            raise ValueError(f"lse must be a contiguous float32 tensor [{n}, {heads}] on {self.device}")
+        if workspace is None:
+            workspace = self.attend_workspace(n, heads, batch)
+        elif workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
+        a = KVQueries(q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), q.stride(0), q.stride(1),
+                      out.stride(0), out.stride(1), n, self._dtypes[q.dtype], heads, batch, page_table.shape[1],
+                      int(causal), int(window), self.head_dim ** -0.5 if scale is None else scale,
+                      page_table.data_ptr(), kv_lens.data_ptr(), None if q_start is None else q_start.data_ptr())
+        size = ctypes.c_size_t(workspace.numel() * workspace.element_size())
+        _check(library().dsq_kv_attend(self._d, self.data.data_ptr(), ctypes.byref(a), workspace.data_ptr(),
+                                       ctypes.byref(size), self._stream(stream)), "dsq_kv_attend")
+        return out if lse is None else (out, lse)

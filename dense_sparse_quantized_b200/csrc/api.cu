@@ -15,20 +15,6 @@ int check_blob_contents(const void *packed, const BlobHeader &h);  // pack.cu
 
 namespace {
 
-// Makes `device` current for the scope and restores the caller's device.
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = false;
-    explicit DeviceGuard(int device) {
-        if (cudaGetDevice(&prev) != cudaSuccess) return;
-        ok = prev == device || cudaSetDevice(device) == cudaSuccess;
-    }
-    ~DeviceGuard() {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
-
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 }  // namespace

@@ -1,0 +1,86 @@
+// kv.h -- the 4-bit key/value cache: its layout, argument checks and the
+// launchers behind dsq_kv_append, dsq_kv_read and dsq_kv_attend.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "internal.h"
+
+namespace dsq {
+
+constexpr int kKvGroup = 32;  // dimensions that share a scale and a zero
+constexpr int kKvTile = 16;   // tokens of a tile: the k extent of one fp16 matrix instruction
+constexpr float kKvClamp = 57344.0f;
+
+// Byte offsets inside a tile of head dimension D.
+__host__ __device__ constexpr int kv_tile_bytes(int D) { return kKvTile * (D + D / 8); }
+__host__ __device__ constexpr int kv_codes(int D, int which) { return which * kKvTile * D / 2; }
+__host__ __device__ constexpr int kv_words(int D, int which) { return kKvTile * D + which * kKvTile * D / 16; }
+
+struct KvView {
+    const uint8_t *cache;
+    int kv_heads, page_tokens, page_tiles, pages;
+    int slots;  // pages * page_tokens < 2^31
+};
+
+inline int kv_check_desc(const dsq_kv_desc *d) {
+    if (!d || d->kv_heads < 1 || d->page_tokens < 1 || d->page_tokens % kKvTile || d->pages < 0 || d->device < 0)
+        return DSQ_ERR_INVALID_ARG;
+    if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256) return DSQ_ERR_UNSUPPORTED;
+    if ((int64_t)d->pages * d->page_tokens >= ((int64_t)1 << 31)) return DSQ_ERR_UNSUPPORTED;
+    return DSQ_OK;
+}
+
+inline KvView kv_view(const dsq_kv_desc *d, const void *cache) {
+    return {(const uint8_t *)cache, d->kv_heads, d->page_tokens, d->page_tokens / kKvTile, d->pages,
+            d->pages * d->page_tokens};
+}
+
+// Where the tile with token offset `off` of (page, head) starts.
+__device__ __forceinline__ int64_t kv_tile_at(const KvView &c, int D, int page, int head, int off) {
+    return (((int64_t)page * c.kv_heads + head) * c.page_tiles + off / kKvTile) * kv_tile_bytes(D);
+}
+
+// A group's word: scale (fp16, low four bits zero) and zero point.
+__device__ __forceinline__ float kv_scale(uint32_t word) { return __half2float(__ushort_as_half((uint16_t)(word & 0xfff0u))); }
+
+struct KvAttend {
+    KvView c;
+    const void *q;
+    void *out;
+    float *lse;
+    int64_t q_token, q_head, out_token, out_head, q_tokens;
+    int q_heads, share, batch, table_pages, causal, window;
+    float scale_log2;  // scale * log2(e): the softmax runs in powers of two
+    const int32_t *page_table, *kv_lens, *q_start;
+};
+
+// Rows and cached tokens of sequence b, clamped to what the buffers hold.
+struct KvSeq {
+    int64_t row0;
+    int rows, len;
+};
+__device__ __forceinline__ KvSeq kv_seq(const KvAttend &a, int b) {
+    KvSeq s;
+    int64_t r0, r1;
+    if (a.q_start) {
+        r0 = min(max((int64_t)a.q_start[b], (int64_t)0), a.q_tokens);
+        r1 = min(max((int64_t)a.q_start[b + 1], r0), a.q_tokens);
+    } else {
+        const int64_t n = a.q_tokens / a.batch;
+        r0 = b * n;
+        r1 = r0 + n;
+    }
+    s.row0 = r0;
+    s.rows = (int)(r1 - r0);
+    const int64_t most = (int64_t)a.table_pages * a.c.page_tokens;
+    s.len = (int)min(max((int64_t)a.kv_lens[b], (int64_t)0), most);
+    return s;
+}
+
+size_t kv_attend_workspace(const dsq_kv_desc *d, const dsq_kv_queries *a, int sms);
+int launch_kv_attend(const KvAttend &a, int head_dim, int dtype, void *workspace, int sms, cudaStream_t stream);
+
+}  // namespace dsq

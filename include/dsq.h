@@ -362,6 +362,150 @@ DSQ_API int dsq_decompose(const dsq_desc *d, const float *w, void *codes, void *
                           int32_t *row_ptr, int32_t *col_idx, void *values, void *workspace,
                           size_t *workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The 4-bit key/value cache: the other tensor a decode step streams next to a
+ * layer's weights.  Keys and values are held like an affine matrix, as 4-bit
+ * codes with a scale and an integral zero per group, quantised as they are
+ * written.  (The pages describe weights only; the cache is this library's
+ * own.)
+ *
+ * What a group of 32 consecutive dimensions of one token's head stands for:
+ *     value = scale * (q - zero),  q and zero integers in [0, 15],
+ * where, with x clamped to [-57344, 57344], lo = min(0, x) and hi = max(0, x)
+ * over the group and d = (hi - lo) / 15 in fp64,
+ *     scale = the least multiple of 2^max(floor(log2 d) - 6, -20) that is
+ *             >= d and >= 2^-20 (seven significant bits),
+ *     zero  = rint(-lo / scale),
+ *     q     = rint(x / scale) + zero, clipped to [0, 15]
+ * (rint: nearest, ties to even).  Seven bits times four: every value the
+ * cache stands for is exactly an fp16, and |x - value| <= scale / 2 for x
+ * inside the clamp.  A group with a NaN has scale NaN and stands for NaN in
+ * all of its 32 dimensions; infinities are clamped.
+ *
+ * Layout (part of the interface; a cache may be stored and reloaded):
+ *   cache: [pages][kv_heads][page_tokens / 16] tiles; a tile is 16 tokens of
+ *   one kv head, 18 * head_dim bytes:
+ *     K codes [16][head_dim / 2] bytes, the even dimension in the low half;
+ *     V codes, the same;
+ *     K words [head_dim / 32][16] uint16: the fp16 bits of scale, whose low
+ *       four are free, with zero in them;
+ *     V words, the same.
+ * 4.5 bits a value.  The slot of a token is page * page_tokens + offset.
+ * ------------------------------------------------------------------------ */
+
+enum { DSQ_DTYPE_F16 = 0, DSQ_DTYPE_BF16 = 1, DSQ_DTYPE_F32 = 2 };
+
+/* One layer's cache.  kv_heads >= 1; head_dim 64, 128 or 256; page_tokens a
+ * positive multiple of 16; pages >= 0; pages * page_tokens < 2^31.  The
+ * kernels run on CUDA device `device`, whichever is current. */
+typedef struct {
+    int32_t device;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t page_tokens;
+    int32_t pages;
+} dsq_kv_desc;
+
+/* Rows of keys and values outside the cache: element (token t, head h,
+ * dimension i) at k[t * k_token + h * k_head + i].  Strides are in elements;
+ * they and the addresses are multiples of 8 elements and 16 bytes. */
+typedef struct {
+    void *k, *v;
+    int64_t k_token, k_head, v_token, v_head;
+    int32_t dtype;  /* DSQ_DTYPE_* */
+} dsq_kv_rows;
+
+/*
+ * dsq_kv_bytes -- the size of the cache's memory, which the caller allocates
+ * on the device (128-byte aligned) and owns.  Host-only.  Returns DSQ_OK,
+ * DSQ_ERR_INVALID_ARG or DSQ_ERR_UNSUPPORTED (a head_dim other than 64, 128
+ * or 256, or 2^31 tokens or more).
+ */
+DSQ_API int dsq_kv_bytes(const dsq_kv_desc *d, size_t *bytes);
+
+/*
+ * dsq_kv_append -- quantise rows of keys and values as they are written.
+ *   cache   device; the cache's memory.
+ *   rows    host; what to write, F16 or BF16, read only.  Strides may be any
+ *           multiple of 8, zero and negative ones among them.
+ *   slots   device int64 [tokens]: the slot of each token.  A token with a
+ *           slot outside [0, pages * page_tokens) is not written (padding
+ *           takes -1).  No slot twice in one call: what such a slot holds
+ *           afterwards is undefined (other slots are as they should be).
+ *   tokens  >= 0.
+ *   stream  cudaStream_t of the device, as void*.
+ * All other bytes of the cache stay as they are.  Asynchronous; one launch,
+ * no workspace.  Returns DSQ_OK, DSQ_ERR_INVALID_ARG (NULL or misaligned
+ * pointer, a stride that is no multiple of 8), DSQ_ERR_UNSUPPORTED or
+ * DSQ_ERR_CUDA.
+ */
+DSQ_API int dsq_kv_append(const dsq_kv_desc *d, void *cache, const dsq_kv_rows *rows, const int64_t *slots,
+                          int64_t tokens, void *stream);
+
+/*
+ * dsq_kv_read -- the values the cache stands for, at the given slots: exact
+ * in F16 and F32, rounded once to nearest in BF16.
+ *   rows    host; where to write; k or v may be NULL (not wanted).  Elements
+ *           must not overlap one another.
+ *   slots   as above; the same slot may come twice, and the rows of a slot
+ *           outside the cache are left as they are.
+ * The rest as for dsq_kv_append.
+ */
+DSQ_API int dsq_kv_read(const dsq_kv_desc *d, const void *cache, const dsq_kv_rows *rows, const int64_t *slots,
+                        int64_t tokens, void *stream);
+
+/* Queries over the cache.  Sequence b holds kv_lens[b] tokens, token j at
+ * offset j % page_tokens of page page_table[b][j / page_tokens]; its queries
+ * are rows q_start[b] .. q_start[b + 1] - 1 of q (q_start NULL: q_tokens /
+ * batch rows each) and belong to its last tokens, the n-th of n queries to
+ * token kv_lens[b] - 1.  Query head h reads kv head h / (q_heads / kv_heads). */
+typedef struct {
+    const void *q;  /* device; (row t, head h, dimension i) at q[t * q_token + h * q_head + i] */
+    void *out;      /* device; likewise, same dtype; elements must not overlap one another or q */
+    float *lse;     /* device fp32 [q_tokens][q_heads], or NULL: log sum_j exp(score_j) */
+    int64_t q_token, q_head, out_token, out_head;  /* strides as in dsq_kv_rows */
+    int64_t q_tokens;   /* rows of q, out and lse */
+    int32_t dtype;      /* DSQ_DTYPE_F16 or DSQ_DTYPE_BF16 */
+    int32_t q_heads;    /* a multiple of kv_heads */
+    int32_t batch;
+    int32_t table_pages; /* columns of page_table */
+    int32_t causal;     /* 1: a query at position p sees tokens 0 .. p; 0: all tokens of its sequence */
+    int32_t window;     /* > 0 (with causal): only the last `window` of those; 0: no limit */
+    float scale;        /* score_j = scale * <q, k_j>; finite */
+    const int32_t *page_table; /* device [batch][table_pages] */
+    const int32_t *kv_lens;    /* device [batch] */
+    const int32_t *q_start;    /* device [batch + 1], nondecreasing from 0; or NULL */
+} dsq_kv_queries;
+
+/*
+ * dsq_kv_attend -- out = softmax(scale * q K^T) V over the cached tokens that
+ * each query sees; for one token per sequence, a few, or whole prompts.
+ *   cache      device; read only.
+ *   a          host; the queries, above.
+ *   workspace  device scratch, 256-byte aligned, *workspace_bytes long, the
+ *              caller's; with workspace NULL (or too small) the call only
+ *              writes the size it needs and returns
+ *              DSQ_ERR_BUFFER_TOO_SMALL.  Its contents need no
+ *              initialisation and mean nothing between calls; calls that may
+ *              overlap on the GPU (two streams, two graphs) need one each.
+ *   stream     cudaStream_t of the device, as void*.
+ * A query that sees no token (an empty sequence, a position before the
+ * first token) has out = 0 and lse = -inf.  Rows at and behind
+ * q_start[batch] are left as they are.  What lies in the cache behind a
+ * sequence's tokens, or before or behind what a query sees, never enters its
+ * result, NaN included.  A NaN that a query sees makes its lse NaN when it is a
+ * key's, and NaN of elements of its out.  Lengths are clamped to [0,
+ * table_pages * page_tokens], row numbers to [0, q_tokens]; tokens on a page
+ * outside [0, pages) are not seen.
+ * Scores, maxima, sums and outputs are accumulated in fp32; the softmax's
+ * numerators are rounded to fp16 before they multiply V.
+ * Asynchronous; allocates nothing; the same inputs give the same bits.
+ * Returns DSQ_OK, DSQ_ERR_INVALID_ARG, DSQ_ERR_UNSUPPORTED,
+ * DSQ_ERR_BUFFER_TOO_SMALL or DSQ_ERR_CUDA.
+ */
+DSQ_API int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_kv_queries *a, void *workspace,
+                          size_t *workspace_bytes, void *stream);
+
 /* Static, never-NULL text for a status code. */
 DSQ_API const char *dsq_status_string(int status);
 

@@ -1,0 +1,613 @@
+"""The 4-bit key/value cache: what dsq_kv_append writes (byte for byte), what
+dsq_kv_read gives back (bit for bit) and dsq_kv_attend against attention in 64
+bits over the same cache.  Refusals run without a GPU.
+
+Tolerance of attend, element by element, from what its header declares.  With
+S = scale * sum_i |q_i k_ti| (largest over the tokens), P = sum_t p_t |v_t|:
+  scores: fp32 sums of D products, each step off by at most an ulp (2^-23):
+    |error| <= (D + 8) 2^-23 S, which moves each p_t, and their sum, by that
+    part of themselves, as 2^-20 covers exp2, its argument's last bits and the
+    other fp32 steps: 2 ((D + 8) 2^-23 S + 2^-20) P;
+  numerators in fp16: 2^-11 of p_t, or 2^-25 of the running maximum's
+    numerator where that is more (subnormal): 2^-11 P + T 2^-25 max |v|;
+  the output's rounding: 2^-11 |out| (fp16), 2^-8 |out| (bf16), or 2^-25.
+The log-sum-exp: (D + 8) 2^-23 S + 2^-20 + 2^-22 |lse|.
+"""
+import ctypes
+
+import numpy as np
+import pytest
+
+import dense_sparse_quantized_b200 as dsq
+from oracle import kv as okv
+
+torch = pytest.importorskip("torch")
+
+EPS = {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+
+
+# ------------------------------------------------- the definition, on the CPU
+
+def test_held_values_are_fp16_and_within_half_a_step():
+    rng = np.random.default_rng(1)
+    for spread in (1e-7, 1e-4, 0.02, 1.0, 300.0, 2e4):
+        x = (rng.standard_normal((400, 64)) * spread).astype(np.float16).astype(np.float64)
+        x[:40] = np.abs(x[:40])
+        codes, scale, zero = okv.encode(x)
+        v = okv.values(codes, scale, zero)
+        assert np.array_equal(v, v.astype(np.float16).astype(np.float64))
+        err = np.abs(v - np.clip(x, -okv.CLAMP, okv.CLAMP)).reshape(400, 2, 32)
+        assert np.all(err <= scale[..., None] / 2)
+        assert np.array_equal(scale.astype(np.float16).view(np.uint16) & 15, np.zeros((400, 2), np.uint16))
+
+
+def test_held_values_worked_by_hand():
+    x = np.zeros((1, 32))
+    codes, scale, zero = okv.encode(x)
+    assert scale[0, 0] == 2.0 ** -20 and zero[0, 0] == 0 and not codes.any()
+    x[0, 3], x[0, 4], x[0, 5] = 15.0, 7.5, 6.5        # step 1: ties go to the even code
+    codes, scale, zero = okv.encode(x)
+    assert scale[0, 0] == 1.0 and zero[0, 0] == 0 and list(codes[0, 3:6]) == [15, 8, 6]
+    x[0, 0] = -1.0                                     # 16 / 15 up to a multiple of 1/64: 69/64
+    codes, scale, zero = okv.encode(x)
+    assert scale[0, 0] == 69 / 64 and zero[0, 0] == 1 and codes[0, 3] == 15 and codes[0, 0] == 0
+    x[0, 9] = np.nan
+    assert np.isnan(okv.held(x)).all()
+    assert okv.held(np.full((1, 32), np.inf)).max() <= 61184
+    top = okv.held(np.concatenate([np.full((1, 16), 7e4), np.full((1, 16), -7e4)], 1))
+    assert np.isfinite(top.astype(np.float16)).all()
+
+
+def test_store_and_load_agree():
+    rng = np.random.default_rng(2)
+    cache = rng.integers(0, 256, 3 * 2 * 2 * okv.tile_bytes(64), dtype=np.uint8)
+    k, v = rng.standard_normal((2, 5, 2, 64)).astype(np.float16)
+    slots = np.array([95, 0, 33, -1, 17])
+    okv.store(cache, 2, 64, 32, k, v, slots)
+    got = okv.load(cache, 2, 64, 32, slots[slots >= 0])
+    assert np.array_equal(got[0], okv.held(k)[slots >= 0]) and np.array_equal(got[1], okv.held(v)[slots >= 0])
+
+
+# ------------------------------------------------------------------ refusals
+
+def _status(fn, *args):
+    return getattr(dsq.library(), fn)(*args)
+
+
+BAD = dsq.DSQ_ERR_INVALID_ARG
+UNS = dsq.DSQ_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("desc,rc", [
+    ((0, 0, 128, 64, 4), BAD), ((0, 8, 128, 0, 4), BAD), ((0, 8, 128, 24, 4), BAD), ((0, 8, 128, 64, -1), BAD),
+    ((-1, 8, 128, 64, 4), BAD), ((0, 8, 96, 64, 4), UNS), ((0, 8, 0, 64, 4), UNS), ((0, 1, 64, 1 << 16, 1 << 15), UNS),
+    ((0, 8, 128, 64, 4), dsq.DSQ_OK), ((0, 1, 64, 16, 0), dsq.DSQ_OK)])
+def test_bytes_refusals(desc, rc):
+    size = ctypes.c_size_t(0)
+    d = dsq.KVDesc(*desc)
+    assert _status("dsq_kv_bytes", ctypes.byref(d), ctypes.byref(size)) == rc
+    assert _status("dsq_kv_bytes", None, ctypes.byref(size)) == BAD
+    assert _status("dsq_kv_bytes", ctypes.byref(d), None) == BAD
+    if rc == dsq.DSQ_OK:
+        assert size.value == desc[4] * desc[1] * desc[3] // 16 * okv.tile_bytes(desc[2])
+    else:  # every call refuses the shape before it looks at anything else
+        assert _status("dsq_kv_append", ctypes.byref(d), None, None, None, 0, None) == rc
+        assert _status("dsq_kv_read", ctypes.byref(d), None, None, None, 0, None) == rc
+        assert _status("dsq_kv_attend", ctypes.byref(d), None, None, None, None, None) == rc
+
+
+GOOD_ROWS = dict(k=4096, v=8192, k_token=1024, k_head=128, v_token=1024, v_head=128, dtype=0)
+
+
+@pytest.mark.parametrize("change", [
+    dict(k=None), dict(v=None), dict(k=4104), dict(v=8194), dict(k_token=1028), dict(k_head=4), dict(v_token=1023),
+    dict(v_head=-4), dict(dtype=3), dict(dtype=-1)])
+def test_append_refusals(change):
+    d = dsq.KVDesc(0, 8, 128, 64, 4)
+    r = dsq.KVRows(**{**GOOD_ROWS, **change})
+    assert _status("dsq_kv_append", ctypes.byref(d), 1 << 20, ctypes.byref(r), 1 << 16, 3, None) == BAD
+
+
+def test_append_refuses_the_rest():
+    d, r = dsq.KVDesc(0, 8, 128, 64, 4), dsq.KVRows(**GOOD_ROWS)
+    call = lambda cache, rows, slots, n: _status("dsq_kv_append", ctypes.byref(d), cache, rows, slots, n, None)  # noqa: E731
+    assert call(None, ctypes.byref(r), 1 << 16, 3) == BAD
+    assert call((1 << 20) + 16, ctypes.byref(r), 1 << 16, 3) == BAD
+    assert call(1 << 20, None, 1 << 16, 3) == BAD
+    assert call(1 << 20, ctypes.byref(r), None, 3) == BAD
+    assert call(1 << 20, ctypes.byref(r), (1 << 16) + 4, 3) == BAD
+    assert call(1 << 20, ctypes.byref(r), 1 << 16, -1) == BAD
+    assert call(None, None, None, 0) == dsq.DSQ_OK
+    r.dtype = dsq.DTYPE_F32
+    assert call(1 << 20, ctypes.byref(r), 1 << 16, 3) == UNS
+    wide = dsq.KVDesc(0, 70000, 64, 16, 1)
+    r.dtype = 0
+    assert _status("dsq_kv_append", ctypes.byref(wide), 1 << 20, ctypes.byref(r), 1 << 16, 3, None) == UNS
+
+
+@pytest.mark.parametrize("change", [
+    dict(k=None, v=None), dict(k=4104), dict(k_token=1028), dict(dtype=3), dict(k_token=0), dict(v_head=64),
+    dict(k_token=1016), dict(k_token=-1024), dict(k_token=128, k_head=256)])
+def test_read_refusals(change):
+    """Misaligned rows, and rows that overlap: three tokens of eight heads."""
+    d = dsq.KVDesc(0, 8, 128, 64, 4)
+    r = dsq.KVRows(**{**GOOD_ROWS, **change})
+    assert _status("dsq_kv_read", ctypes.byref(d), 1 << 20, ctypes.byref(r), 1 << 16, 3, None) == BAD
+
+
+GOOD_Q = dict(q=4096, out=1 << 21, lse=1 << 22, q_token=2048, q_head=128, out_token=2048, out_head=128, q_tokens=6, dtype=0,
+              q_heads=16, batch=3, table_pages=2, causal=1, window=0, scale=0.1, page_table=1 << 16, kv_lens=1 << 17,
+              q_start=None)
+
+
+@pytest.mark.parametrize("change,rc", [
+    (dict(q=None), BAD), (dict(out=None), BAD), (dict(page_table=None), BAD), (dict(kv_lens=None), BAD),
+    (dict(q=4104), BAD), (dict(out=4100), BAD), (dict(lse=2), BAD), (dict(q_start=1026), BAD),
+    (dict(page_table=(1 << 16) + 2), BAD), (dict(kv_lens=(1 << 17) + 1), BAD),
+    (dict(q_token=2044), BAD), (dict(q_head=1), BAD), (dict(out_token=2052), BAD), (dict(out_head=64), BAD),
+    (dict(out_token=0), BAD), (dict(out_token=128), BAD), (dict(q_heads=0), BAD), (dict(q_heads=12), BAD), (dict(batch=-1), BAD),
+    (dict(q_tokens=-6), BAD), (dict(q_tokens=7), BAD), (dict(table_pages=-1), BAD), (dict(window=-1), BAD),
+    (dict(window=4, causal=0), BAD), (dict(scale=float("nan")), BAD), (dict(scale=float("inf")), BAD),
+    (dict(dtype=4), BAD), (dict(dtype=2), UNS), (dict(table_pages=1 << 26), UNS), (dict(q_tokens=3 << 28), UNS)])
+def test_attend_refusals(change, rc):
+    d = dsq.KVDesc(0, 8, 128, 64, 4)
+    size = ctypes.c_size_t(1 << 40)
+    a = dsq.KVQueries(**{**GOOD_Q, **change})
+    assert _status("dsq_kv_attend", ctypes.byref(d), 1 << 20, ctypes.byref(a), 1 << 24, ctypes.byref(size), None) == rc
+
+
+def test_attend_workspace_protocol_and_empty_calls():
+    d, a = dsq.KVDesc(0, 8, 128, 64, 4), dsq.KVQueries(**GOOD_Q)
+    size = ctypes.c_size_t(0)
+    call = lambda cache, ws: _status("dsq_kv_attend", ctypes.byref(d), cache, ctypes.byref(a), ws, ctypes.byref(size), None)  # noqa: E731
+    assert call(1 << 20, None) == dsq.DSQ_ERR_BUFFER_TOO_SMALL and size.value > 0
+    need, size.value = size.value, size.value - 1
+    assert call(1 << 20, 1 << 24) == dsq.DSQ_ERR_BUFFER_TOO_SMALL and size.value == need
+    assert call(1 << 20, (1 << 24) + 128) == BAD     # misaligned workspace
+    assert call((1 << 20) + 64, 1 << 24) == BAD      # misaligned cache
+    assert call(None, 1 << 24) == BAD
+    assert _status("dsq_kv_attend", ctypes.byref(d), 1 << 20, ctypes.byref(a), 1 << 24, None, None) == BAD
+    assert _status("dsq_kv_attend", ctypes.byref(d), 1 << 20, None, 1 << 24, ctypes.byref(size), None) == BAD
+    a.batch = a.q_tokens = 0
+    assert call(None, 1 << 24) == dsq.DSQ_OK
+
+
+# --------------------------------------------------------------------- on a GPU
+
+def _rows(rng, n, h, d):
+    x = rng.standard_normal((n, h, d)) * np.exp(0.6 * rng.standard_normal((h, d)))
+    return torch.from_numpy(x)
+
+
+def _awkward(x):
+    """Groups a quantiser can go wrong in, in the first tokens of x [n, h, d]."""
+    n = x.shape[0]
+    for i, f in enumerate((lambda g: g * 0, lambda g: g.abs(), lambda g: -g.abs(), lambda g: g * 1e-7, lambda g: g * 3e-5,
+                           lambda g: g.clamp(-1, 1) * 65504, lambda g: g * 0 + 1, lambda g: (g * 4).round() / 2,
+                           lambda g: torch.where(g == g.max(), float("inf"), g),
+                           lambda g: torch.where(g == g.min(), -float("inf"), g),
+                           lambda g: torch.where(g == g.max(), float("nan"), g), lambda g: g * 0 - 1e-6)):
+        if i < n:
+            x[i] = f(x[i])
+    return x
+
+
+def _held(t):
+    return okv.held(t.double().cpu().numpy())
+
+
+CASES = [(1, 1, 64, 16), (3, 2, 64, 32), (33, 8, 128, 16), (40, 3, 128, 48), (29, 1, 256, 128), (513, 2, 128, 64), (700, 12, 64, 16)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("n,h,d,page", CASES)
+def test_append_bytes_and_read_values(n, h, d, page, dtype):
+    rng = np.random.default_rng(n + d)
+    pages = -(-n // page) + 2
+    before = torch.from_numpy(rng.integers(0, 256, dsq.KVCache.bytes_for(h, d, pages, page), dtype=np.uint8))
+    kv = dsq.KVCache(h, d, pages, page, data=before.cuda())
+    k, v = (_awkward(_rows(rng, n, h, d)).to(dtype) for _ in range(2))
+    slots = rng.permutation(pages * page)[:n]
+    if n > 20:
+        slots[5], slots[17], slots[19] = -1, pages * page, -(1 << 40)
+    s = torch.from_numpy(slots).cuda()
+    kv.append(k.cuda(), v.cuda(), s)
+    want = before.numpy().copy()
+    okv.store(want, h, d, page, k.double().numpy(), v.double().numpy(), slots)
+    assert np.array_equal(kv.data.cpu().numpy(), want)
+
+    inside = (slots >= 0) & (slots < pages * page)
+    exact = okv.load(want, h, d, page, slots[inside])
+    for out in (F16, BF16, F32):
+        got = kv.read(s, k=torch.full((n, h, d), 7.0, dtype=out, device="cuda"),
+                      v=torch.full((n, h, d), 7.0, dtype=out, device="cuda"))
+        for g, e in zip(got, exact):
+            g = g.cpu()
+            assert torch.equal(torch.nan_to_num(g[torch.from_numpy(inside)], 3e4),
+                               torch.nan_to_num(torch.from_numpy(e).to(out), 3e4))
+            assert (g[torch.from_numpy(~inside)] == 7.0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["fused", "heads_first", "broadcast", "reversed_tokens"])
+def test_append_strides(layout):
+    rng = np.random.default_rng(4)
+    n, h, d = 21, 4, 128
+    if layout == "fused":
+        x = _rows(rng, n, 3 * h, d).half().cuda()
+        k, v = x[:, h:2 * h], x[:, 2 * h:]
+    elif layout == "heads_first":
+        k, v = (_rows(rng, h, n, d).half().cuda().transpose(0, 1) for _ in range(2))
+    elif layout == "broadcast":
+        k, v = _rows(rng, n, 1, d).half().cuda().expand(n, h, d), _rows(rng, 1, h, d).half().cuda().expand(n, h, d)
+    else:  # negative strides reach the C call only
+        k, v = (_rows(rng, n, h, d).half().cuda() for _ in range(2))
+    kv = dsq.KVCache(h, d, 2, 16)
+    slots = torch.from_numpy(rng.permutation(32)[:n]).cuda()
+    if layout == "reversed_tokens":
+        last = (n - 1) * h * d * 2
+        r = dsq.KVRows(k.data_ptr() + last, v.data_ptr() + last, -h * d, d, -h * d, d, 0)
+        rc = dsq.library().dsq_kv_append(ctypes.byref(kv.desc), kv.data.data_ptr(), ctypes.byref(r), slots.data_ptr(), n,
+                                         torch.cuda.current_stream().cuda_stream)
+        assert rc == dsq.DSQ_OK
+        k, v = k.flip(0), v.flip(0)
+    else:
+        kv.append(k, v, slots)
+    into = torch.zeros(h, n, 2, d, dtype=F32, device="cuda")       # read back into strided views of one tensor
+    got = kv.read(slots, k=into[:, :, 0].transpose(0, 1), v=into[:, :, 1].transpose(0, 1))
+    assert np.array_equal(got[0].cpu().double().numpy(), _held(k)) and np.array_equal(got[1].cpu().double().numpy(), _held(v))
+
+
+@pytest.mark.gpu
+def test_read_of_keys_alone_and_of_repeated_slots():
+    rng = np.random.default_rng(5)
+    kv = dsq.KVCache(2, 64, 2, 16)
+    k, v = _rows(rng, 9, 2, 64).half().cuda(), _rows(rng, 9, 2, 64).half().cuda()
+    kv.append(k, v, torch.arange(9, device="cuda"))
+    slots = torch.tensor([8, 3, 3, 0, 8], device="cuda")
+    out = torch.zeros(5, 2, 64, dtype=F16, device="cuda")
+    for which, x in (("k", k), ("v", v)):
+        r = dsq.KVRows(dtype=0, k_token=128, k_head=64, v_token=128, v_head=64)
+        setattr(r, which, out.data_ptr())
+        assert dsq.library().dsq_kv_read(ctypes.byref(kv.desc), kv.data.data_ptr(), ctypes.byref(r), slots.data_ptr(), 5,
+                                         torch.cuda.current_stream().cuda_stream) == dsq.DSQ_OK
+        assert np.array_equal(out.cpu().double().numpy(), _held(x[slots]))
+
+
+def _problem(seed, lens, new, h, share, d, page, dtype, fill=0xFF, extra=2):
+    """A cache with the sequences' tokens on shuffled pages; all other bytes are
+    `fill` (0xFF: NaN scales)."""
+    rng = np.random.default_rng(seed)
+    need = [-(-n // page) for n in lens]
+    pages, cols = sum(need) + extra, max(need + [1])
+    data = torch.full((dsq.KVCache.bytes_for(h, d, pages, page),), fill, dtype=torch.uint8, device="cuda")
+    kv = dsq.KVCache(h, d, pages, page, data=data)
+    order = rng.permutation(pages)
+    table = np.full((len(lens), cols), -1, np.int32)
+    seqs, at = [], 0
+    for b, n in enumerate(lens):
+        table[b, :need[b]] = order[at:at + need[b]]
+        at += need[b]
+        k, v = _rows(rng, n, h, d).to(dtype), _rows(rng, n, h, d).to(dtype)
+        t = np.arange(n)
+        if n:
+            kv.append(k.cuda(), v.cuda(), torch.from_numpy(table[b, t // page].astype(np.int64) * page + t % page).cuda())
+        seqs.append((_held(k), _held(v)))
+    rows = sum(new)
+    q = torch.from_numpy(rng.standard_normal((rows, h * share, d))).to(dtype)
+    start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    return kv, seqs, q, torch.from_numpy(table).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), start
+
+
+def _check(out, lse, q, seqs, lens, start, dtype, causal=True, window=0, scale=None):
+    d = q.shape[-1]
+    scale = d ** -0.5 if scale is None else scale
+    for b, (k, v) in enumerate(seqs):
+        r0, r1 = int(start[b]), int(start[b + 1])
+        if r1 == r0:
+            continue
+        x = q[r0:r1].double().numpy()
+        pos = lens[b] - (r1 - r0) + np.arange(r1 - r0) if causal else None
+        want, want_lse, P = okv.attend(x, k, v, scale, pos, window)
+        share = x.shape[1] // k.shape[1]
+        S = np.zeros(x.shape[:2])
+        if lens[b]:
+            for h in range(x.shape[1]):
+                S[:, h] = abs(scale) * (np.abs(x[:, h]) @ np.abs(k[:, h // share]).T).max(-1)
+        ds = (d + 8) * 2.0 ** -23 * S
+        tol = (2 * (ds + 2.0 ** -20) + 2.0 ** -11)[..., None] * P + (lens[b] * 2.0 ** -25 * np.abs(v).max(initial=0)
+                                                                    + EPS[dtype] * np.abs(want) + 2.0 ** -25)
+        err = np.abs(out[r0:r1].double().cpu().numpy() - want)
+        assert np.all(err <= tol), (b, float((err / tol).max()))
+        if lse is not None:
+            got = lse[r0:r1].double().cpu().numpy()
+            empty = np.isneginf(want_lse)
+            assert np.array_equal(np.isneginf(got), empty), b
+            off = np.abs(got[~empty] - want_lse[~empty])
+            assert np.all(off <= ds[~empty] + 2.0 ** -20 + 2.0 ** -22 * np.abs(want_lse[~empty])), (b, off.max())
+            assert not out[r0:r1].cpu()[torch.from_numpy(empty)].any()
+
+
+SHAPES = [  # lens, new rows, kv heads, share, dim, page
+    ([1], [1], 1, 1, 64, 16),
+    ([1, 17, 0, 255], [1, 1, 1, 1], 2, 1, 128, 16),
+    ([333], [1], 32, 1, 128, 64),
+    ([100, 1500, 31, 16], [1, 1, 1, 1], 2, 4, 128, 64),
+    ([777, 64], [1, 1], 1, 16, 256, 128),
+    ([2100], [1], 1, 71, 64, 32),
+    ([50, 513, 8], [4, 5, 8], 2, 8, 128, 16),
+    ([5, 40], [3, 2], 3, 7, 64, 48),
+    ([300], [300], 2, 4, 128, 64),
+    ([130, 3, 260, 0], [130, 2, 77, 0], 2, 2, 64, 16),
+    ([1000], [129], 1, 1, 256, 32),
+    ([4, 10, 129], [9, 10, 129], 1, 3, 128, 16),   # more queries than tokens: the first see nothing
+    ([700], [260], 1, 8, 256, 64),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("case", range(len(SHAPES)))
+def test_attend_causal(case, dtype):
+    lens, new, h, share, d, page = SHAPES[case]
+    kv, seqs, q, table, kv_lens, start = _problem(case, lens, new, h, share, d, page, dtype)
+    out, lse = kv.attend(q.cuda(), table, kv_lens, q_start=torch.from_numpy(start).cuda(), return_lse=True)
+    _check(out, lse, q, seqs, lens, start, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [1, 3, 6, 9, 11])
+def test_attend_all_tokens(case):
+    lens, new, h, share, d, page = SHAPES[case]
+    kv, seqs, q, table, kv_lens, start = _problem(case + 50, lens, new, h, share, d, page, F16)
+    out, lse = kv.attend(q.cuda(), table, kv_lens, q_start=torch.from_numpy(start).cuda(), causal=False, return_lse=True,
+                         scale=0.2)
+    _check(out, lse, q, seqs, lens, start, F16, causal=False, scale=0.2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window", [1, 16, 100, 1000])
+@pytest.mark.parametrize("case", [1, 3, 6, 9, 10, 11])
+def test_attend_window(case, window):
+    lens, new, h, share, d, page = SHAPES[case]
+    kv, seqs, q, table, kv_lens, start = _problem(case + 100, lens, new, h, share, d, page, BF16)
+    out, lse = kv.attend(q.cuda(), table, kv_lens, q_start=torch.from_numpy(start).cuda(), window=window, return_lse=True)
+    _check(out, lse, q, seqs, lens, start, BF16, window=window)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [1, 6, 200])
+def test_attend_uniform_rows_and_strides(new):
+    """q_start left out; q a slice of a fused projection, out heads first."""
+    lens, h, share, d = [new + 150, new, new + 4], 2, 4, 128
+    kv, seqs, q, table, kv_lens, start = _problem(200 + new, lens, [new] * 3, h, share, d, 32, F16)
+    fused = torch.zeros(3 * new, 12, d, dtype=F16, device="cuda")
+    fused[:, 2:10] = q.cuda()
+    out = torch.zeros(8, 3 * new, d, dtype=F16, device="cuda").transpose(0, 1)
+    got = kv.attend(fused[:, 2:10], table, kv_lens, out=out)
+    assert got is out
+    _check(out, None, q, seqs, lens, start, F16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [3, 6, 8])
+def test_attend_large_and_small_scores(case):
+    """Queries that pick out one token, and ones that see all tokens alike."""
+    lens, new, h, share, d, page = SHAPES[case]
+    kv, seqs, q, table, kv_lens, start = _problem(case + 300, lens, new, h, share, d, page, F16)
+    q[::2] *= 40
+    q[1::2] *= 1e-4
+    out, lse = kv.attend(q.cuda(), table, kv_lens, q_start=torch.from_numpy(start).cuda(), return_lse=True)
+    _check(out, lse, q, seqs, lens, start, F16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("factor", [1e-12, 1e-6, 1e10])
+def test_attend_bf16_queries_outside_fp16(factor):
+    """bf16 rows whose values fp16 could not hold, the scale making up for it."""
+    for case in (3, 8):
+        lens, new, h, share, d, page = SHAPES[case]
+        kv, seqs, q, table, kv_lens, start = _problem(case + 350, lens, new, h, share, d, page, BF16)
+        q = (q.double() * factor).to(BF16)
+        scale = float(d ** -0.5 / factor)
+        out, lse = kv.attend(q.cuda(), table, kv_lens, q_start=torch.from_numpy(start).cuda(), return_lse=True, scale=scale)
+        _check(out, lse, q, seqs, lens, start, BF16, scale=scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [1, 4, 90])
+def test_attend_rows_behind_the_last_sequence_and_bad_pages(new):
+    lens = [new + 30, new + 200]
+    kv, seqs, q, table, kv_lens, start = _problem(400 + new, lens, [new, new], 2, 4, 64, 16, F16)
+    more = torch.zeros(2 * new + 5, 8, 64, dtype=F16)
+    more[:2 * new] = q
+    out = torch.full_like(more, 3.0).cuda()
+    lse = torch.full(more.shape[:2], 5.0, device="cuda")
+    kv.attend(more.cuda(), table, kv_lens, q_start=torch.from_numpy(start).cuda(), out=out, lse=lse)
+    _check(out, lse, q, seqs, lens, start, F16)
+    assert (out[2 * new:] == 3.0).all() and (lse[2 * new:] == 5.0).all()
+    # a page outside the cache is not seen: as if its tokens were not there
+    table[1, 2] = kv.pages
+    table[1, 4] = -7
+    t = np.arange(lens[1])
+    keep = (t // 16 != 2) & (t // 16 != 4)
+    out = kv.attend(q.cuda(), table, kv_lens, causal=False)
+    seqs[1] = tuple(x[keep] for x in seqs[1])
+    lens[1] = int(keep.sum())
+    _check(out, None, q, seqs, lens, start, F16, causal=False)
+    # lengths past the table and below zero are clamped
+    out, lse = kv.attend(q.cuda(), table[:, :1].contiguous(), torch.tensor([1 << 30, -4], dtype=torch.int32, device="cuda"),
+                         causal=False, return_lse=True)
+    _check(out, lse, q, [tuple(x[:16] for x in seqs[0]), tuple(x[:0] for x in seqs[1])], [16, 0], start, F16, causal=False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [1, 3, 150])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attend_nan_stays_where_it_is_seen(new, d):
+    """A NaN token reaches the queries at and behind it, no other."""
+    n = 150
+    kv, seqs, q, table, kv_lens, start = _problem(500 + new, [n], [new], 1, 2, d, 64, F16)
+    clean = kv.attend(q.cuda(), table, kv_lens)
+    at = n - new + new // 2
+    for which in (0, 1):
+        kv2 = dsq.KVCache(1, d, kv.pages, 64, data=kv.data.clone())
+        slot = int(table[0, at // 64]) * 64 + at % 64
+        k, v = (torch.from_numpy(x[at:at + 1]).half().cuda() for x in seqs[0])
+        (k, v)[which][0, 0, 40] = float("nan")
+        kv2.append(k, v, torch.tensor([slot], device="cuda"))
+        out, lse = kv2.attend(q.cuda(), table, kv_lens, return_lse=True)
+        assert torch.equal(out[:new // 2], clean[:new // 2])
+        hit = out[new // 2:]
+        assert torch.isnan(hit).any(-1).all()
+        if which == 0:
+            assert torch.isnan(hit).all() and torch.isnan(lse[new // 2:]).all()
+        else:
+            assert torch.isnan(hit[..., 32:64]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [3, 6, 8])
+def test_attend_workspace_contents_do_not_matter_and_bits_repeat(case):
+    lens, new, h, share, d, page = SHAPES[case]
+    kv, seqs, q, table, kv_lens, start = _problem(case + 600, lens, new, h, share, d, page, F16)
+    q, start = q.cuda(), torch.from_numpy(start).cuda()
+    work = kv.attend_workspace(q.shape[0], q.shape[1], len(lens))
+    first = None
+    for fill in (0, 0xFF, 0x7C):
+        work.fill_(fill)
+        out, lse = kv.attend(q, table, kv_lens, q_start=start, return_lse=True, workspace=work)
+        first = first or (out.clone(), lse.clone())
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for s in streams:
+        for _ in range(4):
+            outs.append(kv.attend(q, table, kv_lens, q_start=start, stream=s, out=torch.zeros_like(q),
+                                  workspace=kv.attend_workspace(q.shape[0], q.shape[1], len(lens))))
+    torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+def test_far_pages_of_a_large_cache():
+    """Byte offsets past 32 bits: a 4.9 GB cache whose first and last pages are used."""
+    h, d, page = 8, 128, 64
+    pages = 66000
+    kv = dsq.KVCache(h, d, pages, page, data=torch.empty(dsq.KVCache.bytes_for(h, d, pages, page), dtype=torch.uint8, device="cuda"))
+    assert kv.data.numel() > 1 << 32
+    rng = np.random.default_rng(9)
+    k, v = _rows(rng, 100, h, d).half(), _rows(rng, 100, h, d).half()
+    slots = torch.cat([torch.arange(64) + (pages - 1) * page, torch.arange(36)]).cuda()
+    kv.append(k.cuda(), v.cuda(), slots)
+    got = kv.read(slots, dtype=F32)
+    assert np.array_equal(got[0].cpu().double().numpy(), _held(k)) and np.array_equal(got[1].cpu().double().numpy(), _held(v))
+    table = torch.tensor([[pages - 1, 0]], dtype=torch.int32, device="cuda")
+    for new in (1, 60):
+        q = torch.from_numpy(rng.standard_normal((new, 16, d))).half()
+        out, lse = kv.attend(q.cuda(), table, torch.tensor([100], dtype=torch.int32, device="cuda"), return_lse=True)
+        _check(out, lse, q, [(_held(k), _held(v))], [100], [0, new], F16)
+
+
+@pytest.mark.gpu
+def test_captured_calls_follow_their_buffers():
+    """append and attend captured once and replayed over changing rows, slots,
+    lengths and pages; two graphs with a workspace each, replayed in turn."""
+    rng = np.random.default_rng(11)
+    h, share, d, page, batch = 2, 4, 128, 16, 3
+    kv = dsq.KVCache(h, d, 40, page)
+    table = torch.from_numpy(rng.permutation(40)[:36].reshape(batch, 12).astype(np.int32)).cuda()
+    lens = torch.zeros(batch, dtype=torch.int32, device="cuda")
+    k, v = (torch.zeros(batch, h, d, dtype=F16, device="cuda") for _ in range(2))
+    q = torch.zeros(batch, h * share, d, dtype=F16, device="cuda")
+    slots = torch.zeros(batch, dtype=torch.int64, device="cuda")
+    graphs, outs = [], []
+    side = torch.cuda.Stream()
+    for _ in range(2):
+        work, out = kv.attend_workspace(batch, h * share, batch), torch.zeros_like(q)
+        with torch.cuda.stream(side):
+            kv.append(k, v, slots)
+            kv.attend(q, table, lens, out=out, workspace=work)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            kv.append(k, v, slots)
+            kv.attend(q, table, lens, out=out, workspace=work)
+        graphs.append((g, work))
+        outs.append(out)
+    host, tab = np.array([0, 30, 170]), table.cpu().numpy()
+    held = [[np.zeros((n, h, d)), np.zeros((n, h, d))] for n in host]
+    kv.data.zero_()     # zero words: scale 0, values 0
+    for step in range(6):
+        new = [_rows(rng, batch, h, d).half() for _ in range(2)]
+        x = torch.from_numpy(rng.standard_normal(q.shape)).half()
+        slots.copy_(torch.from_numpy(np.array([tab[b, host[b] // page] * page + host[b] % page for b in range(batch)])))
+        for b in range(batch):
+            held[b] = [np.concatenate([held[b][i], _held(new[i][b:b + 1])]) for i in range(2)]
+        host = host + 1
+        lens.copy_(torch.from_numpy(host.astype(np.int32)))
+        k.copy_(new[0])
+        v.copy_(new[1])
+        q.copy_(x)
+        graphs[step % 2][0].replay()
+        _check(outs[step % 2], None, x, held, host, range(batch + 1), F16)
+
+
+@pytest.mark.gpu
+def test_decode_steps_with_quantized_projections(orc):
+    """The operators as a layer uses them: q, k and v from quantised matrices
+    (Handle.gemv), appended and attended over, and the result through another
+    quantised matrix; every step against the oracles on the values it was given."""
+    import synth
+    h, heads, d, hidden, batch = 2, 4, 64, 256, 2
+    mats = {n: synth.make_problem(rows, cols, 3, "affine", 0.01, "uniform", s, batch)
+            for n, rows, cols, s in (("q", heads * d, hidden, 1), ("k", h * d, hidden, 2), ("v", h * d, hidden, 3),
+                                     ("o", hidden, heads * d, 4))}
+    handles = {n: dsq.Handle(dsq.pack_problem(p)) for n, p in mats.items()}
+    kv = dsq.KVCache(h, d, 8, 16)
+    table = torch.tensor([[5, 0, 2], [7, 1, 3]], dtype=torch.int32, device="cuda")
+    held = [[np.zeros((0, h, d)), np.zeros((0, h, d))] for _ in range(batch)]
+    rng = np.random.default_rng(20)
+    for step in range(20):
+        x = torch.from_numpy(rng.standard_normal((batch, hidden)) * 3).half().cuda()
+        q, k, v = (handles[n].gemv(x).view(batch, -1, d) for n in "qkv")
+        slots = table[:, step // 16].long() * 16 + step % 16
+        kv.append(k, v, slots)
+        y, lse = kv.attend(q, table, torch.full((batch,), step + 1, dtype=torch.int32, device="cuda"), return_lse=True)
+        out = handles["o"].gemv(y.reshape(batch, heads * d))
+        for b in range(batch):
+            held[b] = [np.concatenate([held[b][i], _held((k, v)[i][b:b + 1])]) for i in range(2)]
+        _check(y, lse, q.cpu(), held, [step + 1] * batch, range(batch + 1), F16)
+        mats["o"].x = y.reshape(batch, heads * d).cpu().view(torch.int16).numpy().view(np.uint16)
+        want, bound = orc.gemv(mats["o"])
+        assert np.all(np.abs(out.cpu().double().numpy() - want) <= 1e-3 * bound)
+    for p in handles.values():
+        p.close()
+
+
+@pytest.mark.gpu
+def test_binding_refusals():
+    kv = dsq.KVCache(2, 64, 2, 16)
+    k = torch.zeros(3, 2, 64, dtype=F16, device="cuda")
+    s = torch.arange(3, device="cuda")
+    t, n = torch.zeros(3, 1, dtype=torch.int32, device="cuda"), torch.ones(3, dtype=torch.int32, device="cuda")
+    for call in (lambda: kv.append(k, k.float(), s), lambda: kv.append(k, k, s.int()), lambda: kv.append(k[:2], k, s),
+                 lambda: kv.append(k.cpu(), k, s), lambda: kv.append(k.transpose(1, 2), k, s),
+                 lambda: kv.read(s, k=k, v=k.float()), lambda: kv.read(s[::2]),
+                 lambda: kv.attend(k, t, n.long()), lambda: kv.attend(k, t[:2], n), lambda: kv.attend(k[0], t, n),
+                 lambda: kv.attend(k, t, n, out=k.float()), lambda: kv.attend(k, t, n, lse=n.float()),
+                 lambda: kv.attend(k, t, n, q_start=n), lambda: kv.attend(k.double(), t, n),
+                 lambda: dsq.KVCache(2, 64, 2, 16, data=torch.zeros(5, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(ValueError):
+            call()
+    for call, rc in ((lambda: kv.append(k.float(), k.float(), s), UNS), (lambda: kv.attend(k.float(), t, n), UNS),
+                     (lambda: kv.attend(k[:, :1].contiguous(), t, n), BAD), (lambda: kv.attend(k, t[:2], n[:2]), BAD),
+                     (lambda: kv.attend(k, t, n, window=3, causal=False), BAD),
+                     (lambda: kv.attend(k, t, n, scale=float("inf")), BAD),
+                     (lambda: kv.attend(k, t, n, workspace=torch.zeros(8, dtype=torch.uint8, device="cuda")),
+                      dsq.DSQ_ERR_BUFFER_TOO_SMALL)):
+        with pytest.raises(dsq.DSQError) as e:
+            call()
+        assert e.value.status == rc
