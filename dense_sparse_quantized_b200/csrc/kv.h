@@ -6,6 +6,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "internal.h"
 
 namespace dsq {
@@ -80,7 +82,34 @@ __device__ __forceinline__ KvSeq kv_seq(const KvAttend &a, int b) {
     return s;
 }
 
-size_t kv_attend_workspace(const dsq_kv_desc *d, const dsq_kv_queries *a, int sms);
-int launch_kv_attend(const KvAttend &a, int head_dim, int dtype, void *workspace, int sms, cudaStream_t stream);
+inline bool kv_aligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
+inline bool kv_multiple8(int64_t s) { return (s & 7) == 0; }
+
+// Whether [tokens][heads] rows of D elements at these strides are apart.
+inline bool kv_rows_apart(int64_t tokens, int64_t heads, int64_t token, int64_t head, int D) {
+    if (tokens <= 1 && heads <= 1) return true;
+    if (tokens <= 1) return head >= D;
+    if (heads <= 1) return token >= D;
+    return (head >= D && token >= (heads - 1) * head + D) || (token >= D && head >= (tokens - 1) * token + D);
+}
+
+// Sets a kernel's shared-memory limit once per device (a call per launch
+// would cost a microsecond of host time).
+struct KvOnce {
+    std::atomic<uint64_t> done{0};
+    bool set_smem(const void *kernel, int bytes) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return false;
+        const uint64_t bit = 1ull << (dev & 63);
+        if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return true;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+        if (dev < 64) done.fetch_or(bit, std::memory_order_release);
+        return true;
+    }
+};
+
+// Few query rows per sequence (kv_split.cu).
+size_t kv_split_workspace();
+int launch_kv_split(const KvAttend &a, int head_dim, int dtype, void *workspace, int sms, cudaStream_t stream);
 
 }  // namespace dsq

@@ -165,22 +165,11 @@ __global__ void __launch_bounds__(kThreads) read_kernel(KvView c, RowsOut r, con
                 (T *)r.v + t * r.v_token + head * r.v_head + dim);
 }
 
-bool aligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
-bool multiple8(int64_t s) { return (s & 7) == 0; }
-
-// Whether [tokens][heads] rows of D elements at these strides are apart.
-bool rows_apart(int64_t tokens, int64_t heads, int64_t token, int64_t head, int D) {
-    if (tokens <= 1 && heads <= 1) return true;
-    if (tokens <= 1) return head >= D;
-    if (heads <= 1) return token >= D;
-    return (head >= D && token >= (heads - 1) * head + D) || (token >= D && head >= (tokens - 1) * token + D);
-}
-
 int check_rows(const dsq_kv_rows *r, bool both) {
     if (!r || (both ? !r->k || !r->v : !r->k && !r->v)) return DSQ_ERR_INVALID_ARG;
     if (r->dtype < DSQ_DTYPE_F16 || r->dtype > DSQ_DTYPE_F32) return DSQ_ERR_INVALID_ARG;
-    if (!aligned(r->k, 16) || !aligned(r->v, 16)) return DSQ_ERR_INVALID_ARG;
-    if (!multiple8(r->k_token) || !multiple8(r->k_head) || !multiple8(r->v_token) || !multiple8(r->v_head))
+    if (!kv_aligned(r->k, 16) || !kv_aligned(r->v, 16)) return DSQ_ERR_INVALID_ARG;
+    if (!kv_multiple8(r->k_token) || !kv_multiple8(r->k_head) || !kv_multiple8(r->v_token) || !kv_multiple8(r->v_head))
         return DSQ_ERR_INVALID_ARG;
     return DSQ_OK;
 }
@@ -235,7 +224,7 @@ extern "C" int dsq_kv_append(const dsq_kv_desc *d, void *cache, const dsq_kv_row
     if (rc != DSQ_OK) return rc;
     if (tokens < 0) return DSQ_ERR_INVALID_ARG;
     if (tokens == 0 || d->pages == 0) return DSQ_OK;
-    if (!cache || !slots || !aligned(cache, 128) || !aligned(slots, 8)) return DSQ_ERR_INVALID_ARG;
+    if (!cache || !slots || !kv_aligned(cache, 128) || !kv_aligned(slots, 8)) return DSQ_ERR_INVALID_ARG;
     if ((rc = check_rows(rows, true)) != DSQ_OK) return rc;
     if (rows->dtype == DSQ_DTYPE_F32) return DSQ_ERR_UNSUPPORTED;
     dim3 grid;
@@ -256,10 +245,10 @@ extern "C" int dsq_kv_read(const dsq_kv_desc *d, const void *cache, const dsq_kv
     if (rc != DSQ_OK) return rc;
     if (tokens < 0) return DSQ_ERR_INVALID_ARG;
     if (tokens == 0 || d->pages == 0) return DSQ_OK;
-    if (!cache || !slots || !aligned(cache, 128) || !aligned(slots, 8)) return DSQ_ERR_INVALID_ARG;
+    if (!cache || !slots || !kv_aligned(cache, 128) || !kv_aligned(slots, 8)) return DSQ_ERR_INVALID_ARG;
     if ((rc = check_rows(rows, false)) != DSQ_OK) return rc;
-    if ((rows->k && !rows_apart(tokens, d->kv_heads, rows->k_token, rows->k_head, d->head_dim)) ||
-        (rows->v && !rows_apart(tokens, d->kv_heads, rows->v_token, rows->v_head, d->head_dim)))
+    if ((rows->k && !kv_rows_apart(tokens, d->kv_heads, rows->k_token, rows->k_head, d->head_dim)) ||
+        (rows->v && !kv_rows_apart(tokens, d->kv_heads, rows->v_token, rows->v_head, d->head_dim)))
         return DSQ_ERR_INVALID_ARG;
     dim3 grid;
     if ((rc = grid_for(tokens, d->kv_heads, d->head_dim, &grid)) != DSQ_OK) return rc;
@@ -271,56 +260,4 @@ extern "C" int dsq_kv_read(const dsq_kv_desc *d, const void *cache, const dsq_kv
     else if (d->head_dim == 128) launch_read<128>(grid, c, rows, slots, tokens, st);
     else launch_read<256>(grid, c, rows, slots, tokens, st);
     return cudaGetLastError() == cudaSuccess ? DSQ_OK : DSQ_ERR_CUDA;
-}
-
-extern "C" int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_kv_queries *a, void *workspace,
-                             size_t *workspace_bytes, void *stream) {
-    int rc = kv_check_desc(d);
-    if (rc != DSQ_OK) return rc;
-    if (!a || !workspace_bytes) return DSQ_ERR_INVALID_ARG;
-    if (a->q_heads < 1 || a->q_heads % d->kv_heads || a->batch < 0 || a->q_tokens < 0 || a->table_pages < 0 ||
-        a->window < 0 || (a->window > 0 && !a->causal) || !isfinite(a->scale))
-        return DSQ_ERR_INVALID_ARG;
-    if (a->dtype != DSQ_DTYPE_F16 && a->dtype != DSQ_DTYPE_BF16)
-        return a->dtype == DSQ_DTYPE_F32 ? DSQ_ERR_UNSUPPORTED : DSQ_ERR_INVALID_ARG;
-    if (a->batch > 0 && !a->q_start && a->q_tokens % a->batch) return DSQ_ERR_INVALID_ARG;
-    if ((int64_t)a->table_pages * d->page_tokens >= ((int64_t)1 << 31) || a->q_tokens * a->q_heads >= ((int64_t)1 << 31))
-        return DSQ_ERR_UNSUPPORTED;
-    const size_t need = kv_attend_workspace(d, a, 148);
-    if (!workspace || *workspace_bytes < need) {
-        *workspace_bytes = need;
-        return DSQ_ERR_BUFFER_TOO_SMALL;
-    }
-    if (a->batch == 0 || a->q_tokens == 0) return DSQ_OK;
-    if (!a->q || !a->out || !a->kv_lens || (a->table_pages > 0 && !a->page_table) || (d->pages > 0 && !cache))
-        return DSQ_ERR_INVALID_ARG;
-    if (!aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->lse, 4) || !aligned(cache, 128) ||
-        !aligned(workspace, 256) || !aligned(a->page_table, 4) || !aligned(a->kv_lens, 4) || !aligned(a->q_start, 4))
-        return DSQ_ERR_INVALID_ARG;
-    if (!multiple8(a->q_token) || !multiple8(a->q_head) || !multiple8(a->out_token) || !multiple8(a->out_head) ||
-        !rows_apart(a->q_tokens, a->q_heads, a->out_token, a->out_head, d->head_dim))
-        return DSQ_ERR_INVALID_ARG;
-    DeviceGuard guard(d->device);
-    if (!guard.ok) return DSQ_ERR_CUDA;
-    KvAttend k = {};
-    k.c = kv_view(d, cache);
-    k.q = a->q;
-    k.out = a->out;
-    k.lse = a->lse;
-    k.q_token = a->q_token;
-    k.q_head = a->q_head;
-    k.out_token = a->out_token;
-    k.out_head = a->out_head;
-    k.q_tokens = a->q_tokens;
-    k.q_heads = a->q_heads;
-    k.share = a->q_heads / d->kv_heads;
-    k.batch = a->batch;
-    k.table_pages = a->table_pages;
-    k.causal = a->causal;
-    k.window = a->window;
-    k.scale_log2 = a->scale * 1.4426950408889634f;
-    k.page_table = a->page_table;
-    k.kv_lens = a->kv_lens;
-    k.q_start = a->q_start;
-    return launch_kv_attend(k, d->head_dim, a->dtype, workspace, 148, (cudaStream_t)stream);
 }

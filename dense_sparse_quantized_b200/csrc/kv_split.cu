@@ -1,0 +1,783 @@
+// kv_split.cu -- attention over the 4-bit cache for few query rows per
+// sequence: bound by the cache's bytes, so everything here serves to stream
+// them.
+//
+// Work.  A job is (sequence, kv head, tile of R query rows), a row being one
+// (query token, query head of the group) pair, so the heads that share a kv
+// head share its bytes.  A job's tokens are cut into units of 32; the units of
+// all jobs, in order, are dealt to the CTAs in equal runs, and a CTA's run to
+// its warps in equal runs, wherever the jobs begin and end: long and short
+// sequences and any number of heads fill the GPU alike.  Each warp finds its
+// place from kv_lens and q_start itself, so nothing is planned on the host
+// and a captured call follows the lengths.
+//
+// A warp runs through its units alone, with a running maximum and sum.  A job
+// inside one warp's run is written at once.  What spans warps of a CTA is
+// merged in shared memory at the end, what spans CTAs through the workspace by
+// combine_kernel, always in the same order.
+//
+// A unit.  Two tiles of 16 tokens, brought to the warp's own ring in shared
+// memory by cp.async of whole tiles.  Scores: mma.sync m16n8k16 with the 16
+// tokens of a tile as M and the rows as N = 8 (a group of eight heads fills
+// it; the cache's codes are unpacked once for all rows).  The order of the 16
+// tokens along M and k and that of the dimensions along k and M is free, so
+// it is chosen such that a lane's fragment is what it can load whole:
+//   keys: lane (r, j) holds D/4 consecutive dimensions of tokens tok(r) and
+//     tok(r) + 2, tok(r) = 4 (r / 2) + r % 2;
+//   values: D/8 consecutive dimensions, from r D/8 on, of tokens 4j .. 4j+3.
+// Codes become fp16 exactly: LOP3 places two in the halves of 1024 (or 64),
+// HADD2 takes off 1024 + zero, HMUL2 multiplies by the scale -- 4 bits times 7
+// bits, no rounding.  The scores' fragment, rounded to fp16 and transposed by
+// movmatrix, is the B operand of the second product, out^T = V^T P^T.
+//
+// The running maximum is raised only when some score exceeds it by more than
+// 2^8 in the numerator (one vote a unit); until then numerators up to 256 are
+// as exact as ones up to 1.
+#include <algorithm>
+
+#include "kv.h"
+#include "ptx.h"
+
+namespace dsq {
+
+namespace {
+
+constexpr float kNoMax = -3.0e38f;  // a maximum of no scores: finite, so that -inf minus it stays -inf
+constexpr float kLazy = 8.0f;       // log2 of how far numerators may pass 1
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kMaxCtas = 160;       // workspace slots; the grid is one CTA per SM, at most this
+
+// A tiling: head dimension, tiles of eight query rows, warps of a CTA, tiles
+// of a warp's ring.  Shared memory of a warp: the ring, whose space takes the
+// warp's last partial result when it is done, and its first partial result.
+template <int D_, int NT_, int NW_, int RING_>
+struct Split {
+    static constexpr int D = D_, NT = NT_, NW = NW_, RING = RING_;
+    static constexpr int R = 8 * NT;
+    static constexpr int kTile = kv_tile_bytes(D);
+    static constexpr int kPart = (R * (D + 2) * 4 + 15) / 16 * 16;
+    static constexpr int kWarp = RING * kTile + kPart;
+    static constexpr int kSmem = NW * kWarp;
+    static_assert(RING * kTile >= kPart && RING % 2 == 0 && kSmem <= 224 * 1024, "shared memory of a CTA");
+};
+
+// What a CTA leaves for combine_kernel: the job that begins in its run and
+// goes on in `more` further CTAs.
+struct Meta {
+    int valid, more, b, head, qt, pad[3];
+};
+
+struct SplitParams {
+    KvAttend a;
+    float *part;  // [CTA][first, last][R][D], then [CTA][2][R] maxima and sums
+    Meta *meta;   // [CTA]
+    int min_run;  // least units of a CTA's run
+};
+
+__device__ __forceinline__ uint32_t lop_magic(uint32_t w, uint32_t mask, uint32_t magic) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));  // (w & mask) | magic
+    return r;
+}
+__device__ __forceinline__ uint32_t hadd2u(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t a) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Scale and zero of a pair of codes: two fp16 scales, and minus 1024 plus
+// zero (for codes at the bottom of the halves) or minus 64 plus zero.
+struct Decode {
+    uint32_t s, z1024, z64;
+    __device__ __forceinline__ explicit Decode(uint32_t words) {
+        s = words & 0xfff0fff0u;
+        z1024 = lop_magic(words, 0x000f000fu, 0xe400e400u);
+        z64 = hadd2u(z1024, 0x63806380u);  // + 960
+    }
+    // Codes 0, 1 of each half of w (bits 0-3 and 4-7).
+    __device__ __forceinline__ uint32_t low(uint32_t w) const {
+        return hmul2u(hadd2u(lop_magic(w, 0x000f000fu, 0x64006400u), z1024), s);
+    }
+    __device__ __forceinline__ uint32_t high(uint32_t w) const {
+        return hmul2u(hadd2u(lop_magic(w, 0x00f000f0u, 0x54005400u), z64), s);
+    }
+};
+
+// Where 16-byte chunk c of a token's row of codes goes in a ring tile, such
+// that the fragment loads below meet no bank twice.  Keys: the rows in the
+// order of M; values: rows t at t / 4 + 4 (t % 4).
+template <int D>
+__device__ __forceinline__ int key_at(int t, int c) {
+    const int row = (t >> 2) * 2 + (t & 1) + ((t & 2) << 2);
+    return row * (D / 2) + (D == 256 ? c ^ (row & 1) : c) * 16;
+}
+template <int D>
+__device__ __forceinline__ int value_at(int t, int c) {
+    const int row = (t >> 2) + 4 * (t & 3);
+    return kv_codes(D, 1) + row * (D / 2) + (D == 256 ? c ^ (2 * (t >> 2)) : D == 128 ? c ^ (2 * (t >> 3)) : c) * 16;
+}
+
+template <int D>
+__device__ __forceinline__ void issue_tile(uint32_t dst, const uint8_t *src, int lane) {
+    constexpr int kRow = D / 32;          // chunks of a token's row
+    constexpr int kCodes = 16 * kRow;     // of K or V codes
+#pragma unroll
+    for (int i = lane; i < kCodes; i += 32) {
+        cp_async16(dst + key_at<D>(i / kRow, i % kRow), src + i * 16);
+        cp_async16(dst + value_at<D>(i / kRow, i % kRow), src + kv_codes(D, 1) + i * 16);
+    }
+    constexpr int kWords = D / 8;         // of K and V words: 16 tokens x D/32 groups x 2 bytes each
+    if (lane < kWords) cp_async16(dst + kv_words(D, 0) + lane * 16, src + kv_words(D, 0) + lane * 16);
+}
+
+// Job numbers of a sequence.
+struct Jobs {
+    int rows, len, lo, units, tiles;  // query rows, tokens, first token any query sees, units of a job, row tiles
+    int64_t row0, weight;             // first row; units of all the sequence's jobs
+};
+template <int R>
+__device__ __forceinline__ Jobs jobs_of(const KvAttend &a, int b) {
+    const KvSeq s = kv_seq(a, b);
+    Jobs j;
+    j.rows = s.rows;
+    j.len = s.len;
+    j.row0 = s.row0;
+    j.lo = a.window ? max(0, s.len - s.rows - a.window + 1) : 0;
+    j.units = max(1, (s.len + 31) / 32 - j.lo / 32);
+    j.tiles = (int)(((int64_t)s.rows * a.share + R - 1) / R);
+    j.weight = (int64_t)a.c.kv_heads * j.tiles * j.units;
+    return j;
+}
+
+// The 16-bit rows of q and out.
+template <typename T>
+struct Pair;
+template <>
+struct Pair<__half> {
+    static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack_h2(a, b); }
+};
+template <>
+struct Pair<__nv_bfloat16> {
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        uint32_t r;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+        return r;
+    }
+};
+
+// Tokens [lo, hi) that query row `rho` of the job (of the sequence's rows x
+// share) sees.
+__device__ __forceinline__ int2 seen_by(const KvAttend &a, const Jobs &j, int rho) {
+    const int pos = j.len - j.rows + rho / a.share;
+    return make_int2(a.window ? max(0, pos - a.window + 1) : 0, a.causal ? min(j.len, pos + 1) : j.len);
+}
+
+template <typename T>
+__device__ __forceinline__ int64_t row_at(const KvAttend &a, const Jobs &j, int head, int rho, int64_t token_stride,
+                                          int64_t head_stride) {
+    return (j.row0 + rho / a.share) * token_stride + (int64_t)(head * a.share + rho % a.share) * head_stride;
+}
+
+template <typename S, typename T>
+__global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_constant__ SplitParams p) {
+    constexpr int D = S::D, NT = S::NT, NW = S::NW, RING = S::RING, R = S::R;
+    constexpr int KW = D / 32;   // 8-code words of a lane's key dimensions
+    constexpr int VW = D / 64;   // and of its value dimensions
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int head_valid[NW], head_ended[NW], tail_valid[NW];
+    __shared__ int job_id[NW + 1][3];  // (b, kv head, row tile) of each warp's last job; [NW]: of the CTA's first
+    __shared__ int64_t job_end[NW];    // unit behind the last job's last
+    const KvAttend &a = p.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, jj = lane & 3;
+    const uint32_t ring = smem_u32(smem) + warp * S::kWarp;
+    float *const head_part = reinterpret_cast<float *>(smem + warp * S::kWarp + RING * S::kTile);
+    float *const tail_part = reinterpret_cast<float *>(smem + warp * S::kWarp);
+
+    // Total work, and this warp's run [u, u_end) of it.
+    int64_t total = 0;
+    for (int b = lane; b < a.batch; b += 32) total += jobs_of<R>(a, b).weight;
+#pragma unroll
+    for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(kFull, total, m);
+    const int64_t run = max((total + gridDim.x - 1) / gridDim.x, (int64_t)p.min_run);
+    const int64_t cta0 = min(total, run * blockIdx.x), cta1 = min(total, cta0 + run);
+    const int64_t mine = (cta1 - cta0 + NW - 1) / NW;
+    int64_t u = min(cta1, cta0 + warp * mine);
+    const int64_t u_end = min(cta1, u + mine);
+    if (lane == 0) head_valid[warp] = head_ended[warp] = tail_valid[warp] = 0;
+    if (threadIdx.x == 0) p.meta[blockIdx.x].valid = 0;
+
+    // The sequence u lies in, and the units before that sequence.
+    int b = 0;
+    int64_t before = 0;
+    if (u < u_end) {
+        for (int b0 = 0; b0 < a.batch; b0 += 32) {
+            const int64_t w = b0 + lane < a.batch ? jobs_of<R>(a, b0 + lane).weight : 0;
+            int64_t sum = w;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const int64_t up = __shfl_up_sync(kFull, sum, m);
+                if (lane >= m) sum += up;
+            }
+            const uint32_t past = __ballot_sync(kFull, before + sum > u);
+            if (past) {
+                const int l = __ffs(past) - 1;
+                b = b0 + l;
+                before += __shfl_sync(kFull, sum - w, l);
+                break;
+            }
+            before += __shfl_sync(kFull, sum, 31);
+        }
+    }
+
+    while (u < u_end && b < a.batch) {
+        Jobs j = jobs_of<R>(a, b);
+        if (u >= before + j.weight) {
+            before += j.weight;
+            b++;
+            continue;
+        }
+        // The job, and the units of it that are in this run.
+        const int64_t rel = u - before;
+        const int64_t job = rel / j.units;
+        const int head = (int)(job / j.tiles), qt = (int)(job % j.tiles);
+        const int first = (int)(rel - job * j.units);
+        const int last = (int)min((int64_t)j.units, first + (u_end - u));  // units [first, last) of the job
+        const int rho0 = qt * R, rho1 = min(rho0 + R, j.rows * a.share) - 1;
+        const int2 seen0 = seen_by(a, j, rho0), seen1 = seen_by(a, j, rho1);
+        const int lo_any = seen0.x, hi_any = seen1.y, lo_all = seen1.x, hi_all = seen0.y;
+        // Tiles of 16 tokens: those of the units, less what no row sees.
+        const int unit0 = j.lo / 32;
+        const int tile0 = max((unit0 + first) * 2, lo_any / 32 * 2);
+        const int tile1 = min((unit0 + last) * 2, (max(hi_any, 0) + 15) / 16);
+
+        // Page numbers of the next 64 table columns, one per lane and register.
+        int col = tile0 / a.c.page_tiles, in_page = tile0 - col * a.c.page_tiles, col0 = col;
+        const int32_t *row = a.page_table + (int64_t)b * a.table_pages;
+        auto pages_from = [&](int c) { return c + lane < a.table_pages ? row[c + lane] : -1; };
+        int pages = pages_from(col0), pages_next = pages_from(col0 + 32);
+        const uint8_t *const base = a.c.cache + (int64_t)head * a.c.page_tiles * S::kTile;
+        uint32_t valid = 0;  // bit i: ring tile i holds a tile of the cache
+        int slot = 0, next = tile0;
+        auto issue = [&] {
+            const int page = __shfl_sync(kFull, pages, col - col0);
+            const bool there = next < tile1 && (uint32_t)page < (uint32_t)a.c.pages;
+            if (there)
+                issue_tile<D>(ring + slot * S::kTile,
+                              base + ((int64_t)page * a.c.kv_heads * a.c.page_tiles + in_page) * S::kTile, lane);
+            cp_async_commit();
+            valid = (valid & ~(1u << slot)) | ((uint32_t)there << slot);
+            slot = slot + 1 == RING ? 0 : slot + 1;
+            next++;
+            if (++in_page == a.c.page_tiles) {
+                in_page = 0;
+                if (++col - col0 == 32) {
+                    col0 += 32;
+                    pages = pages_next;
+                    pages_next = pages_from(col0 + 32);
+                }
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < RING; i++) issue();
+
+        // Queries: the B operand of the scores, column n = r.  bf16 rows are
+        // scaled by a power of two so that fp16 holds them.
+        uint32_t q[D / 16][NT][2];
+        float scale[NT][2];  // of the accumulator's columns 2 jj, 2 jj + 1
+        int2 seen[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            const int rho = min(rho0 + 8 * n + r, rho1);
+            const uint4 *src = reinterpret_cast<const uint4 *>((const T *)a.q + row_at<T>(a, j, head, rho, a.q_token, a.q_head) +
+                                                               jj * (D / 4));
+            uint4 raw[KW];
+#pragma unroll
+            for (int w = 0; w < KW; w++) raw[w] = src[w];
+            float factor = a.scale_log2;
+            if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
+                uint32_t top = 0;  // largest magnitude, as bits
+#pragma unroll
+                for (int w = 0; w < KW; w++) {
+                    const uint32_t x[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
+#pragma unroll
+                    for (int i = 0; i < 4; i++) top = max(top, max(x[i] & 0x7fffu, (x[i] >> 16) & 0x7fffu));
+                }
+                top = max(top, __shfl_xor_sync(kFull, top, 1));
+                top = max(top, __shfl_xor_sync(kFull, top, 2));
+                const int e = (int)(top >> 7);  // biased; 0 for zero, 255 for an infinity or a NaN
+                const int k = e == 0 || e == 255 ? 0 : min(127 + 14 - e, 120);
+                const float up = __uint_as_float((uint32_t)(127 + k) << 23);
+                factor *= __uint_as_float((uint32_t)(127 - k) << 23);
+#pragma unroll
+                for (int w = 0; w < KW; w++) {
+                    uint32_t x[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        x[i] = pack_h2(__uint_as_float(x[i] << 16) * up, __uint_as_float(x[i] & 0xffff0000u) * up);
+                    raw[w] = make_uint4(x[0], x[1], x[2], x[3]);
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < KW; w++) {  // dimensions (0, 4), (1, 5), (2, 6), (3, 7) of eight, as the codes come
+                q[2 * w][n][0] = prmt(raw[w].x, raw[w].z, 0x5410);
+                q[2 * w][n][1] = prmt(raw[w].x, raw[w].z, 0x7632);
+                q[2 * w + 1][n][0] = prmt(raw[w].y, raw[w].w, 0x5410);
+                q[2 * w + 1][n][1] = prmt(raw[w].y, raw[w].w, 0x7632);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                scale[n][c] = __shfl_sync(kFull, factor, (2 * jj + c) * 4);
+                seen[n][c] = seen_by(a, j, min(rho0 + 8 * n + 2 * jj + c, rho1));
+            }
+        }
+
+        float o[D / 16][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+        for (int i = 0; i < D / 16; i++)
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int k = 0; k < 4; k++) o[i][n][k] = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                m[n][c] = kNoMax;
+                l[n][c] = 0.0f;
+            }
+
+        int at = 0;  // ring tile of the next unit
+        for (int tile = tile0; tile < tile1; tile += 2) {
+            cp_async_wait<RING - 2>();
+            __syncwarp();
+            const int t0 = tile * 16;
+            const bool masked = t0 < lo_all || t0 + 32 > hi_all || ((valid >> at) & 3u) != 3u;
+            float s[2][NT][4];
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const uint32_t buf = ring + (at + h) * S::kTile;
+#pragma unroll
+                for (int n = 0; n < NT; n++)
+#pragma unroll
+                    for (int k = 0; k < 4; k++) s[h][n][k] = 0.0f;
+                uint32_t kw[2][KW];
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const uint32_t at_row = buf + (r + 8 * e) * (D / 2);
+                    if constexpr (D == 64)
+                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(kw[e][0]), "=r"(kw[e][1]) : "r"(at_row + jj * 8));
+                    else {
+#pragma unroll
+                        for (int c = 0; c < KW / 4; c++) {
+                            const int chunk = jj * (KW / 4) + c;
+                            const uint4 v = lds128(at_row + (D == 256 ? chunk ^ (r & 1) : chunk) * 16);
+                            kw[e][4 * c] = v.x;
+                            kw[e][4 * c + 1] = v.y;
+                            kw[e][4 * c + 2] = v.z;
+                            kw[e][4 * c + 3] = v.w;
+                        }
+                    }
+                }
+                constexpr int G = D == 256 ? 2 : 1;  // groups of a lane's key dimensions
+#pragma unroll
+                for (int g = 0; g < G; g++) {
+                    const int tok = 4 * (r >> 1) + (r & 1);
+                    const uint32_t word_at = buf + kv_words(D, 0) + (jj * (D / 4) / 32 + g) * 32 + tok * 2;
+                    uint16_t p0, p1;
+                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(p0) : "r"(word_at));
+                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(p1) : "r"(word_at + 4));
+                    const Decode d0(prmt(p0, p0, 0x1010)), d1(prmt(p1, p1, 0x1010));
+#pragma unroll
+                    for (int w = g * (KW / G); w < (g + 1) * (KW / G); w++) {
+                        const uint32_t x = kw[0][w], y = kw[1][w];
+                        const uint32_t f0[4] = {d0.low(x), d1.low(y), d0.high(x), d1.high(y)};
+                        const uint32_t f1[4] = {d0.low(x >> 8), d1.low(y >> 8), d0.high(x >> 8), d1.high(y >> 8)};
+#pragma unroll
+                        for (int n = 0; n < NT; n++) {
+                            mma16816(s[h][n], f0, q[2 * w][n][0], q[2 * w][n][1]);
+                            mma16816(s[h][n], f1, q[2 * w + 1][n][0], q[2 * w + 1][n][1]);
+                        }
+                    }
+                }
+            }
+            // Scores in powers of two; column c of s is k % 2, its token tok + 2 (k / 2).
+            bool raise = false;
+            float top[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int c = 0; c < 2; c++) {
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        s[h][n][c] *= scale[n][c];
+                        s[h][n][2 + c] *= scale[n][c];
+                    }
+                }
+            if (masked) {
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const bool there = (valid >> (at + h)) & 1u;
+#pragma unroll
+                    for (int n = 0; n < NT; n++)
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            const int t = t0 + 16 * h + 4 * (r >> 1) + (r & 1) + (k & 2);
+                            if (!there || t < seen[n][k & 1].x || t >= seen[n][k & 1].y) s[h][n][k] = -INFINITY;
+                        }
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int c = 0; c < 2; c++) {
+                    top[n][c] = fmaxf(fmaxf(s[0][n][c], s[0][n][2 + c]), fmaxf(s[1][n][c], s[1][n][2 + c]));
+                    raise |= top[n][c] > m[n][c] + kLazy;
+                }
+            if (__any_sync(kFull, raise)) {
+#pragma unroll
+                for (int n = 0; n < NT; n++)
+#pragma unroll
+                    for (int c = 0; c < 2; c++) {
+                        float x = top[n][c];
+                        x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
+                        x = fmaxf(x, m[n][c]);
+                        const float keep = exp2f(m[n][c] - x);
+                        m[n][c] = x;
+                        l[n][c] *= keep;
+#pragma unroll
+                        for (int i = 0; i < D / 16; i++) {
+                            o[i][n][c] *= keep;
+                            o[i][n][2 + c] *= keep;
+                        }
+                    }
+            }
+            uint32_t pb[2][NT][2];
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+#pragma unroll
+                for (int n = 0; n < NT; n++) {
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        s[h][n][k] = exp2f(s[h][n][k] - m[n][k & 1]);
+                        l[n][k & 1] += s[h][n][k];
+                    }
+                }
+            // Values.  In a unit whose rows see different tokens, a NaN value
+            // must reach the rows that see it alone: its scale becomes 0 and
+            // those rows' numerators NaN.  Tokens that no row sees, which may
+            // be anything, get scale 0.
+            uint2 vp[2];
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const uint32_t word_at = ring + (at + h) * S::kTile + kv_words(D, 1) + (r * (D / 8) / 32) * 32 + jj * 8;
+                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(vp[h].x), "=r"(vp[h].y) : "r"(word_at));
+                if (masked) {
+                    const bool there = (valid >> (at + h)) & 1u;
+                    uint32_t bad = 0;
+                    uint32_t w[2] = {vp[h].x, vp[h].y};
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const int t = t0 + 16 * h + 4 * jj + i;
+                        const bool use = there && t >= lo_any && t < hi_any;
+                        const bool nan = ((w[i / 2] >> (16 * (i % 2))) & 0x7c00u) == 0x7c00u;
+                        if (!use || nan) w[i / 2] &= i % 2 ? 0x0000ffffu : 0xffff0000u;
+                        if (use && nan) bad |= 1u << (4 * jj + i);
+                    }
+                    vp[h] = make_uint2(w[0], w[1]);
+                    bad = __reduce_or_sync(kFull, bad);
+                    if (bad) {
+#pragma unroll
+                        for (int n = 0; n < NT; n++)
+#pragma unroll
+                            for (int k = 0; k < 4; k++) {
+                                const int t = 4 * (r >> 1) + (r & 1) + (k & 2);
+                                if (((bad >> t) & 1u) && t0 + 16 * h + t >= seen[n][k & 1].x && t0 + 16 * h + t < seen[n][k & 1].y)
+                                    s[h][n][k] = NAN;
+                            }
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NT; n++) {
+                    pb[h][n][0] = movmatrix_t(pack_h2(s[h][n][0], s[h][n][1]));
+                    pb[h][n][1] = movmatrix_t(pack_h2(s[h][n][2], s[h][n][3]));
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const uint32_t buf = ring + (at + h) * S::kTile;
+                uint32_t vw[4][VW];
+#pragma unroll
+                for (int i = 0; i < 4; i++) {  // token 4 jj + i: row jj + 4 i
+                    const uint32_t at_row = buf + kv_codes(D, 1) + (jj + 4 * i) * (D / 2);
+                    if constexpr (D == 64)
+                        vw[i][0] = lds32(at_row + r * 4);
+                    else if constexpr (D == 128)
+                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(vw[i][0]), "=r"(vw[i][1]) : "r"(at_row + ((r >> 1) ^ (2 * (jj >> 1))) * 16 + (r & 1) * 8));
+                    else {
+                        const uint4 v = lds128(at_row + (r ^ (2 * jj)) * 16);
+                        vw[i][0] = v.x;
+                        vw[i][1] = v.y;
+                        vw[i][2] = v.z;
+                        vw[i][3] = v.w;
+                    }
+                }
+                const Decode d0(vp[h].x), d1(vp[h].y);
+#pragma unroll
+                for (int w = 0; w < VW; w++) {
+#pragma unroll
+                    for (int half = 0; half < 2; half++) {
+                        const uint32_t sel = half ? 0x7632u : 0x5410u;
+                        const uint32_t x = prmt(vw[0][w], vw[1][w], sel), y = prmt(vw[2][w], vw[3][w], sel);
+                        const uint32_t f0[4] = {d0.low(x), d0.high(x), d1.low(y), d1.high(y)};
+                        const uint32_t f1[4] = {d0.low(x >> 8), d0.high(x >> 8), d1.low(y >> 8), d1.high(y >> 8)};
+#pragma unroll
+                        for (int n = 0; n < NT; n++) {
+                            mma16816(o[4 * w + 2 * half][n], f0, pb[h][n][0], pb[h][n][1]);
+                            mma16816(o[4 * w + 2 * half + 1][n], f1, pb[h][n][0], pb[h][n][1]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            at = at + 2 == RING ? 0 : at + 2;
+            issue();
+            issue();
+        }
+        cp_async_wait<0>();
+        __syncwarp();
+
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                l[n][c] += __shfl_xor_sync(kFull, l[n][c], 4);
+                l[n][c] += __shfl_xor_sync(kFull, l[n][c], 8);
+                l[n][c] += __shfl_xor_sync(kFull, l[n][c], 16);
+            }
+        const bool begins = first == 0, ends = last == j.units;
+        if (begins && ends) {
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int c = 0; c < 2; c++) {
+                    const int rho = rho0 + 8 * n + 2 * jj + c;
+                    if (rho > rho1) continue;
+                    const float inv = l[n][c] == 0.0f ? 0.0f : 1.0f / l[n][c];
+                    T *dst = (T *)a.out + row_at<T>(a, j, head, rho, a.out_token, a.out_head) + r * (D / 8);
+#pragma unroll
+                    for (int i = 0; i < D / 16; i += 4)
+                        *reinterpret_cast<uint4 *>(dst + 2 * i) =
+                            make_uint4(Pair<T>::pack(o[i][n][c] * inv, o[i][n][2 + c] * inv),
+                                       Pair<T>::pack(o[i + 1][n][c] * inv, o[i + 1][n][2 + c] * inv),
+                                       Pair<T>::pack(o[i + 2][n][c] * inv, o[i + 2][n][2 + c] * inv),
+                                       Pair<T>::pack(o[i + 3][n][c] * inv, o[i + 3][n][2 + c] * inv));
+                    if (a.lse && r == 0)
+                        a.lse[row_at<T>(a, j, head, rho, a.q_heads, 1)] =
+                            l[n][c] == 0.0f ? -INFINITY : (m[n][c] + log2f(l[n][c])) * 0.69314718055994531f;
+                }
+        } else {
+            float *dst = begins ? tail_part : head_part;
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int c = 0; c < 2; c++) {
+                    const int row_n = 8 * n + 2 * jj + c;
+#pragma unroll
+                    for (int i = 0; i < D / 16; i++)
+                        *reinterpret_cast<float2 *>(dst + row_n * D + r * (D / 8) + 2 * i) = make_float2(o[i][n][c], o[i][n][2 + c]);
+                    if (r == 0) {
+                        dst[R * D + row_n] = m[n][c];
+                        dst[R * D + R + row_n] = l[n][c];
+                    }
+                }
+            if (lane == 0) {
+                if (begins) {
+                    tail_valid[warp] = 1;
+                    job_id[warp][0] = b;
+                    job_id[warp][1] = head;
+                    job_id[warp][2] = qt;
+                    job_end[warp] = before + (job + 1) * j.units;
+                } else {
+                    head_valid[warp] = 1;
+                    head_ended[warp] = ends;
+                }
+            }
+        }
+        u += last - first;
+    }
+    __syncthreads();
+
+    // What spans warps: every chain of partial results, first to last.
+    for (int w = -1; w < NW; w++) {
+        if (w < 0 ? !head_valid[0] : !tail_valid[w]) continue;
+        int n = w < 0 ? 0 : 1, k = w + 1;  // partial results: warp w's last, then the first ones of warps w + 1 .. w + n
+        bool ended = false;
+        for (; k < NW && head_valid[k] && !ended; k++, n++) ended = head_ended[k];
+        auto part = [&](int i) {
+            const bool tail = w >= 0 && i == 0;
+            const int of = w < 0 ? i : w + i;
+            return reinterpret_cast<const float *>(smem + of * S::kWarp + (tail ? 0 : RING * S::kTile));
+        };
+        const bool whole = w >= 0 && ended;
+        Jobs j;
+        int head = 0, rho0 = 0;
+        float *to = nullptr;
+        if (whole) {
+            j = jobs_of<R>(a, job_id[w][0]);
+            head = job_id[w][1];
+            rho0 = job_id[w][2] * R;
+        } else {
+            to = p.part + (int64_t)(2 * blockIdx.x + (w < 0 ? 0 : 1)) * R * (D + 2);
+            if (w >= 0 && threadIdx.x == 0) {
+                Meta mt = {1, (int)((job_end[w] - 1) / run) - (int)blockIdx.x, job_id[w][0], job_id[w][1], job_id[w][2], {}};
+                p.meta[blockIdx.x] = mt;
+            }
+        }
+        for (int i = threadIdx.x; i < R * D / 2; i += NW * 32) {
+            const int row = i / (D / 2), d = i % (D / 2) * 2;
+            float top = kNoMax, sum = 0.0f, x = 0.0f, y = 0.0f;
+            for (int k2 = 0; k2 < n; k2++) top = fmaxf(top, part(k2)[R * D + row]);
+            for (int k2 = 0; k2 < n; k2++) {
+                const float *src = part(k2);
+                const float f = exp2f(src[R * D + row] - top);
+                const float2 v = *reinterpret_cast<const float2 *>(src + row * D + d);
+                sum += f * src[R * D + R + row];
+                x += f * v.x;
+                y += f * v.y;
+            }
+            if (whole) {
+                if (rho0 + row >= j.rows * a.share) continue;
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                *reinterpret_cast<uint32_t *>((T *)a.out + row_at<T>(a, j, head, rho0 + row, a.out_token, a.out_head) + d) =
+                    Pair<T>::pack(x * inv, y * inv);
+                if (a.lse && d == 0)
+                    a.lse[row_at<T>(a, j, head, rho0 + row, a.q_heads, 1)] =
+                        sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+            } else {
+                *reinterpret_cast<float2 *>(to + row * D + d) = make_float2(x, y);
+                if (d == 0) {
+                    to[R * D + row] = top;
+                    to[R * D + R + row] = sum;
+                }
+            }
+        }
+    }
+}
+
+// One block per CTA of split_kernel and row: the job that began in that CTA's
+// run and went on, over all of its CTAs in order.
+template <typename S, typename T>
+__global__ void __launch_bounds__(S::D / 2) combine_kernel(const __grid_constant__ SplitParams p) {
+    constexpr int D = S::D, R = S::R;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Meta mt = p.meta[blockIdx.x];
+    if (!mt.valid) return;
+    const KvAttend &a = p.a;
+    const Jobs j = jobs_of<R>(a, mt.b);
+    const int row = blockIdx.y, rho = mt.qt * R + row;
+    if (rho >= j.rows * a.share) return;
+    auto part = [&](int i) { return p.part + (int64_t)(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * R * (D + 2); };
+    float top = kNoMax, sum = 0.0f, x = 0.0f, y = 0.0f;
+    for (int i = 0; i <= mt.more; i++) top = fmaxf(top, part(i)[R * D + row]);
+    for (int i = 0; i <= mt.more; i++) {
+        const float *src = part(i);
+        const float f = exp2f(src[R * D + row] - top);
+        const float2 v = *reinterpret_cast<const float2 *>(src + row * D + threadIdx.x * 2);
+        sum += f * src[R * D + R + row];
+        x += f * v.x;
+        y += f * v.y;
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    *reinterpret_cast<uint32_t *>((T *)a.out + row_at<T>(a, j, mt.head, rho, a.out_token, a.out_head) + threadIdx.x * 2) =
+        Pair<T>::pack(x * inv, y * inv);
+    if (a.lse && threadIdx.x == 0)
+        a.lse[row_at<T>(a, j, mt.head, rho, a.q_heads, 1)] =
+            sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+}
+
+template <typename S>
+constexpr size_t part_bytes() {
+    return (size_t)kMaxCtas * 2 * S::R * (S::D + 2) * 4;
+}
+
+template <typename S, typename T>
+int launch_split(const KvAttend &a, void *workspace, int sms, cudaStream_t st) {
+    SplitParams p = {};
+    p.a = a;
+    p.part = (float *)workspace;
+    p.meta = (Meta *)((uint8_t *)workspace + part_bytes<S>());
+    p.min_run = 4;
+    auto kernel = split_kernel<S, T>;
+    static KvOnce once;
+    if (!once.set_smem((const void *)kernel, S::kSmem)) return DSQ_ERR_CUDA;
+    const int grid = std::min(sms, kMaxCtas);
+    kernel<<<grid, S::NW * 32, S::kSmem, st>>>(p);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, S::R);
+    cfg.blockDim = S::D / 2;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, combine_kernel<S, T>, p) != cudaSuccess) return DSQ_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? DSQ_OK : DSQ_ERR_CUDA;
+}
+
+template <typename T>
+int launch_of(const KvAttend &a, int head_dim, void *workspace, int sms, cudaStream_t st) {
+    // Sixteen rows at once when a job has more than eight: the cache is read
+    // and unpacked half as often.
+    const bool wide = a.q_tokens / a.batch * a.share > 8;
+    if (head_dim == 64)
+        return wide ? launch_split<Split<64, 2, 16, 8>, T>(a, workspace, sms, st)
+                    : launch_split<Split<64, 1, 16, 8>, T>(a, workspace, sms, st);
+    if (head_dim == 128)
+        return wide ? launch_split<Split<128, 2, 12, 4>, T>(a, workspace, sms, st)
+                    : launch_split<Split<128, 1, 16, 4>, T>(a, workspace, sms, st);
+    return launch_split<Split<256, 1, 8, 4>, T>(a, workspace, sms, st);
+}
+
+}  // namespace
+
+size_t kv_split_workspace() {
+    return std::max(std::max(part_bytes<Split<64, 2, 16, 8>>(), part_bytes<Split<128, 2, 12, 4>>()),
+                    part_bytes<Split<256, 1, 8, 4>>()) + kMaxCtas * sizeof(Meta);
+}
+
+int launch_kv_split(const KvAttend &a, int head_dim, int dtype, void *workspace, int sms, cudaStream_t st) {
+    if (dtype == DSQ_DTYPE_F16) return launch_of<__half>(a, head_dim, workspace, sms, st);
+    return launch_of<__nv_bfloat16>(a, head_dim, workspace, sms, st);
+}
+
+}  // namespace dsq
