@@ -5,6 +5,7 @@
 #include <new>
 #include <vector>
 
+#include "device_guard.h"
 #include "internal.h"
 
 using namespace dsq;

@@ -83,20 +83,6 @@ struct dsq_handle_s {
 
 namespace dsq {
 
-// Makes `device` current for the scope and restores the caller's device.
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = false;
-    explicit DeviceGuard(int device) {
-        if (cudaGetDevice(&prev) != cudaSuccess) return;
-        ok = prev == device || cudaSetDevice(device) == cudaSuccess;
-    }
-    ~DeviceGuard() {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
-
 // Launchers; each returns a dsq_status and never synchronises.
 int launch_gemv_generic(const dsq_handle_s *h, const __half *x, __half *y, int batch,
                         cudaStream_t stream);

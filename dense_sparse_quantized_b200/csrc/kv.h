@@ -8,6 +8,7 @@
 
 #include <atomic>
 
+#include "device_guard.h"
 #include "internal.h"
 
 namespace dsq {
@@ -111,5 +112,9 @@ struct KvOnce {
 // Few query rows per sequence (kv_split.cu).
 size_t kv_split_workspace();
 int launch_kv_split(const KvAttend &a, int head_dim, int dtype, void *workspace, int sms, cudaStream_t stream);
+
+// Many query rows per sequence (kv_prompt.cu).
+size_t kv_prompt_workspace(int head_dim);
+int launch_kv_prompt(const KvAttend &a, int head_dim, int dtype, void *workspace, int sms, cudaStream_t stream);
 
 }  // namespace dsq

@@ -14,6 +14,12 @@ int sm_count(int device) {
     return n;
 }
 
+// Rows of a job, on average: query tokens of a sequence times the heads of a
+// group.
+bool many_rows(const dsq_kv_desc *d, const dsq_kv_queries *a) {
+    return a->batch > 0 && a->q_tokens / a->batch * (a->q_heads / d->kv_heads) > 16;
+}
+
 }  // namespace
 
 extern "C" int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_kv_queries *a, void *workspace,
@@ -29,7 +35,8 @@ extern "C" int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_
     if (a->batch > 0 && !a->q_start && a->q_tokens % a->batch) return DSQ_ERR_INVALID_ARG;
     if ((int64_t)a->table_pages * d->page_tokens >= ((int64_t)1 << 31) || a->q_tokens * a->q_heads >= ((int64_t)1 << 31))
         return DSQ_ERR_UNSUPPORTED;
-    const size_t need = kv_split_workspace();
+    const bool many = many_rows(d, a);
+    const size_t need = many ? kv_prompt_workspace(d->head_dim) : kv_split_workspace();
     if (!workspace || *workspace_bytes < need) {
         *workspace_bytes = need;
         return DSQ_ERR_BUFFER_TOO_SMALL;
@@ -65,5 +72,7 @@ extern "C" int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_
     k.page_table = a->page_table;
     k.kv_lens = a->kv_lens;
     k.q_start = a->q_start;
-    return launch_kv_split(k, d->head_dim, a->dtype, workspace, sm_count(d->device), (cudaStream_t)stream);
+    const int sms = sm_count(d->device);
+    return many ? launch_kv_prompt(k, d->head_dim, a->dtype, workspace, sms, (cudaStream_t)stream)
+                : launch_kv_split(k, d->head_dim, a->dtype, workspace, sms, (cudaStream_t)stream);
 }

@@ -1,0 +1,719 @@
+// kv_prompt.cu -- attention over the 4-bit cache for many query rows per
+// sequence (prompts, drafts checked at once): bound by matrix products and
+// exponentials, so both products run on tcgen05.
+//
+// Work.  A job is (sequence, kv head, tile of R query rows), a row being one
+// (query token, query head of the group) pair.  Its tokens are cut into units
+// of 128, of which only those that some row sees count; the units of all
+// jobs, in order, are dealt to the CTAs in equal runs, wherever jobs begin and
+// end.  What a job's runs leave is joined through the workspace, in order.
+//
+// A CTA works on two row tiles of 128 at once (one at 256 dimensions), so that
+// one tile's products run under the other's softmax:
+//   warps 0-3, 4-7  softmax of row tile 0, 1: thread = row.  Reads its 128
+//                   scores from tensor memory, raises the running maximum if
+//                   one exceeds it by more than 2^8 in the numerator (then the
+//                   output so far is rescaled in tensor memory), writes the
+//                   numerators back as fp16 over the scores.
+//   warps 8-11      bring K and V: codes from global memory to registers a
+//                   unit ahead, unpacked exactly to fp16 (kv_device.h) into the
+//                   128-byte-swizzled tiles of a ring in shared memory.  Eight
+//                   dimensions come out as 0 4 1 5 2 6 3 7; the queries are
+//                   stored in that order, the output's columns renamed.
+//   warp 12         one thread issues the products: S = Q K^T (K-major), then
+//                   O += P V with P from tensor memory and V token-major
+//                   (MN-major B).
+// Unit t + 1's scores of a row tile are issued after unit t's output product
+// of the same tile, so the commit that announces them also says that this
+// product is done, and the output may be rescaled.
+//
+// Tokens that no row of the job sees get scale 0, whatever the cache holds
+// there.  A NaN among the values would reach every row of the unit through
+// the product, so its scale becomes 0 too and the rows that see the token get
+// a NaN numerator; which tokens these are, and pages that do not exist, goes
+// beside the tiles in `flags`.
+//
+// Every mbarrier wait is bounded (ptx.h); one that runs out ends its role, the
+// others' waits run out in turn, and the CTA frees its tensor memory and
+// returns.
+#include <algorithm>
+
+#include "kv_device.h"
+#include "ptx.h"
+
+namespace dsq {
+
+namespace {
+
+constexpr int kN = 128;          // tokens of a unit
+constexpr int kBlk = 128 * 128;  // bytes of 128 rows x 64 dimensions, swizzled
+constexpr int kThreads = 512;
+constexpr int kFlags = 4;        // units whose flags are kept
+
+template <int D_>
+struct Shape {
+    static constexpr int D = D_;
+    static constexpr int A = D == 256 ? 1 : 2;       // row tiles at once: 128 (A + D / 128) columns of tensor memory each
+    static constexpr int R = 128 * A;
+    static constexpr int kStages = D == 256 ? 1 : 2; // K and V tiles in the ring
+    static constexpr int kTile = D / 64 * kBlk;      // bytes of 128 rows
+    static constexpr int kSmem = (A + 2 * kStages) * kTile + 1024;
+    static constexpr int kO = A * 128;               // first column of the outputs
+    static constexpr int kChunks = D == 64 ? 2 : 4;  // of 16 bytes that a thread moves at a time
+    static constexpr int kItems = D == 256 ? 2 : 1;  // times per K or V tile
+};
+
+struct PromptParams {
+    KvAttend a;
+    float *parts;
+    KvCarry *carries;
+};
+
+struct Shared {
+    uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], qfull[2], ofull[2];
+    uint4 nans[kFlags], holes[kFlags];  // by loading warp: NaN tokens; sub-tiles without a page
+    uint32_t tmem;
+    int b, head, qt, first;  // where this CTA's run begins
+    int64_t left, run, end;  // units of it; of every CTA's; its end among all units
+};
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t at, float *v) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; i++) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A B, fp16, fp32 accumulator; A from shared or tensor memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(0u)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %5, %5}, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(0u)
+        : "memory");
+}
+
+// Shared-memory operand of 128-byte rows, 128-byte swizzle, groups of eight
+// rows 1024 bytes apart.  K-major: a row is one of M or N, 64 elements of k.
+// MN-major: a row is one k, 64 elements of N, the next 64 of N kBlk bytes on.
+__device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t leading) {
+    return ((uint64_t)(at >> 4) & 0x3fffu) | ((uint64_t)(leading >> 4) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+constexpr uint32_t instruction(int n, bool b_mn_major) {
+    return (1u << 4) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// Units [x, y) of a row tile's job: at least one, so that every row is written.
+template <int R>
+__device__ __forceinline__ int2 units_of(const KvAttend &a, const KvSeq &s, int qt) {
+    const int last = min((qt + 1) * R, s.rows * a.share) - 1;
+    const int lo = seen_by(a, s, qt * R).x / kN, hi = (max(seen_by(a, s, last).y, 0) + kN - 1) / kN;
+    return make_int2(lo, max(hi, lo + 1));
+}
+template <int R>
+__device__ __forceinline__ int tiles_of(const KvAttend &a, const KvSeq &s) {
+    return (int)(((int64_t)s.rows * a.share + R - 1) / R);
+}
+
+// A piece of a CTA's run: units [t0, t1) of one job.
+struct Piece {
+    KvSeq s;
+    int b, head, qt, t0, t1, rest;  // rest: the job's units behind t1
+    bool begins;
+};
+template <int R>
+struct Walk {
+    int b, head, qt, first;
+    int64_t left;
+    __device__ __forceinline__ explicit Walk(const Shared &sh) : b(sh.b), head(sh.head), qt(sh.qt), first(sh.first), left(sh.left) {}
+    __device__ __forceinline__ bool next(const KvAttend &a, Piece &p) {
+        while (left > 0 && b < a.batch) {
+            p.s = kv_seq(a, b);
+            const int tiles = tiles_of<R>(a, p.s);
+            if (qt >= tiles) {
+                qt = 0;
+                if (tiles == 0 || ++head >= a.c.kv_heads) {
+                    head = 0;
+                    b++;
+                }
+                continue;
+            }
+            const int2 u = units_of<R>(a, p.s, qt);
+            p.b = b;
+            p.head = head;
+            p.qt = qt;
+            p.t0 = u.x + first;
+            p.t1 = (int)min((int64_t)u.y, p.t0 + left);
+            p.rest = u.y - p.t1;
+            p.begins = first == 0;
+            left -= p.t1 - p.t0;
+            first = 0;
+            qt++;
+            return true;
+        }
+        return false;
+    }
+};
+
+// Units of the piece that row tile r of it works on: none if it has no rows.
+template <int R>
+__device__ __forceinline__ int2 active(const KvAttend &a, const Piece &p, int r) {
+    const int first = p.qt * R + 128 * r, last = min(min(first + 128, (p.qt + 1) * R), p.s.rows * a.share) - 1;
+    if (first > last) return make_int2(p.t0, p.t0);
+    const int lo = max(p.t0, seen_by(a, p.s, first).x / kN);
+    return make_int2(lo, max(lo, min(p.t1, (max(seen_by(a, p.s, last).y, 0) + kN - 1) / kN)));
+}
+
+// Finds this CTA's run (one warp).
+template <int R>
+__device__ __forceinline__ void find_run(const KvAttend &a, Shared &sh) {
+    const int lane = threadIdx.x & 31;
+    auto head_units = [&](int b) -> int64_t {  // of one kv head of sequence b
+        const KvSeq s = kv_seq(a, b);
+        const int tiles = tiles_of<R>(a, s);
+        int64_t n = 0;
+        for (int qt = 0; qt < tiles; qt++) {
+            const int2 u = units_of<R>(a, s, qt);
+            n += u.y - u.x;
+        }
+        return n;
+    };
+    auto scan = [&](int64_t w) {
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int64_t up = __shfl_up_sync(kFull, w, m);
+            if (lane >= m) w += up;
+        }
+        return w;
+    };
+    int64_t total = 0;
+    for (int b = lane; b < a.batch; b += 32) total += head_units(b) * a.c.kv_heads;
+#pragma unroll
+    for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(kFull, total, m);
+    const int64_t run = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t u0 = min(total, run * blockIdx.x), u1 = min(total, u0 + run);
+    int64_t before = 0;
+    int b = a.batch, head = 0, qt = 0, first = 0;
+    for (int b0 = 0; b0 < a.batch && u0 < u1; b0 += 32) {
+        const int64_t w = b0 + lane < a.batch ? head_units(b0 + lane) : 0, sum = scan(w * a.c.kv_heads);
+        const uint32_t past = __ballot_sync(kFull, before + sum > u0);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            b = b0 + l;
+            before += __shfl_sync(kFull, sum - w * a.c.kv_heads, l);
+            const int64_t per_head = max((int64_t)1, __shfl_sync(kFull, w, l));
+            head = (int)((u0 - before) / per_head);
+            before += head * per_head;
+            break;
+        }
+        before += __shfl_sync(kFull, sum, 31);
+    }
+    if (b < a.batch) {
+        const KvSeq s = kv_seq(a, b);
+        const int tiles = tiles_of<R>(a, s);
+        for (int q0 = 0; q0 < tiles; q0 += 32) {
+            int w = 0;
+            if (q0 + lane < tiles) {
+                const int2 u = units_of<R>(a, s, q0 + lane);
+                w = u.y - u.x;
+            }
+            const int64_t sum = scan(w);
+            const uint32_t past = __ballot_sync(kFull, before + sum > u0);
+            if (past) {
+                const int l = __ffs(past) - 1;
+                qt = q0 + l;
+                first = (int)(u0 - before - __shfl_sync(kFull, sum - w, l));
+                break;
+            }
+            before += __shfl_sync(kFull, sum, 31);
+        }
+    }
+    if (lane == 0) {
+        sh.b = b;
+        sh.head = head;
+        sh.qt = qt;
+        sh.first = first;
+        sh.left = u1 - u0;
+        sh.run = run;
+        sh.end = u1;
+    }
+}
+
+// ------------------------------------------------------------ warps 8-11
+template <int D>
+struct Loader {
+    using S = Shape<D>;
+    static constexpr int CH = S::kChunks;
+    const KvAttend &a;
+    Walk<S::R> walk;
+    Piece p;
+    int t;
+    bool more;
+    const int lane, warp, tok, pair;
+
+    // A unit on its way: its pages, then its addresses.
+    struct Unit {
+        bool there;
+        int lo, hi;       // tokens of the unit that some row sees
+        int page[2], in_page[2], head;
+    };
+    __device__ __forceinline__ Loader(const KvAttend &a_, const Shared &sh)
+        : a(a_), walk(sh), lane(threadIdx.x & 31), warp((threadIdx.x >> 5) & 3), tok(lane >> 1), pair(lane & 1) {
+        more = walk.next(a, p);
+        t = p.t0;
+    }
+    __device__ __forceinline__ Unit next() {
+        Unit u = {};
+        u.there = more;
+        if (!more) return u;
+        const int last = min((p.qt + 1) * S::R, p.s.rows * a.share) - 1;
+        u.lo = seen_by(a, p.s, p.qt * S::R).x - t * kN;
+        u.hi = seen_by(a, p.s, last).y - t * kN;
+        u.head = p.head;
+        const int32_t *row = a.page_table + (int64_t)p.b * a.table_pages;
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const int tile = t * (kN / kKvTile) + 2 * warp + i, col = tile / a.c.page_tiles;
+            u.in_page[i] = tile - col * a.c.page_tiles;
+            u.page[i] = col < a.table_pages && u.hi > (2 * warp + i) * kKvTile ? row[col] : -1;
+        }
+        if (++t == p.t1) {
+            more = walk.next(a, p);
+            t = p.t0;
+        }
+        return u;
+    }
+    __device__ __forceinline__ static int group(int item, int c, int pair) {
+        return D == 64 ? pair : 2 * (2 * item + (c & 1)) + pair;
+    }
+    __device__ __forceinline__ static int sub(int c) { return D == 64 ? c : c >> 1; }
+    // Loads one item (which: K or V) of the unit into x and its words into w;
+    // with the keys also the values' words, into nan, for their NaNs.
+    __device__ __forceinline__ void load(const Unit &u, int which, int item, uint4 (&x)[CH], uint32_t (&w)[CH], bool (&nan)[CH]) const {
+#pragma unroll
+        for (int c = 0; c < CH; c++) {
+            const int i = sub(c), g = group(item, c, pair), at = (2 * warp + i) * kKvTile + tok;
+            const int page = u.page[i];
+            x[c] = make_uint4(0, 0, 0, 0);
+            w[c] = 0;
+            nan[c] = false;
+            if (u.there && (uint32_t)page < (uint32_t)a.c.pages && at >= u.lo && at < u.hi) {
+                const uint8_t *tile =
+                    a.c.cache + (((int64_t)page * a.c.kv_heads + u.head) * a.c.page_tiles + u.in_page[i]) * kv_tile_bytes(D);
+                x[c] = *reinterpret_cast<const uint4 *>(tile + kv_codes(D, which) + tok * (D / 2) + g * 16);
+                w[c] = *reinterpret_cast<const uint16_t *>(tile + kv_words(D, which) + (g * kKvTile + tok) * 2);
+                if (which == 0)
+                    nan[c] = (*reinterpret_cast<const uint16_t *>(tile + kv_words(D, 1) + (g * kKvTile + tok) * 2) & 0x7c00u) == 0x7c00u;
+            }
+        }
+    }
+    // Unpacks an item into the tile at `to`.
+    __device__ __forceinline__ void store(uint32_t to, int which, int item, const uint4 (&x)[CH], const uint32_t (&w)[CH]) const {
+#pragma unroll
+        for (int c = 0; c < CH; c++) {
+            const int g = group(item, c, pair), at = (2 * warp + sub(c)) * kKvTile + tok;
+            const uint32_t word = which == 1 && (w[c] & 0x7c00u) == 0x7c00u ? 0u : w[c];
+            const Decode d(prmt(word, word, 0x1010));
+            const uint32_t row = to + (g >> 1) * kBlk + at * 128;
+            const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const uint32_t y = v[i] >> 8;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((((g & 1) * 4 + i) ^ (at & 7)) << 4)),
+                             "r"(d.low(v[i])), "r"(d.high(v[i])), "r"(d.low(y)), "r"(d.high(y))
+                             : "memory");
+            }
+        }
+    }
+};
+
+template <int D>
+__device__ __forceinline__ void load_role(const KvAttend &a, Shared &sh, uint32_t kbuf, uint32_t vbuf) {
+    using S = Shape<D>;
+    constexpr int CH = S::kChunks, N = S::kItems;
+    Loader<D> ld(a, sh);
+    typename Loader<D>::Unit u = ld.next(), u1 = ld.next();
+    uint4 x[2][CH];      // items by turns: the keys' and the values' at 128 dimensions and below
+    uint32_t w[2][CH];
+    bool nan[2][CH];
+    ld.load(u, 0, 0, x[0], w[0], nan[0]);
+    ld.load(u, N == 2 ? 0 : 1, N == 2 ? 1 : 0, x[1], w[1], nan[1]);
+    for (uint32_t it = 0; u.there; it++) {
+        const typename Loader<D>::Unit u2 = ld.next();
+        const uint32_t stage = it % S::kStages, phase = it / S::kStages & 1;
+        // keys, and the flags of the unit
+        if (!mbar_wait_warp(&sh.kempty[stage], phase ^ 1)) return;
+        uint32_t bad = 0;
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+#pragma unroll
+            for (int c = 0; c < CH; c++)
+                if (__any_sync(kFull, nan[i][c])) {
+                    uint32_t two = __ballot_sync(kFull, nan[i][c]);  // two lanes a token
+                    two |= two >> 1;
+                    uint32_t bits = 0;
+                    for (int k = 0; k < 16; k++) bits |= (two >> (2 * k) & 1u) << k;
+                    bad |= bits << (16 * Loader<D>::sub(c));
+                }
+            ld.store(kbuf + stage * S::kTile, 0, i, x[i], w[i]);
+            if (N == 2) ld.load(u, 1, i, x[i], w[i], nan[i]);
+        }
+        if (ld.lane == 0) {
+            reinterpret_cast<uint32_t *>(&sh.nans[it % kFlags])[ld.warp] = bad;
+            reinterpret_cast<uint32_t *>(&sh.holes[it % kFlags])[ld.warp] =
+                (uint32_t)((uint32_t)u.page[0] >= (uint32_t)a.c.pages) | (uint32_t)((uint32_t)u.page[1] >= (uint32_t)a.c.pages) << 1;
+        }
+        fence_async();
+        __syncwarp();
+        if (ld.lane == 0) mbar_arrive(&sh.kfull[stage]);
+        if (N == 1) ld.load(u1, 0, 0, x[0], w[0], nan[0]);
+        // values
+        if (!mbar_wait_warp(&sh.vempty[stage], phase ^ 1)) return;
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            ld.store(vbuf + stage * S::kTile, 1, i, x[N == 2 ? i : 1], w[N == 2 ? i : 1]);
+            if (N == 2) ld.load(u1, 0, i, x[i], w[i], nan[i]);
+        }
+        fence_async();
+        __syncwarp();
+        if (ld.lane == 0) mbar_arrive(&sh.vfull[stage]);
+        if (N == 1) ld.load(u1, 1, 0, x[1], w[1], nan[1]);
+        u = u1;
+        u1 = u2;
+    }
+}
+
+// ---------------------------------------------------------------- warp 12
+template <int D>
+__device__ __forceinline__ void product_role(const KvAttend &a, Shared &sh, uint32_t qbuf, uint32_t kbuf, uint32_t vbuf) {
+    using S = Shape<D>;
+    constexpr uint32_t kScores = instruction(kN, false), kOut = instruction(D, true);
+    const uint32_t tmem = sh.tmem;
+    Walk<S::R> walk(sh);
+    Piece p;
+    uint32_t it = 0, pn[2] = {0, 0}, qn[2] = {0, 0};
+    while (walk.next(a, p)) {
+        int2 on[S::A];
+#pragma unroll
+        for (int r = 0; r < S::A; r++) on[r] = active<S::R>(a, p, r);
+        auto scores = [&](int r, uint32_t stage) {
+#pragma unroll
+            for (int k = 0; k < D / 16; k++) {
+                const uint32_t at = k / 4 * kBlk + k % 4 * 32;
+                mma_ss(tmem + 128 * r, operand(qbuf + r * S::kTile + at, 16), operand(kbuf + stage * S::kTile + at, 16), kScores, k > 0);
+            }
+            commit(&sh.sfull[r]);
+        };
+#pragma unroll
+        for (int r = 0; r < S::A; r++)
+            if (on[r].x < on[r].y && !mbar_wait(&sh.qfull[r], qn[r]++ & 1)) return;
+        if (!mbar_wait(&sh.kfull[it % S::kStages], it / S::kStages & 1)) return;
+        fence_after();
+#pragma unroll
+        for (int r = 0; r < S::A; r++)
+            if (on[r].x == p.t0 && on[r].x < on[r].y) scores(r, it % S::kStages);
+        commit(&sh.kempty[it % S::kStages]);
+        for (int t = p.t0; t < p.t1; t++, it++) {
+            const uint32_t stage = it % S::kStages, next = (it + 1) % S::kStages;
+            if (!mbar_wait(&sh.vfull[stage], it / S::kStages & 1)) return;
+            bool got = false;
+#pragma unroll
+            for (int r = 0; r < S::A; r++) {
+                if (t >= on[r].x && t < on[r].y) {
+                    if (!mbar_wait(&sh.pfull[r], pn[r]++ & 1)) return;
+                    fence_after();
+#pragma unroll
+                    for (int k = 0; k < kN / 16; k++)
+                        mma_ts(tmem + S::kO + D * r, tmem + 128 * r + 8 * k, operand(vbuf + stage * S::kTile + k * 2048, kBlk), kOut,
+                               k > 0 || t > on[r].x);
+                    if (t == on[r].y - 1) commit(&sh.ofull[r]);
+                }
+                if (r == S::A - 1) commit(&sh.vempty[stage]);
+                if (t + 1 < p.t1) {
+                    if (!got) {
+                        if (!mbar_wait(&sh.kfull[next], (it + 1) / S::kStages & 1)) return;
+                        fence_after();
+                        got = true;
+                    }
+                    if (t + 1 >= on[r].x && t + 1 < on[r].y) scores(r, next);
+                    if (r == S::A - 1) commit(&sh.kempty[next]);
+                }
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------- warps 0-7
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+template <int D, typename T>
+__device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh, uint32_t qbuf, int r) {
+    using S = Shape<D>;
+    const KvAttend &a = pp.a;
+    const int row = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)(row & 96) << 16;  // this warp's quarter of tensor memory
+    const uint32_t st = sh.tmem + 128 * r + lanes, ot = sh.tmem + S::kO + D * r + lanes;
+    Walk<S::R> walk(sh);
+    Piece p;
+    uint32_t it0 = 0, sn = 0, on = 0;
+    while (walk.next(a, p)) {
+        const int2 mine = active<S::R>(a, p, r);
+        const int first = p.qt * S::R + 128 * r, rho = first + row;
+        const int end = min(first + 128, p.s.rows * a.share);
+        float m = kNoMax, l = 0.0f, o_scale = 0.0f;
+        if (mine.x < mine.y) {
+            const int my = min(rho, end - 1);
+            const int2 seen = seen_by(a, p.s, my), all = make_int2(seen_by(a, p.s, end - 1).x, seen_by(a, p.s, first).y);
+            // The queries, into the tile's rows.  A negative scale is the
+            // queries' sign, so that the largest score stays the largest.
+            float f = fabsf(a.scale_log2);
+            {
+                const T *src = (const T *)a.q + row_at(a, p.s, p.head, my, a.q_token, a.q_head);
+                const uint32_t sign = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+                const int up = query_exponent<T, D>(src);
+                f = fmaxf(f * exponent(-up), 1.17549435e-38f);  // not 0: a masked score times it is to stay -inf
+#pragma unroll 2
+                for (int i = 0; i < D / 8; i++) {
+                    uint4 x[1] = {reinterpret_cast<const uint4 *>(src)[i]};
+                    query_codes_order<T, 1>(x, up);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     qbuf + r * S::kTile + i / 8 * kBlk + row * 128 + (((i & 7) ^ (row & 7)) << 4)),
+                                 "r"(x[0].x ^ sign), "r"(x[0].y ^ sign), "r"(x[0].z ^ sign), "r"(x[0].w ^ sign)
+                                 : "memory");
+                }
+            }
+            fence_async();
+            fence_before();
+            mbar_arrive(&sh.qfull[r]);
+
+            for (int t = mine.x; t < mine.y; t++) {
+                if (!mbar_wait_warp(&sh.sfull[r], sn++ & 1)) return;
+                fence_after();
+                float s[kN];
+#pragma unroll
+                for (int i = 0; i < kN; i += 32) tmem_ld32(st + i, s + i);
+                const uint32_t flag = (it0 + t - p.t0) % kFlags;
+                const uint4 nans = sh.nans[flag], holes = sh.holes[flag];
+                wait_ld();
+                const int lo = seen.x - t * kN, hi = seen.y - t * kN;
+                if (all.x > t * kN || all.y < (t + 1) * kN || (nans.x | nans.y | nans.z | nans.w | holes.x | holes.y | holes.z | holes.w)) {
+                    const uint32_t hole = holes.x | holes.y << 2 | holes.z << 4 | holes.w << 6;
+                    const uint32_t nan[4] = {nans.x, nans.y, nans.z, nans.w};
+#pragma unroll
+                    for (int i = 0; i < kN; i++) {
+                        if (i < lo || i >= hi || (hole >> (i / 16) & 1u)) s[i] = -INFINITY;
+                        else if (nan[i / 32] >> (i % 32) & 1u) s[i] = NAN;
+                    }
+                }
+                float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int i = 4; i < kN; i += 8)
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        top[k] = i + 4 + k < kN ? max3(top[k], s[i + k], s[i + 4 + k]) : fmaxf(top[k], s[i + k]);
+                const float x = fmaxf(max3(top[0], top[1], top[2]), top[3]) * f;
+                if (__any_sync(kFull, x > m + kLazy)) {
+                    const float next = fmaxf(m, x), keep = ex2(m - next);
+                    m = next;
+                    l *= keep;
+                    if (t > mine.x) {
+#pragma unroll 1
+                        for (int i = 0; i < D; i += 32) {
+                            float o[32];
+                            tmem_ld32(ot + i, o);
+                            wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 32; k++) o[k] *= keep;
+                            tmem_st32(ot + i, reinterpret_cast<const uint32_t *>(o));
+                        }
+                    }
+                }
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < kN; i += 64) {
+                    uint32_t ph[32];
+#pragma unroll
+                    for (int k = 0; k < 32; k++) {
+                        const float p0 = ex2(fmaf(s[i + 2 * k], f, -m)), p1 = ex2(fmaf(s[i + 2 * k + 1], f, -m));
+                        sum[2 * k % 4] += p0;
+                        sum[(2 * k + 1) % 4] += p1;
+                        ph[k] = pack_h2(p0, p1);
+                    }
+                    tmem_st32(st + i / 2, ph);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                wait_st();
+                fence_before();
+                mbar_arrive(&sh.pfull[r]);
+            }
+            if (!mbar_wait_warp(&sh.ofull[r], on++ & 1)) return;
+            fence_after();
+            o_scale = 1.0f;
+        }
+        it0 += p.t1 - p.t0;
+
+        // The rows' outputs, or the piece's partial result.
+        const bool whole = p.begins && p.rest == 0;
+        float *part = pp.parts + (2 * blockIdx.x + (p.begins ? 1 : 0)) * kv_part_floats<D, S::R>();
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        T *dst = (T *)a.out + (rho < end ? row_at(a, p.s, p.head, rho, a.out_token, a.out_head) : 0);
+#pragma unroll 1
+        for (int i = 0; i < D; i += 32) {
+            float o[32];
+            if (o_scale != 0.0f) {
+                tmem_ld32(ot + i, o);
+                wait_ld();
+            } else {
+#pragma unroll
+                for (int k = 0; k < 32; k++) o[k] = 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+                // columns k .. k + 7 are dimensions 0 4 1 5 2 6 3 7
+                if (whole) {
+                    if (rho < end)
+                        *reinterpret_cast<uint4 *>(dst + i + k) =
+                            make_uint4(pack_out<T>(o[k] * inv, o[k + 2] * inv), pack_out<T>(o[k + 4] * inv, o[k + 6] * inv),
+                                       pack_out<T>(o[k + 1] * inv, o[k + 3] * inv), pack_out<T>(o[k + 5] * inv, o[k + 7] * inv));
+                } else {
+                    float4 *to = reinterpret_cast<float4 *>(part + (128 * r + row) * D + i + k);
+                    to[0] = make_float4(o[k], o[k + 2], o[k + 4], o[k + 6]);
+                    to[1] = make_float4(o[k + 1], o[k + 3], o[k + 5], o[k + 7]);
+                }
+            }
+        }
+        if (whole) {
+            if (a.lse && rho < end) a.lse[row_at(a, p.s, p.head, rho, a.q_heads, 1)] = lse_of(m, l);
+        } else {
+            part[S::R * D + 128 * r + row] = m;
+            part[S::R * D + S::R + 128 * r + row] = l;
+            if (p.begins && r == 0 && row == 0) {
+                const KvCarry c = {1, (int)((sh.end + p.rest - 1) / sh.run) - (int)blockIdx.x, p.b, p.head, p.qt, {}};
+                pp.carries[blockIdx.x] = c;
+            }
+        }
+        fence_before();
+    }
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ PromptParams pp) {
+    using S = Shape<D>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Shared sh;
+    const uint32_t qbuf = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t kbuf = qbuf + S::A * S::kTile, vbuf = kbuf + S::kStages * S::kTile;
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&sh.kfull[i], 4);
+            mbar_init(&sh.vfull[i], 4);
+            mbar_init(&sh.kempty[i], 1);
+            mbar_init(&sh.vempty[i], 1);
+            mbar_init(&sh.sfull[i], 1);
+            mbar_init(&sh.ofull[i], 1);
+            mbar_init(&sh.pfull[i], 128);
+            mbar_init(&sh.qfull[i], 128);
+        }
+        fence_mbar_init();
+        pp.carries[blockIdx.x].valid = 0;
+    }
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else if (warp == 8)
+        find_run<S::R>(pp.a, sh);
+    fence_before();
+    __syncthreads();
+    fence_after();
+
+    // 512 threads x 128 registers: 2 x 184 + 96 + 48 for the four warpgroups.
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        if (warp < 4 * S::A) softmax_role<D, T>(pp, sh, qbuf, warp >> 2);
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        load_role<D>(pp.a, sh, kbuf, vbuf);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (threadIdx.x == 12 * 32) product_role<D>(pp.a, sh, qbuf, kbuf, vbuf);
+        __syncwarp();
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem), "r"(512) : "memory");
+    }
+}
+
+template <int D, typename T>
+int launch_prompt(const KvAttend &a, void *workspace, int sms, cudaStream_t st) {
+    using S = Shape<D>;
+    const PromptParams p = {a, (float *)workspace, kv_carries<D, S::R>(workspace)};
+    auto kernel = prompt_kernel<D, T>;
+    static KvOnce once;
+    if (!once.set_smem((const void *)kernel, S::kSmem)) return DSQ_ERR_CUDA;
+    const int grid = std::min(sms, kMaxCtas);
+    kernel<<<grid, kThreads, S::kSmem, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return DSQ_ERR_CUDA;
+    return launch_join<D, S::R, T>(a, p.parts, p.carries, grid, st);
+}
+
+template <typename T>
+int launch_of(const KvAttend &a, int head_dim, void *workspace, int sms, cudaStream_t st) {
+    if (head_dim == 64) return launch_prompt<64, T>(a, workspace, sms, st);
+    if (head_dim == 128) return launch_prompt<128, T>(a, workspace, sms, st);
+    return launch_prompt<256, T>(a, workspace, sms, st);
+}
+
+}  // namespace
+
+size_t kv_prompt_workspace(int head_dim) {
+    return head_dim == 64 ? kv_parts_bytes<64, Shape<64>::R>() : head_dim == 128 ? kv_parts_bytes<128, Shape<128>::R>()
+                                                                                 : kv_parts_bytes<256, Shape<256>::R>();
+}
+
+int launch_kv_prompt(const KvAttend &a, int head_dim, int dtype, void *workspace, int sms, cudaStream_t st) {
+    if (dtype == DSQ_DTYPE_F16) return launch_of<__half>(a, head_dim, workspace, sms, st);
+    return launch_of<__nv_bfloat16>(a, head_dim, workspace, sms, st);
+}
+
+}  // namespace dsq

@@ -14,7 +14,7 @@
 // A warp runs through its units alone, with a running maximum and sum.  A job
 // inside one warp's run is written at once.  What spans warps of a CTA is
 // merged in shared memory at the end, what spans CTAs through the workspace by
-// combine_kernel, always in the same order.
+// join_kernel, always in the same order.
 //
 // A unit.  Two tiles of 16 tokens, brought to the warp's own ring in shared
 // memory by cp.async of whole tiles.  Scores: mma.sync m16n8k16 with the 16
@@ -35,17 +35,12 @@
 // as exact as ones up to 1.
 #include <algorithm>
 
-#include "kv.h"
+#include "kv_device.h"
 #include "ptx.h"
 
 namespace dsq {
 
 namespace {
-
-constexpr float kNoMax = -3.0e38f;  // a maximum of no scores: finite, so that -inf minus it stays -inf
-constexpr float kLazy = 8.0f;       // log2 of how far numerators may pass 1
-constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kMaxCtas = 160;       // workspace slots; the grid is one CTA per SM, at most this
 
 // A tiling: head dimension, tiles of eight query rows, warps of a CTA, tiles
 // of a warp's ring.  Shared memory of a warp: the ring, whose space takes the
@@ -61,34 +56,13 @@ struct Split {
     static_assert(RING * kTile >= kPart && RING % 2 == 0 && kSmem <= 224 * 1024, "shared memory of a CTA");
 };
 
-// What a CTA leaves for combine_kernel: the job that begins in its run and
-// goes on in `more` further CTAs.
-struct Meta {
-    int valid, more, b, head, qt, pad[3];
-};
-
 struct SplitParams {
     KvAttend a;
-    float *part;  // [CTA][first, last][R][D], then [CTA][2][R] maxima and sums
-    Meta *meta;   // [CTA]
+    float *parts;
+    KvCarry *carries;
     int min_run;  // least units of a CTA's run
 };
 
-__device__ __forceinline__ uint32_t lop_magic(uint32_t w, uint32_t mask, uint32_t magic) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));  // (w & mask) | magic
-    return r;
-}
-__device__ __forceinline__ uint32_t hadd2u(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -101,35 +75,6 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t a) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
     return r;
 }
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-    uint32_t r;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-// Scale and zero of a pair of codes: two fp16 scales, and minus 1024 plus
-// zero (for codes at the bottom of the halves) or minus 64 plus zero.
-struct Decode {
-    uint32_t s, z1024, z64;
-    __device__ __forceinline__ explicit Decode(uint32_t words) {
-        s = words & 0xfff0fff0u;
-        z1024 = lop_magic(words, 0x000f000fu, 0xe400e400u);
-        z64 = hadd2u(z1024, 0x63806380u);  // + 960
-    }
-    // Codes 0, 1 of each half of w (bits 0-3 and 4-7).
-    __device__ __forceinline__ uint32_t low(uint32_t w) const {
-        return hmul2u(hadd2u(lop_magic(w, 0x000f000fu, 0x64006400u), z1024), s);
-    }
-    __device__ __forceinline__ uint32_t high(uint32_t w) const {
-        return hmul2u(hadd2u(lop_magic(w, 0x00f000f0u, 0x54005400u), z64), s);
-    }
-};
-
 // Where 16-byte chunk c of a token's row of codes goes in a ring tile, such
 // that the fragment loads below meet no bank twice.  Keys: the rows in the
 // order of M; values: rows t at t / 4 + 4 (t % 4).
@@ -157,52 +102,20 @@ __device__ __forceinline__ void issue_tile(uint32_t dst, const uint8_t *src, int
     if (lane < kWords) cp_async16(dst + kv_words(D, 0) + lane * 16, src + kv_words(D, 0) + lane * 16);
 }
 
-// Job numbers of a sequence.
-struct Jobs {
-    int rows, len, lo, units, tiles;  // query rows, tokens, first token any query sees, units of a job, row tiles
-    int64_t row0, weight;             // first row; units of all the sequence's jobs
+// The jobs of a sequence.
+struct Jobs : KvSeq {
+    int lo, units, tiles;  // first token any query sees, units of a job, row tiles
+    int64_t weight;        // units of all of the sequence's jobs
 };
 template <int R>
 __device__ __forceinline__ Jobs jobs_of(const KvAttend &a, int b) {
-    const KvSeq s = kv_seq(a, b);
     Jobs j;
-    j.rows = s.rows;
-    j.len = s.len;
-    j.row0 = s.row0;
-    j.lo = a.window ? max(0, s.len - s.rows - a.window + 1) : 0;
-    j.units = max(1, (s.len + 31) / 32 - j.lo / 32);
-    j.tiles = (int)(((int64_t)s.rows * a.share + R - 1) / R);
+    static_cast<KvSeq &>(j) = kv_seq(a, b);
+    j.lo = a.window ? max(0, j.len - j.rows - a.window + 1) : 0;
+    j.units = max(1, (j.len + 31) / 32 - j.lo / 32);
+    j.tiles = (int)(((int64_t)j.rows * a.share + R - 1) / R);
     j.weight = (int64_t)a.c.kv_heads * j.tiles * j.units;
     return j;
-}
-
-// The 16-bit rows of q and out.
-template <typename T>
-struct Pair;
-template <>
-struct Pair<__half> {
-    static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack_h2(a, b); }
-};
-template <>
-struct Pair<__nv_bfloat16> {
-    static __device__ __forceinline__ uint32_t pack(float a, float b) {
-        uint32_t r;
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-        return r;
-    }
-};
-
-// Tokens [lo, hi) that query row `rho` of the job (of the sequence's rows x
-// share) sees.
-__device__ __forceinline__ int2 seen_by(const KvAttend &a, const Jobs &j, int rho) {
-    const int pos = j.len - j.rows + rho / a.share;
-    return make_int2(a.window ? max(0, pos - a.window + 1) : 0, a.causal ? min(j.len, pos + 1) : j.len);
-}
-
-template <typename T>
-__device__ __forceinline__ int64_t row_at(const KvAttend &a, const Jobs &j, int head, int rho, int64_t token_stride,
-                                          int64_t head_stride) {
-    return (j.row0 + rho / a.share) * token_stride + (int64_t)(head * a.share + rho % a.share) * head_stride;
 }
 
 template <typename S, typename T>
@@ -231,7 +144,7 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
     int64_t u = min(cta1, cta0 + warp * mine);
     const int64_t u_end = min(cta1, u + mine);
     if (lane == 0) head_valid[warp] = head_ended[warp] = tail_valid[warp] = 0;
-    if (threadIdx.x == 0) p.meta[blockIdx.x].valid = 0;
+    if (threadIdx.x == 0) p.carries[blockIdx.x].valid = 0;
 
     // The sequence u lies in, and the units before that sequence.
     int b = 0;
@@ -307,49 +220,34 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
 #pragma unroll
         for (int i = 0; i < RING; i++) issue();
 
-        // Queries: the B operand of the scores, column n = r.  bf16 rows are
-        // scaled by a power of two so that fp16 holds them.
+        // Queries: the B operand of the scores, column n = r.
         uint32_t q[D / 16][NT][2];
         float scale[NT][2];  // of the accumulator's columns 2 jj, 2 jj + 1
         int2 seen[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; n++) {
             const int rho = min(rho0 + 8 * n + r, rho1);
-            const uint4 *src = reinterpret_cast<const uint4 *>((const T *)a.q + row_at<T>(a, j, head, rho, a.q_token, a.q_head) +
-                                                               jj * (D / 4));
-            uint4 raw[KW];
+            uint4 x[KW];
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                (const T *)a.q + row_at(a, j, head, rho, a.q_token, a.q_head) + jj * (D / 4));
 #pragma unroll
-            for (int w = 0; w < KW; w++) raw[w] = src[w];
-            float factor = a.scale_log2;
-            if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
-                uint32_t top = 0;  // largest magnitude, as bits
+            for (int w = 0; w < KW; w++) x[w] = src[w];
+            int up = 0;
+            if constexpr (!std::is_same<T, __half>::value) {  // four lanes share the row
+                uint32_t top = 0;
 #pragma unroll
-                for (int w = 0; w < KW; w++) {
-                    const uint32_t x[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
-#pragma unroll
-                    for (int i = 0; i < 4; i++) top = max(top, max(x[i] & 0x7fffu, (x[i] >> 16) & 0x7fffu));
-                }
+                for (int w = 0; w < KW; w++) top = top_bits(x[w], top);
                 top = max(top, __shfl_xor_sync(kFull, top, 1));
-                top = max(top, __shfl_xor_sync(kFull, top, 2));
-                const int e = (int)(top >> 7);  // biased; 0 for zero, 255 for an infinity or a NaN
-                const int k = e == 0 || e == 255 ? 0 : min(127 + 14 - e, 120);
-                const float up = __uint_as_float((uint32_t)(127 + k) << 23);
-                factor *= __uint_as_float((uint32_t)(127 - k) << 23);
-#pragma unroll
-                for (int w = 0; w < KW; w++) {
-                    uint32_t x[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
-#pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        x[i] = pack_h2(__uint_as_float(x[i] << 16) * up, __uint_as_float(x[i] & 0xffff0000u) * up);
-                    raw[w] = make_uint4(x[0], x[1], x[2], x[3]);
-                }
+                up = up_of(max(top, __shfl_xor_sync(kFull, top, 2)));
             }
+            query_codes_order<T, KW>(x, up);
+            const float factor = a.scale_log2 * exponent(-up);
 #pragma unroll
-            for (int w = 0; w < KW; w++) {  // dimensions (0, 4), (1, 5), (2, 6), (3, 7) of eight, as the codes come
-                q[2 * w][n][0] = prmt(raw[w].x, raw[w].z, 0x5410);
-                q[2 * w][n][1] = prmt(raw[w].x, raw[w].z, 0x7632);
-                q[2 * w + 1][n][0] = prmt(raw[w].y, raw[w].w, 0x5410);
-                q[2 * w + 1][n][1] = prmt(raw[w].y, raw[w].w, 0x7632);
+            for (int w = 0; w < KW; w++) {
+                q[2 * w][n][0] = x[w].x;
+                q[2 * w][n][1] = x[w].y;
+                q[2 * w + 1][n][0] = x[w].z;
+                q[2 * w + 1][n][1] = x[w].w;
             }
 #pragma unroll
             for (int c = 0; c < 2; c++) {
@@ -470,7 +368,7 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
                         x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
                         x = fmaxf(x, m[n][c]);
-                        const float keep = exp2f(m[n][c] - x);
+                        const float keep = ex2(m[n][c] - x);
                         m[n][c] = x;
                         l[n][c] *= keep;
 #pragma unroll
@@ -487,7 +385,7 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
                 for (int n = 0; n < NT; n++) {
 #pragma unroll
                     for (int k = 0; k < 4; k++) {
-                        s[h][n][k] = exp2f(s[h][n][k] - m[n][k & 1]);
+                        s[h][n][k] = ex2(s[h][n][k] - m[n][k & 1]);
                         l[n][k & 1] += s[h][n][k];
                     }
                 }
@@ -592,17 +490,17 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
                     const int rho = rho0 + 8 * n + 2 * jj + c;
                     if (rho > rho1) continue;
                     const float inv = l[n][c] == 0.0f ? 0.0f : 1.0f / l[n][c];
-                    T *dst = (T *)a.out + row_at<T>(a, j, head, rho, a.out_token, a.out_head) + r * (D / 8);
+                    T *dst = (T *)a.out + row_at(a, j, head, rho, a.out_token, a.out_head) + r * (D / 8);
 #pragma unroll
                     for (int i = 0; i < D / 16; i += 4)
                         *reinterpret_cast<uint4 *>(dst + 2 * i) =
-                            make_uint4(Pair<T>::pack(o[i][n][c] * inv, o[i][n][2 + c] * inv),
-                                       Pair<T>::pack(o[i + 1][n][c] * inv, o[i + 1][n][2 + c] * inv),
-                                       Pair<T>::pack(o[i + 2][n][c] * inv, o[i + 2][n][2 + c] * inv),
-                                       Pair<T>::pack(o[i + 3][n][c] * inv, o[i + 3][n][2 + c] * inv));
+                            make_uint4(pack_out<T>(o[i][n][c] * inv, o[i][n][2 + c] * inv),
+                                       pack_out<T>(o[i + 1][n][c] * inv, o[i + 1][n][2 + c] * inv),
+                                       pack_out<T>(o[i + 2][n][c] * inv, o[i + 2][n][2 + c] * inv),
+                                       pack_out<T>(o[i + 3][n][c] * inv, o[i + 3][n][2 + c] * inv));
                     if (a.lse && r == 0)
-                        a.lse[row_at<T>(a, j, head, rho, a.q_heads, 1)] =
-                            l[n][c] == 0.0f ? -INFINITY : (m[n][c] + log2f(l[n][c])) * 0.69314718055994531f;
+                        a.lse[row_at(a, j, head, rho, a.q_heads, 1)] =
+                            lse_of(m[n][c], l[n][c]);
                 }
         } else {
             float *dst = begins ? tail_part : head_part;
@@ -656,10 +554,10 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
             head = job_id[w][1];
             rho0 = job_id[w][2] * R;
         } else {
-            to = p.part + (int64_t)(2 * blockIdx.x + (w < 0 ? 0 : 1)) * R * (D + 2);
+            to = p.parts + (2 * blockIdx.x + (w < 0 ? 0 : 1)) * kv_part_floats<D, R>();
             if (w >= 0 && threadIdx.x == 0) {
-                Meta mt = {1, (int)((job_end[w] - 1) / run) - (int)blockIdx.x, job_id[w][0], job_id[w][1], job_id[w][2], {}};
-                p.meta[blockIdx.x] = mt;
+                const KvCarry mt = {1, (int)((job_end[w] - 1) / run) - (int)blockIdx.x, job_id[w][0], job_id[w][1], job_id[w][2], {}};
+                p.carries[blockIdx.x] = mt;
             }
         }
         for (int i = threadIdx.x; i < R * D / 2; i += NW * 32) {
@@ -668,7 +566,7 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
             for (int k2 = 0; k2 < n; k2++) top = fmaxf(top, part(k2)[R * D + row]);
             for (int k2 = 0; k2 < n; k2++) {
                 const float *src = part(k2);
-                const float f = exp2f(src[R * D + row] - top);
+                const float f = ex2(src[R * D + row] - top);
                 const float2 v = *reinterpret_cast<const float2 *>(src + row * D + d);
                 sum += f * src[R * D + R + row];
                 x += f * v.x;
@@ -677,11 +575,11 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
             if (whole) {
                 if (rho0 + row >= j.rows * a.share) continue;
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                *reinterpret_cast<uint32_t *>((T *)a.out + row_at<T>(a, j, head, rho0 + row, a.out_token, a.out_head) + d) =
-                    Pair<T>::pack(x * inv, y * inv);
+                *reinterpret_cast<uint32_t *>((T *)a.out + row_at(a, j, head, rho0 + row, a.out_token, a.out_head) + d) =
+                    pack_out<T>(x * inv, y * inv);
                 if (a.lse && d == 0)
-                    a.lse[row_at<T>(a, j, head, rho0 + row, a.q_heads, 1)] =
-                        sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+                    a.lse[row_at(a, j, head, rho0 + row, a.q_heads, 1)] =
+                        lse_of(top, sum);
             } else {
                 *reinterpret_cast<float2 *>(to + row * D + d) = make_float2(x, y);
                 if (d == 0) {
@@ -693,65 +591,16 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
     }
 }
 
-// One block per CTA of split_kernel and row: the job that began in that CTA's
-// run and went on, over all of its CTAs in order.
-template <typename S, typename T>
-__global__ void __launch_bounds__(S::D / 2) combine_kernel(const __grid_constant__ SplitParams p) {
-    constexpr int D = S::D, R = S::R;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Meta mt = p.meta[blockIdx.x];
-    if (!mt.valid) return;
-    const KvAttend &a = p.a;
-    const Jobs j = jobs_of<R>(a, mt.b);
-    const int row = blockIdx.y, rho = mt.qt * R + row;
-    if (rho >= j.rows * a.share) return;
-    auto part = [&](int i) { return p.part + (int64_t)(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * R * (D + 2); };
-    float top = kNoMax, sum = 0.0f, x = 0.0f, y = 0.0f;
-    for (int i = 0; i <= mt.more; i++) top = fmaxf(top, part(i)[R * D + row]);
-    for (int i = 0; i <= mt.more; i++) {
-        const float *src = part(i);
-        const float f = exp2f(src[R * D + row] - top);
-        const float2 v = *reinterpret_cast<const float2 *>(src + row * D + threadIdx.x * 2);
-        sum += f * src[R * D + R + row];
-        x += f * v.x;
-        y += f * v.y;
-    }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    *reinterpret_cast<uint32_t *>((T *)a.out + row_at<T>(a, j, mt.head, rho, a.out_token, a.out_head) + threadIdx.x * 2) =
-        Pair<T>::pack(x * inv, y * inv);
-    if (a.lse && threadIdx.x == 0)
-        a.lse[row_at<T>(a, j, mt.head, rho, a.q_heads, 1)] =
-            sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
-}
-
-template <typename S>
-constexpr size_t part_bytes() {
-    return (size_t)kMaxCtas * 2 * S::R * (S::D + 2) * 4;
-}
-
 template <typename S, typename T>
 int launch_split(const KvAttend &a, void *workspace, int sms, cudaStream_t st) {
-    SplitParams p = {};
-    p.a = a;
-    p.part = (float *)workspace;
-    p.meta = (Meta *)((uint8_t *)workspace + part_bytes<S>());
-    p.min_run = 4;
+    const SplitParams p = {a, (float *)workspace, kv_carries<S::D, S::R>(workspace), 4};
     auto kernel = split_kernel<S, T>;
     static KvOnce once;
     if (!once.set_smem((const void *)kernel, S::kSmem)) return DSQ_ERR_CUDA;
     const int grid = std::min(sms, kMaxCtas);
     kernel<<<grid, S::NW * 32, S::kSmem, st>>>(p);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, S::R);
-    cfg.blockDim = S::D / 2;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, combine_kernel<S, T>, p) != cudaSuccess) return DSQ_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? DSQ_OK : DSQ_ERR_CUDA;
+    if (cudaGetLastError() != cudaSuccess) return DSQ_ERR_CUDA;
+    return launch_join<S::D, S::R, T>(a, p.parts, p.carries, grid, st);
 }
 
 template <typename T>
@@ -771,8 +620,7 @@ int launch_of(const KvAttend &a, int head_dim, void *workspace, int sms, cudaStr
 }  // namespace
 
 size_t kv_split_workspace() {
-    return std::max(std::max(part_bytes<Split<64, 2, 16, 8>>(), part_bytes<Split<128, 2, 12, 4>>()),
-                    part_bytes<Split<256, 1, 8, 4>>()) + kMaxCtas * sizeof(Meta);
+    return std::max(std::max(kv_parts_bytes<64, 16>(), kv_parts_bytes<128, 16>()), kv_parts_bytes<256, 8>());
 }
 
 int launch_kv_split(const KvAttend &a, int head_dim, int dtype, void *workspace, int sms, cudaStream_t st) {
