@@ -49,8 +49,22 @@ __device__ __forceinline__ int64_t kv_tile_at(const KvView &c, int D, int page, 
 // A group's word: scale (fp16, low four bits zero) and zero point.
 __device__ __forceinline__ float kv_scale(uint32_t word) { return __half2float(__ushort_as_half((uint16_t)(word & 0xfff0u))); }
 
+// Division of 0 <= n < 2^31 by a number the host knows: with l = ceil(log2 d)
+// and mul = ceil(2^(31 + l) / d), n mul / 2^(31 + l) exceeds n / d by less than
+// n / 2^(31 + l) < 1 / d.
+struct KvDivisor {
+    uint32_t mul, shift, d;
+    __device__ __forceinline__ int div(int n) const { return (int)(((uint64_t)(uint32_t)n * mul) >> shift); }
+};
+inline KvDivisor kv_divisor(int d) {
+    uint32_t l = 0;
+    while ((1ll << l) < d) l++;
+    return {(uint32_t)(((1ull << (31 + l)) + d - 1) / d), 31 + l, (uint32_t)d};
+}
+
 struct KvAttend {
     KvView c;
+    KvDivisor share_by, page_by;  // by heads of a group, by tiles of a page
     const void *q;
     void *out;
     float *lse;

@@ -35,7 +35,7 @@ extern "C" int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_
     if (a->batch > 0 && !a->q_start && a->q_tokens % a->batch) return DSQ_ERR_INVALID_ARG;
     if ((int64_t)a->table_pages * d->page_tokens >= ((int64_t)1 << 31) || a->q_tokens * a->q_heads >= ((int64_t)1 << 31))
         return DSQ_ERR_UNSUPPORTED;
-    const bool many = many_rows(d, a);
+    const bool many = many_rows(d, a) && d->pages > 0;
     const size_t need = many ? kv_prompt_workspace(d->head_dim) : kv_split_workspace();
     if (!workspace || *workspace_bytes < need) {
         *workspace_bytes = need;
@@ -64,6 +64,8 @@ extern "C" int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_
     k.q_tokens = a->q_tokens;
     k.q_heads = a->q_heads;
     k.share = a->q_heads / d->kv_heads;
+    k.share_by = kv_divisor(k.share);
+    k.page_by = kv_divisor(k.c.page_tiles);
     k.batch = a->batch;
     k.table_pages = a->table_pages;
     k.causal = a->causal;

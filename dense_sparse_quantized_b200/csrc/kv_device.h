@@ -112,14 +112,15 @@ __device__ __forceinline__ void query_codes_order(uint4 (&x)[N], int up) {
 // Tokens [x, y) that query row `rho` of a kv head (of the sequence's rows
 // times the heads of a group) sees.
 __device__ __forceinline__ int2 seen_by(const KvAttend &a, const KvSeq &s, int rho) {
-    const int pos = s.len - s.rows + rho / a.share;
+    const int pos = s.len - s.rows + a.share_by.div(rho);
     return make_int2(a.window ? max(0, pos - a.window + 1) : 0, a.causal ? min(s.len, pos + 1) : s.len);
 }
 
 // Where that row of kv head `head` lies.
 __device__ __forceinline__ int64_t row_at(const KvAttend &a, const KvSeq &s, int head, int rho, int64_t token_stride,
                                           int64_t head_stride) {
-    return (s.row0 + rho / a.share) * token_stride + (int64_t)(head * a.share + rho % a.share) * head_stride;
+    const int i = a.share_by.div(rho);
+    return (s.row0 + i) * token_stride + (int64_t)(head * a.share + rho - i * a.share) * head_stride;
 }
 
 __device__ __forceinline__ float lse_of(float top, float sum) {

@@ -74,7 +74,8 @@ struct Shared {
     uint4 nans[kFlags], holes[kFlags];  // by loading warp: NaN tokens; sub-tiles without a page
     uint32_t tmem;
     int b, head, qt, first;  // where this CTA's run begins
-    int64_t left, run, end;  // units of it; of every CTA's; its end among all units
+    int left;                // units of it
+    int64_t run, end;        // units of every CTA's run; where this one ends among all units
 };
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -110,30 +111,31 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t *r) {
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D[tmem] (+)= A B, fp16, fp32 accumulator; A from shared or tensor memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(0u)
-        : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %5, %5}, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(0u)
-        : "memory");
-}
-
 // Shared-memory operand of 128-byte rows, 128-byte swizzle, groups of eight
-// rows 1024 bytes apart.  K-major: a row is one of M or N, 64 elements of k.
-// MN-major: a row is one k, 64 elements of N, the next 64 of N kBlk bytes on.
-__device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t leading) {
-    return ((uint64_t)(at >> 4) & 0x3fffu) | ((uint64_t)(leading >> 4) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
+// rows 1024 bytes apart: the descriptor's low word (address and leading
+// dimension) and its high word, which all operands here have in common.
+// K-major: a row is one of M or N, 64 elements of k.  MN-major: a row is one k,
+// 64 elements of N, the next 64 of N kBlk bytes on.
+__device__ __forceinline__ uint32_t operand(uint32_t at, uint32_t leading) { return at >> 4 | (leading >> 4) << 16; }
+constexpr uint32_t kOperandHigh = 64u | 1u << 14 | 2u << 29;
 constexpr uint32_t instruction(int n, bool b_mn_major) {
     return (1u << 4) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// D[tmem] (+)= A B, fp16, fp32 accumulator; A from shared or tensor memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(add), "n"(kOperandHigh)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(add), "n"(kOperandHigh)
+        : "memory");
 }
 
 // Units [x, y) of a row tile's job: at least one, so that every row is written.
@@ -156,8 +158,7 @@ struct Piece {
 };
 template <int R>
 struct Walk {
-    int b, head, qt, first;
-    int64_t left;
+    int b, head, qt, first, left;
     __device__ __forceinline__ explicit Walk(const Shared &sh) : b(sh.b), head(sh.head), qt(sh.qt), first(sh.first), left(sh.left) {}
     __device__ __forceinline__ bool next(const KvAttend &a, Piece &p) {
         while (left > 0 && b < a.batch) {
@@ -176,7 +177,7 @@ struct Walk {
             p.head = head;
             p.qt = qt;
             p.t0 = u.x + first;
-            p.t1 = (int)min((int64_t)u.y, p.t0 + left);
+            p.t1 = min(u.y, p.t0 + left);
             p.rest = u.y - p.t1;
             p.begins = first == 0;
             left -= p.t1 - p.t0;
@@ -220,7 +221,17 @@ __device__ __forceinline__ void find_run(const KvAttend &a, Shared &sh) {
         return w;
     };
     int64_t total = 0;
-    for (int b = lane; b < a.batch; b += 32) total += head_units(b) * a.c.kv_heads;
+    if (a.batch < 8) {  // few sequences: the lanes take row tiles, else sequences
+        for (int b = 0; b < a.batch; b++) {
+            const KvSeq s = kv_seq(a, b);
+            const int tiles = tiles_of<R>(a, s);
+            for (int qt = lane; qt < tiles; qt += 32) {
+                const int2 u = units_of<R>(a, s, qt);
+                total += (int64_t)(u.y - u.x) * a.c.kv_heads;
+            }
+        }
+    } else
+        for (int b = lane; b < a.batch; b += 32) total += head_units(b) * a.c.kv_heads;
 #pragma unroll
     for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(kFull, total, m);
     const int64_t run = (total + gridDim.x - 1) / gridDim.x;
@@ -266,7 +277,7 @@ __device__ __forceinline__ void find_run(const KvAttend &a, Shared &sh) {
         sh.head = head;
         sh.qt = qt;
         sh.first = first;
-        sh.left = u1 - u0;
+        sh.left = (int)(u1 - u0);
         sh.run = run;
         sh.end = u1;
     }
@@ -284,20 +295,30 @@ struct Loader {
     bool more;
     const int lane, warp, tok, pair;
 
-    // A unit on its way: its pages, then its addresses.
+    // A unit on its way: the pages of this warp's two tiles of 16 tokens, and
+    // which tokens of the unit some row sees.
     struct Unit {
+        int lo, hi, page[2], in_page[2], head;
         bool there;
-        int lo, hi;       // tokens of the unit that some row sees
-        int page[2], in_page[2], head;
     };
+    // Its addresses: this lane's token in both tiles.  Tiles that hold no such
+    // token, or have no page, read the cache's first.
+    struct Source {
+        const uint8_t *at[2];
+        bool use[2];
+    };
+    uint32_t to[4];  // this lane's chunks in a row block of the swizzled tile
     __device__ __forceinline__ Loader(const KvAttend &a_, const Shared &sh)
         : a(a_), walk(sh), lane(threadIdx.x & 31), warp((threadIdx.x >> 5) & 3), tok(lane >> 1), pair(lane & 1) {
         more = walk.next(a, p);
         t = p.t0;
+#pragma unroll
+        for (int i = 0; i < 4; i++) to[i] = (2 * warp * kKvTile + tok) * 128 + (((pair * 4 + i) ^ (tok & 7)) << 4);
     }
     __device__ __forceinline__ Unit next() {
         Unit u = {};
         u.there = more;
+        u.page[0] = u.page[1] = -1;
         if (!more) return u;
         const int last = min((p.qt + 1) * S::R, p.s.rows * a.share) - 1;
         u.lo = seen_by(a, p.s, p.qt * S::R).x - t * kN;
@@ -306,9 +327,9 @@ struct Loader {
         const int32_t *row = a.page_table + (int64_t)p.b * a.table_pages;
 #pragma unroll
         for (int i = 0; i < 2; i++) {
-            const int tile = t * (kN / kKvTile) + 2 * warp + i, col = tile / a.c.page_tiles;
+            const int tile = t * (kN / kKvTile) + 2 * warp + i, col = a.page_by.div(tile);
             u.in_page[i] = tile - col * a.c.page_tiles;
-            u.page[i] = col < a.table_pages && u.hi > (2 * warp + i) * kKvTile ? row[col] : -1;
+            if (col < a.table_pages && u.hi > (2 * warp + i) * kKvTile) u.page[i] = row[col];
         }
         if (++t == p.t1) {
             more = walk.next(a, p);
@@ -316,44 +337,58 @@ struct Loader {
         }
         return u;
     }
-    __device__ __forceinline__ static int group(int item, int c, int pair) {
-        return D == 64 ? pair : 2 * (2 * item + (c & 1)) + pair;
+    __device__ __forceinline__ Source source(const Unit &u) const {
+        Source s;
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const bool there = (uint32_t)u.page[i] < (uint32_t)a.c.pages;
+            const int64_t tile = there ? ((int64_t)u.page[i] * a.c.kv_heads + u.head) * a.c.page_tiles + u.in_page[i] : 0;
+            const int at = (2 * warp + i) * kKvTile + tok;
+            s.at[i] = a.c.cache + tile * kv_tile_bytes(D);
+            s.use[i] = there && at >= u.lo && at < u.hi;
+        }
+        return s;
     }
-    __device__ __forceinline__ static int sub(int c) { return D == 64 ? c : c >> 1; }
-    // Loads one item (which: K or V) of the unit into x and its words into w;
-    // with the keys also the values' words, into nan, for their NaNs.
-    __device__ __forceinline__ void load(const Unit &u, int which, int item, uint4 (&x)[CH], uint32_t (&w)[CH], bool (&nan)[CH]) const {
+    // Chunk c of an item: tile sub(c), group 2 * block(item, c) + pair.
+    __device__ __forceinline__ static constexpr int sub(int c) { return D == 64 ? c : c >> 1; }
+    __device__ __forceinline__ static constexpr int block(int item, int c) { return D == 64 ? 0 : 2 * item + (c & 1); }
+    // Loads one item (which: K or V) into x and its words into w.
+    __device__ __forceinline__ void load(const Source &s, int which, int item, uint4 (&x)[CH], uint32_t (&w)[CH]) const {
 #pragma unroll
         for (int c = 0; c < CH; c++) {
-            const int i = sub(c), g = group(item, c, pair), at = (2 * warp + i) * kKvTile + tok;
-            const int page = u.page[i];
-            x[c] = make_uint4(0, 0, 0, 0);
-            w[c] = 0;
-            nan[c] = false;
-            if (u.there && (uint32_t)page < (uint32_t)a.c.pages && at >= u.lo && at < u.hi) {
-                const uint8_t *tile =
-                    a.c.cache + (((int64_t)page * a.c.kv_heads + u.head) * a.c.page_tiles + u.in_page[i]) * kv_tile_bytes(D);
-                x[c] = *reinterpret_cast<const uint4 *>(tile + kv_codes(D, which) + tok * (D / 2) + g * 16);
-                w[c] = *reinterpret_cast<const uint16_t *>(tile + kv_words(D, which) + (g * kKvTile + tok) * 2);
-                if (which == 0)
-                    nan[c] = (*reinterpret_cast<const uint16_t *>(tile + kv_words(D, 1) + (g * kKvTile + tok) * 2) & 0x7c00u) == 0x7c00u;
-            }
+            const uint8_t *at = s.at[sub(c)];
+            x[c] = *reinterpret_cast<const uint4 *>(at + kv_codes(D, which) + block(item, c) * 32 + tok * (D / 2) + pair * 16);
+            const uint32_t word =
+                *reinterpret_cast<const uint16_t *>(at + kv_words(D, which) + block(item, c) * 4 * kKvTile + (pair * kKvTile + tok) * 2);
+            w[c] = s.use[sub(c)] ? word : 0u;
         }
     }
-    // Unpacks an item into the tile at `to`.
-    __device__ __forceinline__ void store(uint32_t to, int which, int item, const uint4 (&x)[CH], const uint32_t (&w)[CH]) const {
+    // Whether this lane's value words of the unit hold a NaN, by tile.
+    __device__ __forceinline__ uint32_t value_nans(const Source &s) const {
+        uint32_t bad = 0;
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int g = 0; g < D / 64; g++) {
+                const uint32_t word =
+                    *reinterpret_cast<const uint16_t *>(s.at[i] + kv_words(D, 1) + g * 4 * kKvTile + (pair * kKvTile + tok) * 2);
+                if (s.use[i] && (word & 0x7c00u) == 0x7c00u) bad |= 1u << i;
+            }
+        return bad;
+    }
+    // Unpacks an item into the tile at `tile`.
+    __device__ __forceinline__ void store(uint32_t tile, int which, int item, const uint4 (&x)[CH], const uint32_t (&w)[CH]) const {
 #pragma unroll
         for (int c = 0; c < CH; c++) {
-            const int g = group(item, c, pair), at = (2 * warp + sub(c)) * kKvTile + tok;
             const uint32_t word = which == 1 && (w[c] & 0x7c00u) == 0x7c00u ? 0u : w[c];
             const Decode d(prmt(word, word, 0x1010));
-            const uint32_t row = to + (g >> 1) * kBlk + at * 128;
+            const uint32_t at = tile + block(item, c) * kBlk + sub(c) * kKvTile * 128;
             const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 const uint32_t y = v[i] >> 8;
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((((g & 1) * 4 + i) ^ (at & 7)) << 4)),
-                             "r"(d.low(v[i])), "r"(d.high(v[i])), "r"(d.low(y)), "r"(d.high(y))
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + to[i]), "r"(d.low(v[i])), "r"(d.high(v[i])),
+                             "r"(d.low(y)), "r"(d.high(y))
                              : "memory");
             }
         }
@@ -364,55 +399,58 @@ template <int D>
 __device__ __forceinline__ void load_role(const KvAttend &a, Shared &sh, uint32_t kbuf, uint32_t vbuf) {
     using S = Shape<D>;
     constexpr int CH = S::kChunks, N = S::kItems;
-    Loader<D> ld(a, sh);
-    typename Loader<D>::Unit u = ld.next(), u1 = ld.next();
-    uint4 x[2][CH];      // items by turns: the keys' and the values' at 128 dimensions and below
+    using L = Loader<D>;
+    L ld(a, sh);
+    typename L::Unit u = ld.next(), u1 = ld.next();
+    uint4 x[2][CH];  // two items on their way: of K and of V, or the two of each at 256 dimensions
     uint32_t w[2][CH];
-    bool nan[2][CH];
-    ld.load(u, 0, 0, x[0], w[0], nan[0]);
-    ld.load(u, N == 2 ? 0 : 1, N == 2 ? 1 : 0, x[1], w[1], nan[1]);
+    typename L::Source s = ld.source(u);
+    ld.load(s, 0, 0, x[0], w[0]);
+    ld.load(s, N == 2 ? 0 : 1, N - 1, x[1], w[1]);
+    uint32_t nan = ld.value_nans(s);
     for (uint32_t it = 0; u.there; it++) {
-        const typename Loader<D>::Unit u2 = ld.next();
+        const typename L::Unit u2 = ld.next();
+        const typename L::Source s1 = ld.source(u1);
         const uint32_t stage = it % S::kStages, phase = it / S::kStages & 1;
         // keys, and the flags of the unit
         if (!mbar_wait_warp(&sh.kempty[stage], phase ^ 1)) return;
         uint32_t bad = 0;
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-#pragma unroll
-            for (int c = 0; c < CH; c++)
-                if (__any_sync(kFull, nan[i][c])) {
-                    uint32_t two = __ballot_sync(kFull, nan[i][c]);  // two lanes a token
-                    two |= two >> 1;
-                    uint32_t bits = 0;
-                    for (int k = 0; k < 16; k++) bits |= (two >> (2 * k) & 1u) << k;
-                    bad |= bits << (16 * Loader<D>::sub(c));
-                }
-            ld.store(kbuf + stage * S::kTile, 0, i, x[i], w[i]);
-            if (N == 2) ld.load(u, 1, i, x[i], w[i], nan[i]);
+        if (__any_sync(kFull, nan)) {
+#pragma unroll 1
+            for (int i = 0; i < 32; i++) {  // lane i: token i / 2 of both tiles
+                const uint32_t of = __shfl_sync(kFull, nan, i);
+                bad |= (of & 1u) << (i >> 1) | (of >> 1) << (16 + (i >> 1));
+            }
         }
         if (ld.lane == 0) {
             reinterpret_cast<uint32_t *>(&sh.nans[it % kFlags])[ld.warp] = bad;
             reinterpret_cast<uint32_t *>(&sh.holes[it % kFlags])[ld.warp] =
                 (uint32_t)((uint32_t)u.page[0] >= (uint32_t)a.c.pages) | (uint32_t)((uint32_t)u.page[1] >= (uint32_t)a.c.pages) << 1;
         }
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            ld.store(kbuf + stage * S::kTile, 0, i, x[i], w[i]);
+            if (N == 2) ld.load(s, 1, i, x[i], w[i]);
+        }
         fence_async();
         __syncwarp();
         if (ld.lane == 0) mbar_arrive(&sh.kfull[stage]);
-        if (N == 1) ld.load(u1, 0, 0, x[0], w[0], nan[0]);
+        if (N == 1) ld.load(s1, 0, 0, x[0], w[0]);
+        nan = ld.value_nans(s1);
         // values
         if (!mbar_wait_warp(&sh.vempty[stage], phase ^ 1)) return;
 #pragma unroll
         for (int i = 0; i < N; i++) {
             ld.store(vbuf + stage * S::kTile, 1, i, x[N == 2 ? i : 1], w[N == 2 ? i : 1]);
-            if (N == 2) ld.load(u1, 0, i, x[i], w[i], nan[i]);
+            if (N == 2) ld.load(s1, 0, i, x[i], w[i]);
         }
         fence_async();
         __syncwarp();
         if (ld.lane == 0) mbar_arrive(&sh.vfull[stage]);
-        if (N == 1) ld.load(u1, 1, 0, x[1], w[1], nan[1]);
+        if (N == 1) ld.load(s1, 1, 0, x[1], w[1]);
         u = u1;
         u1 = u2;
+        s = s1;
     }
 }
 
@@ -421,7 +459,7 @@ template <int D>
 __device__ __forceinline__ void product_role(const KvAttend &a, Shared &sh, uint32_t qbuf, uint32_t kbuf, uint32_t vbuf) {
     using S = Shape<D>;
     constexpr uint32_t kScores = instruction(kN, false), kOut = instruction(D, true);
-    const uint32_t tmem = sh.tmem;
+    const uint32_t tmem = sh.tmem, q0 = operand(qbuf, 16), k0 = operand(kbuf, 16), v0 = operand(vbuf, kBlk);
     Walk<S::R> walk(sh);
     Piece p;
     uint32_t it = 0, pn[2] = {0, 0}, qn[2] = {0, 0};
@@ -432,8 +470,8 @@ __device__ __forceinline__ void product_role(const KvAttend &a, Shared &sh, uint
         auto scores = [&](int r, uint32_t stage) {
 #pragma unroll
             for (int k = 0; k < D / 16; k++) {
-                const uint32_t at = k / 4 * kBlk + k % 4 * 32;
-                mma_ss(tmem + 128 * r, operand(qbuf + r * S::kTile + at, 16), operand(kbuf + stage * S::kTile + at, 16), kScores, k > 0);
+                const uint32_t at = (k / 4 * kBlk + k % 4 * 32) >> 4;
+                mma_ss(tmem + 128 * r, q0 + (r * S::kTile >> 4) + at, k0 + stage * (S::kTile >> 4) + at, kScores, k > 0);
             }
             commit(&sh.sfull[r]);
         };
@@ -457,7 +495,7 @@ __device__ __forceinline__ void product_role(const KvAttend &a, Shared &sh, uint
                     fence_after();
 #pragma unroll
                     for (int k = 0; k < kN / 16; k++)
-                        mma_ts(tmem + S::kO + D * r, tmem + 128 * r + 8 * k, operand(vbuf + stage * S::kTile + k * 2048, kBlk), kOut,
+                        mma_ts(tmem + S::kO + D * r, tmem + 128 * r + 8 * k, v0 + stage * (S::kTile >> 4) + k * (2048 >> 4), kOut,
                                k > 0 || t > on[r].x);
                     if (t == on[r].y - 1) commit(&sh.ofull[r]);
                 }
@@ -480,6 +518,23 @@ __device__ __forceinline__ void product_role(const KvAttend &a, Shared &sh, uint
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Two at once: a * b + c, and a + b.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
 
@@ -565,20 +620,21 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
                         }
                     }
                 }
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
 #pragma unroll
                 for (int i = 0; i < kN; i += 64) {
                     uint32_t ph[32];
 #pragma unroll
                     for (int k = 0; k < 32; k++) {
-                        const float p0 = ex2(fmaf(s[i + 2 * k], f, -m)), p1 = ex2(fmaf(s[i + 2 * k + 1], f, -m));
-                        sum[2 * k % 4] += p0;
-                        sum[(2 * k + 1) % 4] += p1;
-                        ph[k] = pack_h2(p0, p1);
+                        const float2 y = fma2(make_float2(s[i + 2 * k], s[i + 2 * k + 1]), make_float2(f, f), make_float2(-m, -m));
+                        const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                        sum[k & 1] = add2(sum[k & 1], e);
+                        ph[k] = pack_h2(e.x, e.y);
                     }
                     tmem_st32(st + i / 2, ph);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                sum[0] = add2(sum[0], sum[1]);
+                l += sum[0].x + sum[0].y;
                 wait_st();
                 fence_before();
                 mbar_arrive(&sh.pfull[r]);

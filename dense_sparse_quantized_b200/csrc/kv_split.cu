@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
         const int tile1 = min((unit0 + last) * 2, (max(hi_any, 0) + 15) / 16);
 
         // Page numbers of the next 64 table columns, one per lane and register.
-        int col = tile0 / a.c.page_tiles, in_page = tile0 - col * a.c.page_tiles, col0 = col;
+        int col = a.page_by.div(tile0), in_page = tile0 - col * a.c.page_tiles, col0 = col;
         const int32_t *row = a.page_table + (int64_t)b * a.table_pages;
         auto pages_from = [&](int c) { return c + lane < a.table_pages ? row[c + lane] : -1; };
         int pages = pages_from(col0), pages_next = pages_from(col0 + 32);
