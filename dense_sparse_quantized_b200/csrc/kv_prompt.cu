@@ -57,10 +57,16 @@ struct Shape {
     static constexpr int R = 128 * A;
     static constexpr int kStages = D == 256 ? 1 : 2; // K and V tiles in the ring
     static constexpr int kTile = D / 64 * kBlk;      // bytes of 128 rows
-    static constexpr int kSmem = (A + 2 * kStages) * kTile + 1024;
+    // Of a loading warp: the codes and key words of its two tiles, and twice
+    // their value words.  At 256 dimensions key and value codes take turns in
+    // one place; there is no room for two.
+    static constexpr bool kTurns = D == 256;
+    static constexpr int kRawTile = (kTurns ? 1 : 2) * kKvTile * D / 2 + D, kRaw = 2 * kRawTile + 4 * D;
+    __host__ __device__ static constexpr int raw_codes(int which) { return kTurns ? 0 : which * kKvTile * D / 2; }
+    static constexpr int kRawWords = kRawTile - D;
+    static constexpr int kSmem = (A + 2 * kStages) * kTile + 4 * kRaw + 1024;
+    static_assert(kSmem + 512 <= 227 * 1024, "shared memory of a CTA");
     static constexpr int kO = A * 128;               // first column of the outputs
-    static constexpr int kChunks = D == 64 ? 2 : 4;  // of 16 bytes that a thread moves at a time
-    static constexpr int kItems = D == 256 ? 2 : 1;  // times per K or V tile
 };
 
 struct PromptParams {
@@ -106,6 +112,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t *r) {
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
         "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -284,36 +298,32 @@ __device__ __forceinline__ void find_run(const KvAttend &a, Shared &sh) {
 }
 
 // ------------------------------------------------------------ warps 8-11
+// Each warp brings tiles 2 w and 2 w + 1 of a unit's eight: by cp.async as they
+// are into its own `raw`, keys and values apart so that one's copy runs while
+// the other is unpacked, and from there unpacked into the operand.  The value
+// words come with the keys, so that their NaNs are known when the keys are
+// handed over; they are kept for two units.  The loops are kept rolled: four
+// roles' code has to fit the instruction caches.
 template <int D>
 struct Loader {
     using S = Shape<D>;
-    static constexpr int CH = S::kChunks;
     const KvAttend &a;
     Walk<S::R> walk;
     Piece p;
     int t;
     bool more;
-    const int lane, warp, tok, pair;
+    const int lane, warp;
 
-    // A unit on its way: the pages of this warp's two tiles of 16 tokens, and
-    // which tokens of the unit some row sees.
+    // A unit on its way: the pages of the warp's tiles, and which tokens of
+    // the unit some row sees.
     struct Unit {
         int lo, hi, page[2], in_page[2], head;
         bool there;
     };
-    // Its addresses: this lane's token in both tiles.  Tiles that hold no such
-    // token, or have no page, read the cache's first.
-    struct Source {
-        const uint8_t *at[2];
-        bool use[2];
-    };
-    uint32_t to[4];  // this lane's chunks in a row block of the swizzled tile
     __device__ __forceinline__ Loader(const KvAttend &a_, const Shared &sh)
-        : a(a_), walk(sh), lane(threadIdx.x & 31), warp((threadIdx.x >> 5) & 3), tok(lane >> 1), pair(lane & 1) {
+        : a(a_), walk(sh), lane(threadIdx.x & 31), warp((threadIdx.x >> 5) & 3) {
         more = walk.next(a, p);
         t = p.t0;
-#pragma unroll
-        for (int i = 0; i < 4; i++) to[i] = (2 * warp * kKvTile + tok) * 128 + (((pair * 4 + i) ^ (tok & 7)) << 4);
     }
     __device__ __forceinline__ Unit next() {
         Unit u = {};
@@ -337,129 +347,135 @@ struct Loader {
         }
         return u;
     }
-    __device__ __forceinline__ Source source(const Unit &u) const {
-        Source s;
-#pragma unroll
-        for (int i = 0; i < 2; i++) {
-            const bool there = (uint32_t)u.page[i] < (uint32_t)a.c.pages;
-            const int64_t tile = there ? ((int64_t)u.page[i] * a.c.kv_heads + u.head) * a.c.page_tiles + u.in_page[i] : 0;
-            const int at = (2 * warp + i) * kKvTile + tok;
-            s.at[i] = a.c.cache + tile * kv_tile_bytes(D);
-            s.use[i] = there && at >= u.lo && at < u.hi;
-        }
-        return s;
+    __device__ __forceinline__ bool there(const Unit &u, int i) const {
+        return (uint32_t)(i ? u.page[1] : u.page[0]) < (uint32_t)a.c.pages;
     }
-    // Chunk c of an item: tile sub(c), group 2 * block(item, c) + pair.
-    __device__ __forceinline__ static constexpr int sub(int c) { return D == 64 ? c : c >> 1; }
-    __device__ __forceinline__ static constexpr int block(int item, int c) { return D == 64 ? 0 : 2 * item + (c & 1); }
-    // Loads one item (which: K or V) into x and its words into w.
-    __device__ __forceinline__ void load(const Source &s, int which, int item, uint4 (&x)[CH], uint32_t (&w)[CH]) const {
-#pragma unroll
-        for (int c = 0; c < CH; c++) {
-            const uint8_t *at = s.at[sub(c)];
-            x[c] = *reinterpret_cast<const uint4 *>(at + kv_codes(D, which) + block(item, c) * 32 + tok * (D / 2) + pair * 16);
-            const uint32_t word =
-                *reinterpret_cast<const uint16_t *>(at + kv_words(D, which) + block(item, c) * 4 * kKvTile + (pair * kKvTile + tok) * 2);
-            w[c] = s.use[sub(c)] ? word : 0u;
-        }
-    }
-    // Whether this lane's value words of the unit hold a NaN, by tile.
-    __device__ __forceinline__ uint32_t value_nans(const Source &s) const {
-        uint32_t bad = 0;
+    // Starts the copy of both tiles' keys or values; a tile without a page is
+    // not copied, and not used.
+    __device__ __forceinline__ void copy(const Unit &u, int which, uint32_t raw, uint32_t value_words) const {
 #pragma unroll
         for (int i = 0; i < 2; i++)
+            if (there(u, i)) {
+                const uint8_t *src =
+                    a.c.cache + (((int64_t)u.page[i] * a.c.kv_heads + u.head) * a.c.page_tiles + u.in_page[i]) * kv_tile_bytes(D);
+                const uint32_t dst = raw + i * S::kRawTile;
+#pragma unroll
+                for (int k = 0; k < D / 64; k++)
+                    cp_async16(dst + S::raw_codes(which) + k * 512 + lane * 16, src + kv_codes(D, which) + k * 512 + lane * 16);
+                if (which == 0 && lane < D / 8)  // D / 16 chunks of key words, then as many of value words
+                    cp_async16(lane < D / 16 ? dst + S::kRawWords + lane * 16 : value_words + i * D + (lane - D / 16) * 16,
+                               src + kv_words(D, 0) + lane * 16);
+            }
+        cp_async_commit();
+    }
+    // Which of this lane's value words are NaN, by tile (bits 0, 1).
+    __device__ __forceinline__ uint32_t nans(const Unit &u, uint32_t value_words) const {
+        const int tok = lane >> 1, pair = lane & 1;
+        uint32_t bad = 0;
+#pragma unroll 1
+        for (int i = 0; i < 2; i++) {
+            const int at = (2 * warp + i) * kKvTile + tok;
+            const bool use = there(u, i) && at >= u.lo && at < u.hi;
 #pragma unroll
             for (int g = 0; g < D / 64; g++) {
-                const uint32_t word =
-                    *reinterpret_cast<const uint16_t *>(s.at[i] + kv_words(D, 1) + g * 4 * kKvTile + (pair * kKvTile + tok) * 2);
-                if (s.use[i] && (word & 0x7c00u) == 0x7c00u) bad |= 1u << i;
+                uint16_t word;
+                asm volatile("ld.shared.u16 %0, [%1];"
+                             : "=h"(word)
+                             : "r"(value_words + i * D + g * 4 * kKvTile + (pair * kKvTile + tok) * 2));
+                if (use && (word & 0x7c00u) == 0x7c00u) bad |= 1u << i;
             }
+        }
         return bad;
     }
-    // Unpacks an item into the tile at `tile`.
-    __device__ __forceinline__ void store(uint32_t tile, int which, int item, const uint4 (&x)[CH], const uint32_t (&w)[CH]) const {
+    // Unpacks them into the operand at `tile`.  Lane: token lane / 2, groups of
+    // 32 dimensions lane % 2, + 2, ...
+    __device__ __forceinline__ void unpack(const Unit &u, int which, uint32_t raw, uint32_t value_words, uint32_t tile) const {
+        const int tok = lane >> 1, pair = lane & 1;
+#pragma unroll 1
+        for (int i = 0; i < 2; i++) {
+            const int at = (2 * warp + i) * kKvTile + tok;
+            const bool use = there(u, i) && at >= u.lo && at < u.hi;
+            uint32_t from = raw + i * S::kRawTile + S::raw_codes(which) + tok * (D / 2) + pair * 16;
+            uint32_t word_at = (which ? value_words + i * D : raw + i * S::kRawTile + S::kRawWords) + (pair * kKvTile + tok) * 2;
+            uint32_t to = tile + at * 128;
+#pragma unroll 1
+            for (int g = 0; g < D / 64; g++, from += 32, word_at += 4 * kKvTile, to += kBlk) {
+                uint16_t word;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(word) : "r"(word_at));
+                const uint4 x = lds128(from);
+                const uint32_t w = use && !(which == 1 && (word & 0x7c00u) == 0x7c00u) ? word : 0u;
+                const Decode d(prmt(w, w, 0x1010));
+                const uint32_t v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int c = 0; c < CH; c++) {
-            const uint32_t word = which == 1 && (w[c] & 0x7c00u) == 0x7c00u ? 0u : w[c];
-            const Decode d(prmt(word, word, 0x1010));
-            const uint32_t at = tile + block(item, c) * kBlk + sub(c) * kKvTile * 128;
-            const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const uint32_t y = v[i] >> 8;
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + to[i]), "r"(d.low(v[i])), "r"(d.high(v[i])),
-                             "r"(d.low(y)), "r"(d.high(y))
-                             : "memory");
+                for (int k = 0; k < 4; k++) {
+                    const uint32_t y = v[k] >> 8;
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((pair * 4 + k) ^ (tok & 7)) << 4)),
+                                 "r"(d.low(v[k])), "r"(d.high(v[k])), "r"(d.low(y)), "r"(d.high(y))
+                                 : "memory");
+                }
             }
         }
     }
 };
 
 template <int D>
-__device__ __forceinline__ void load_role(const KvAttend &a, Shared &sh, uint32_t kbuf, uint32_t vbuf) {
+__device__ __forceinline__ void load_role(const KvAttend &a, Shared &sh, uint32_t kbuf, uint32_t vbuf, uint32_t raw0) {
     using S = Shape<D>;
-    constexpr int CH = S::kChunks, N = S::kItems;
     using L = Loader<D>;
     L ld(a, sh);
+    const uint32_t raw = raw0 + ld.warp * S::kRaw, words = raw + 2 * S::kRawTile;
     typename L::Unit u = ld.next(), u1 = ld.next();
-    uint4 x[2][CH];  // two items on their way: of K and of V, or the two of each at 256 dimensions
-    uint32_t w[2][CH];
-    typename L::Source s = ld.source(u);
-    ld.load(s, 0, 0, x[0], w[0]);
-    ld.load(s, N == 2 ? 0 : 1, N - 1, x[1], w[1]);
-    uint32_t nan = ld.value_nans(s);
+    ld.copy(u, 0, raw, words);
+    if (!S::kTurns) ld.copy(u, 1, raw, words);
     for (uint32_t it = 0; u.there; it++) {
         const typename L::Unit u2 = ld.next();
-        const typename L::Source s1 = ld.source(u1);
         const uint32_t stage = it % S::kStages, phase = it / S::kStages & 1;
-        // keys, and the flags of the unit
-        if (!mbar_wait_warp(&sh.kempty[stage], phase ^ 1)) return;
-        uint32_t bad = 0;
-        if (__any_sync(kFull, nan)) {
+        const uint32_t words0 = words + (it & 1) * 2 * D, words1 = words + (~it & 1) * 2 * D;
 #pragma unroll 1
-            for (int i = 0; i < 32; i++) {  // lane i: token i / 2 of both tiles
-                const uint32_t of = __shfl_sync(kFull, nan, i);
-                bad |= (of & 1u) << (i >> 1) | (of >> 1) << (16 + (i >> 1));
+        for (int which = 0; which < 2; which++) {
+            if (!mbar_wait_warp(which ? &sh.vempty[stage] : &sh.kempty[stage], phase ^ 1)) {
+                cp_async_wait<0>();
+                return;
             }
+            cp_async_wait<S::kTurns ? 0 : 1>();  // all copies but the other half's, the last started
+            __syncwarp();
+            if (which == 0) {
+                const uint32_t nan = ld.nans(u, words0);
+                uint32_t bad = 0;
+                if (__any_sync(kFull, nan)) {
+#pragma unroll 1
+                    for (int i = 0; i < 32; i++) {  // lane i: token i / 2 of both tiles
+                        const uint32_t of = __shfl_sync(kFull, nan, i);
+                        bad |= (of & 1u) << (i >> 1) | (of >> 1) << (16 + (i >> 1));
+                    }
+                }
+                if (ld.lane == 0) {
+                    reinterpret_cast<uint32_t *>(&sh.nans[it % kFlags])[ld.warp] = bad;
+                    reinterpret_cast<uint32_t *>(&sh.holes[it % kFlags])[ld.warp] = (uint32_t)!ld.there(u, 0) | (uint32_t)!ld.there(u, 1) << 1;
+                }
+            }
+            ld.unpack(u, which, raw, words0, (which ? vbuf : kbuf) + stage * S::kTile);
+            fence_async();
+            __syncwarp();
+            if (ld.lane == 0) mbar_arrive(which ? &sh.vfull[stage] : &sh.kfull[stage]);
+            if (!S::kTurns) ld.copy(u1, which, raw, words1);
+            else if (which == 0) ld.copy(u, 1, raw, words0);
+            else ld.copy(u1, 0, raw, words1);
         }
-        if (ld.lane == 0) {
-            reinterpret_cast<uint32_t *>(&sh.nans[it % kFlags])[ld.warp] = bad;
-            reinterpret_cast<uint32_t *>(&sh.holes[it % kFlags])[ld.warp] =
-                (uint32_t)((uint32_t)u.page[0] >= (uint32_t)a.c.pages) | (uint32_t)((uint32_t)u.page[1] >= (uint32_t)a.c.pages) << 1;
-        }
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            ld.store(kbuf + stage * S::kTile, 0, i, x[i], w[i]);
-            if (N == 2) ld.load(s, 1, i, x[i], w[i]);
-        }
-        fence_async();
-        __syncwarp();
-        if (ld.lane == 0) mbar_arrive(&sh.kfull[stage]);
-        if (N == 1) ld.load(s1, 0, 0, x[0], w[0]);
-        nan = ld.value_nans(s1);
-        // values
-        if (!mbar_wait_warp(&sh.vempty[stage], phase ^ 1)) return;
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            ld.store(vbuf + stage * S::kTile, 1, i, x[N == 2 ? i : 1], w[N == 2 ? i : 1]);
-            if (N == 2) ld.load(s1, 0, i, x[i], w[i]);
-        }
-        fence_async();
-        __syncwarp();
-        if (ld.lane == 0) mbar_arrive(&sh.vfull[stage]);
-        if (N == 1) ld.load(s1, 1, 0, x[1], w[1]);
         u = u1;
         u1 = u2;
-        s = s1;
     }
+    cp_async_wait<0>();
 }
 
 // ---------------------------------------------------------------- warp 12
+// All lanes walk, one issues.
 template <int D>
 __device__ __forceinline__ void product_role(const KvAttend &a, Shared &sh, uint32_t qbuf, uint32_t kbuf, uint32_t vbuf) {
     using S = Shape<D>;
     constexpr uint32_t kScores = instruction(kN, false), kOut = instruction(D, true);
     const uint32_t tmem = sh.tmem, q0 = operand(qbuf, 16), k0 = operand(kbuf, 16), v0 = operand(vbuf, kBlk);
+    const bool lead = (threadIdx.x & 31) == 0;
     Walk<S::R> walk(sh);
     Piece p;
     uint32_t it = 0, pn[2] = {0, 0}, qn[2] = {0, 0};
@@ -468,48 +484,56 @@ __device__ __forceinline__ void product_role(const KvAttend &a, Shared &sh, uint
 #pragma unroll
         for (int r = 0; r < S::A; r++) on[r] = active<S::R>(a, p, r);
         auto scores = [&](int r, uint32_t stage) {
+            if (lead) {
+                uint32_t q = q0 + (r * S::kTile >> 4), k = k0 + stage * (S::kTile >> 4);
+#pragma unroll 1
+                for (int b = 0; b < D / 64; b++, q += kBlk >> 4, k += kBlk >> 4) {
 #pragma unroll
-            for (int k = 0; k < D / 16; k++) {
-                const uint32_t at = (k / 4 * kBlk + k % 4 * 32) >> 4;
-                mma_ss(tmem + 128 * r, q0 + (r * S::kTile >> 4) + at, k0 + stage * (S::kTile >> 4) + at, kScores, k > 0);
+                    for (int i = 0; i < 4; i++) mma_ss(tmem + 128 * r, q + 2 * i, k + 2 * i, kScores, b + i);
+                }
+                commit(&sh.sfull[r]);
             }
-            commit(&sh.sfull[r]);
         };
-#pragma unroll
-        for (int r = 0; r < S::A; r++)
-            if (on[r].x < on[r].y && !mbar_wait(&sh.qfull[r], qn[r]++ & 1)) return;
-        if (!mbar_wait(&sh.kfull[it % S::kStages], it / S::kStages & 1)) return;
-        fence_after();
-#pragma unroll
-        for (int r = 0; r < S::A; r++)
-            if (on[r].x == p.t0 && on[r].x < on[r].y) scores(r, it % S::kStages);
-        commit(&sh.kempty[it % S::kStages]);
-        for (int t = p.t0; t < p.t1; t++, it++) {
-            const uint32_t stage = it % S::kStages, next = (it + 1) % S::kStages;
-            if (!mbar_wait(&sh.vfull[stage], it / S::kStages & 1)) return;
-            bool got = false;
-#pragma unroll
+        for (int t = p.t0 - 1; t < p.t1; t++) {
+            const uint32_t stage = it % S::kStages, next = t < p.t0 ? stage : (it + 1) % S::kStages;
+            const uint32_t next_phase = (t < p.t0 ? it : it + 1) / S::kStages & 1;
+            if (t >= p.t0 && !mbar_wait_warp(&sh.vfull[stage], it / S::kStages & 1)) return;
+#pragma unroll 1
             for (int r = 0; r < S::A; r++) {
-                if (t >= on[r].x && t < on[r].y) {
-                    if (!mbar_wait(&sh.pfull[r], pn[r]++ & 1)) return;
+                const int2 mine = on[S::A == 2 ? r : 0];
+                if (t >= mine.x && t < mine.y) {
+                    if (!mbar_wait_warp(&sh.pfull[r], (r ? pn[1] : pn[0]) & 1)) return;
+                    if (r) pn[1]++;
+                    else pn[0]++;
                     fence_after();
+                    if (lead) {
+                        uint32_t v = v0 + stage * (S::kTile >> 4), s = tmem + 128 * r;
+#pragma unroll 1
+                        for (int b = 0; b < 2; b++, v += 4 * (2048 >> 4), s += 32) {
 #pragma unroll
-                    for (int k = 0; k < kN / 16; k++)
-                        mma_ts(tmem + S::kO + D * r, tmem + 128 * r + 8 * k, v0 + stage * (S::kTile >> 4) + k * (2048 >> 4), kOut,
-                               k > 0 || t > on[r].x);
-                    if (t == on[r].y - 1) commit(&sh.ofull[r]);
-                }
-                if (r == S::A - 1) commit(&sh.vempty[stage]);
-                if (t + 1 < p.t1) {
-                    if (!got) {
-                        if (!mbar_wait(&sh.kfull[next], (it + 1) / S::kStages & 1)) return;
-                        fence_after();
-                        got = true;
+                            for (int i = 0; i < 4; i++)
+                                mma_ts(tmem + S::kO + D * r, s + 8 * i, v + i * (2048 >> 4), kOut, b + i + (t - mine.x));
+                        }
+                        if (t == mine.y - 1) commit(&sh.ofull[r]);
                     }
-                    if (t + 1 >= on[r].x && t + 1 < on[r].y) scores(r, next);
-                    if (r == S::A - 1) commit(&sh.kempty[next]);
                 }
+                if (r == S::A - 1 && t >= p.t0 && lead) commit(&sh.vempty[stage]);
+                if (t + 1 < p.t1) {
+                    if (r == 0 && !mbar_wait_warp(&sh.kfull[next], next_phase)) return;
+                    if (t + 1 >= mine.x && t + 1 < mine.y) {
+                        if (t + 1 == mine.x) {
+                            if (!mbar_wait_warp(&sh.qfull[r], (r ? qn[1] : qn[0]) & 1)) return;
+                            if (r) qn[1]++;
+                            else qn[0]++;
+                        }
+                        fence_after();
+                        scores(r, next);
+                    }
+                    if (r == S::A - 1 && lead) commit(&sh.kempty[next]);
+                }
+                __syncwarp();
             }
+            if (t >= p.t0) it++;
         }
     }
 }
@@ -520,6 +544,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
+
+// The largest of x and v, NaNs aside.
+__device__ __forceinline__ float max_of(const float (&v)[32], float x) {
+    float a = max3(v[0], v[1], x), b = fmaxf(v[2], v[3]);
+#pragma unroll
+    for (int i = 4; i < 32; i += 4) {
+        a = max3(a, v[i], v[i + 1]);
+        b = max3(b, v[i + 2], v[i + 3]);
+    }
+    return fmaxf(a, b);
+}
+// The lowest n bits, none for n <= 0, all for n >= 32.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
 // Two at once: a * b + c, and a + b.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -564,7 +601,7 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
                 const uint32_t sign = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
                 const int up = query_exponent<T, D>(src);
                 f = fmaxf(f * exponent(-up), 1.17549435e-38f);  // not 0: a masked score times it is to stay -inf
-#pragma unroll 2
+#pragma unroll 8
                 for (int i = 0; i < D / 8; i++) {
                     uint4 x[1] = {reinterpret_cast<const uint4 *>(src)[i]};
                     query_codes_order<T, 1>(x, up);
@@ -581,29 +618,41 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
             for (int t = mine.x; t < mine.y; t++) {
                 if (!mbar_wait_warp(&sh.sfull[r], sn++ & 1)) return;
                 fence_after();
-                float s[kN];
-#pragma unroll
-                for (int i = 0; i < kN; i += 32) tmem_ld32(st + i, s + i);
                 const uint32_t flag = (it0 + t - p.t0) % kFlags;
                 const uint4 nans = sh.nans[flag], holes = sh.holes[flag];
-                wait_ld();
-                const int lo = seen.x - t * kN, hi = seen.y - t * kN;
-                if (all.x > t * kN || all.y < (t + 1) * kN || (nans.x | nans.y | nans.z | nans.w | holes.x | holes.y | holes.z | holes.w)) {
-                    const uint32_t hole = holes.x | holes.y << 2 | holes.z << 4 | holes.w << 6;
-                    const uint32_t nan[4] = {nans.x, nans.y, nans.z, nans.w};
+                float x = -INFINITY;
+                if (all.x <= t * kN && all.y >= (t + 1) * kN && !(nans.x | nans.y | nans.z | nans.w | holes.x | holes.y | holes.z | holes.w)) {
+                    float s[2][32];
+                    tmem_ld32(st, s[0]);
 #pragma unroll
-                    for (int i = 0; i < kN; i++) {
-                        if (i < lo || i >= hi || (hole >> (i / 16) & 1u)) s[i] = -INFINITY;
-                        else if (nan[i / 32] >> (i % 32) & 1u) s[i] = NAN;
+                    for (int i = 0; i < 4; i++) {
+                        wait_ld();
+                        if (i < 3) tmem_ld32(st + 32 * (i + 1), s[(i + 1) & 1]);
+                        x = max_of(s[i & 1], x);
                     }
+                } else {  // some row sees part of the unit: its scores go back masked
+                    const uint32_t hole = holes.x | holes.y << 2 | holes.z << 4 | holes.w << 6;
+                    const int lo = seen.x - t * kN, hi = seen.y - t * kN;
+#pragma unroll 1
+                    for (int i = 0; i < 4; i++) {
+                        float s[32];
+                        tmem_ld32(st + 32 * i, s);
+                        wait_ld();
+                        const uint32_t nan = i == 0 ? nans.x : i == 1 ? nans.y : i == 2 ? nans.z : nans.w;
+                        // bits of the 32 tokens that this row does not see
+                        uint32_t off = below(lo - 32 * i) | ~below(hi - 32 * i);
+                        off |= (hole >> (2 * i) & 1u ? 0x0000ffffu : 0u) | (hole >> (2 * i) & 2u ? 0xffff0000u : 0u);
+#pragma unroll
+                        for (int k = 0; k < 32; k++) {
+                            if (nan >> k & 1u) s[k] = NAN;
+                            if (off >> k & 1u) s[k] = -INFINITY;
+                        }
+                        x = max_of(s, x);
+                        tmem_st32(st + 32 * i, reinterpret_cast<const uint32_t *>(s));
+                    }
+                    wait_st();
                 }
-                float top[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                for (int i = 4; i < kN; i += 8)
-#pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        top[k] = i + 4 + k < kN ? max3(top[k], s[i + k], s[i + 4 + k]) : fmaxf(top[k], s[i + k]);
-                const float x = fmaxf(max3(top[0], top[1], top[2]), top[3]) * f;
+                x *= f;
                 if (__any_sync(kFull, x > m + kLazy)) {
                     const float next = fmaxf(m, x), keep = ex2(m - next);
                     m = next;
@@ -621,17 +670,23 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
                     }
                 }
                 float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+                {
+                    float s[2][32];
+                    tmem_ld32(st, s[0]);
 #pragma unroll
-                for (int i = 0; i < kN; i += 64) {
-                    uint32_t ph[32];
+                    for (int i = 0; i < 4; i++) {
+                        wait_ld();
+                        if (i < 3) tmem_ld32(st + 32 * (i + 1), s[(i + 1) & 1]);
+                        uint32_t ph[16];
 #pragma unroll
-                    for (int k = 0; k < 32; k++) {
-                        const float2 y = fma2(make_float2(s[i + 2 * k], s[i + 2 * k + 1]), make_float2(f, f), make_float2(-m, -m));
-                        const float2 e = make_float2(ex2(y.x), ex2(y.y));
-                        sum[k & 1] = add2(sum[k & 1], e);
-                        ph[k] = pack_h2(e.x, e.y);
+                        for (int k = 0; k < 16; k++) {
+                            const float2 y = fma2(make_float2(s[i & 1][2 * k], s[i & 1][2 * k + 1]), make_float2(f, f), make_float2(-m, -m));
+                            const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                            sum[k & 1] = add2(sum[k & 1], e);
+                            ph[k] = pack_h2(e.x, e.y);
+                        }
+                        tmem_st16(st + 16 * i, ph);
                     }
-                    tmem_st32(st + i / 2, ph);
                 }
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
@@ -720,17 +775,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     __syncthreads();
     fence_after();
 
-    // 512 threads x 128 registers: 2 x 184 + 96 + 48 for the four warpgroups.
+    // 512 threads x 128 registers: 2 x 152 + 112 + 96 for the four warpgroups.
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
         if (warp < 4 * S::A) softmax_role<D, T>(pp, sh, qbuf, warp >> 2);
     } else if (warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-        load_role<D>(pp.a, sh, kbuf, vbuf);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+        load_role<D>(pp.a, sh, kbuf, vbuf, vbuf + S::kStages * S::kTile);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        if (threadIdx.x == 12 * 32) product_role<D>(pp.a, sh, qbuf, kbuf, vbuf);
-        __syncwarp();
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        if (warp == 12) product_role<D>(pp.a, sh, qbuf, kbuf, vbuf);
     }
     fence_before();
     __syncthreads();
