@@ -20,8 +20,8 @@
 //                   128-byte-swizzled tiles of a ring in shared memory.  Eight
 //                   dimensions come out as 0 4 1 5 2 6 3 7; the queries are
 //                   stored in that order, the output's columns renamed.
-//   warp 12         one thread issues the products: S = Q K^T (K-major), then
-//                   O += P V with P from tensor memory and V token-major
+//   warps 12, 13    issue the products of row tile 0, 1: S = Q K^T (K-major),
+//                   then O += P V with P from tensor memory and V token-major
 //                   (MN-major B).
 // Unit t + 1's scores of a row tile are issued after unit t's output product
 // of the same tile, so the commit that announces them also says that this
@@ -76,7 +76,7 @@ struct PromptParams {
 };
 
 struct Shared {
-    uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], qfull[2], ofull[2];
+    uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2][2], qfull[2], ofull[2];
     uint4 nans[kFlags], holes[kFlags];  // by loading warp: NaN tokens; sub-tiles without a page
     uint32_t tmem;
     int b, head, qt, first;  // where this CTA's run begins
@@ -103,6 +103,17 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, float *v) {
         : "memory");
 #pragma unroll
     for (int i = 0; i < 32; i++) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t at, float *v) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t *r) {
     asm volatile(
@@ -134,6 +145,21 @@ __device__ __forceinline__ uint32_t operand(uint32_t at, uint32_t leading) { ret
 constexpr uint32_t kOperandHigh = 64u | 1u << 14 | 2u << 29;
 constexpr uint32_t instruction(int n, bool b_mn_major) {
     return (1u << 4) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// A warp's wait, all lanes testing; the same answer for all.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
+    if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = global_ns();
+    for (uint32_t i = 1;; i++) {
+        if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+        if ((i & 63u) == 0 && __any_sync(kFull, global_ns() - t0 > kWaitNs)) return false;
+    }
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
 }
 
 // D[tmem] (+)= A B, fp16, fp32 accumulator; A from shared or tensor memory.
@@ -398,7 +424,7 @@ struct Loader {
             uint32_t from = raw + i * S::kRawTile + S::raw_codes(which) + tok * (D / 2) + pair * 16;
             uint32_t word_at = (which ? value_words + i * D : raw + i * S::kRawTile + S::kRawWords) + (pair * kKvTile + tok) * 2;
             uint32_t to = tile + at * 128;
-#pragma unroll 1
+#pragma unroll 2
             for (int g = 0; g < D / 64; g++, from += 32, word_at += 4 * kKvTile, to += kBlk) {
                 uint16_t word;
                 asm volatile("ld.shared.u16 %0, [%1];" : "=h"(word) : "r"(word_at));
@@ -433,7 +459,7 @@ __device__ __forceinline__ void load_role(const KvAttend &a, Shared &sh, uint32_
         const uint32_t words0 = words + (it & 1) * 2 * D, words1 = words + (~it & 1) * 2 * D;
 #pragma unroll 1
         for (int which = 0; which < 2; which++) {
-            if (!mbar_wait_warp(which ? &sh.vempty[stage] : &sh.kempty[stage], phase ^ 1)) {
+            if (!warp_wait(which ? &sh.vempty[stage] : &sh.kempty[stage], phase ^ 1)) {
                 cp_async_wait<0>();
                 return;
             }
@@ -468,72 +494,57 @@ __device__ __forceinline__ void load_role(const KvAttend &a, Shared &sh, uint32_
     cp_async_wait<0>();
 }
 
-// ---------------------------------------------------------------- warp 12
-// All lanes walk, one issues.
+// ----------------------------------------------------------- warps 12, 13
+// One for each row tile, so that neither waits for the other's softmax.  All
+// lanes walk, one issues.
 template <int D>
-__device__ __forceinline__ void product_role(const KvAttend &a, Shared &sh, uint32_t qbuf, uint32_t kbuf, uint32_t vbuf) {
+__device__ __forceinline__ void product_role(const KvAttend &a, Shared &sh, uint32_t qbuf, uint32_t kbuf, uint32_t vbuf, int r) {
     using S = Shape<D>;
     constexpr uint32_t kScores = instruction(kN, false), kOut = instruction(D, true);
-    const uint32_t tmem = sh.tmem, q0 = operand(qbuf, 16), k0 = operand(kbuf, 16), v0 = operand(vbuf, kBlk);
-    const bool lead = (threadIdx.x & 31) == 0;
+    const uint32_t st = sh.tmem + 128 * r, ot = sh.tmem + S::kO + D * r;
+    const uint32_t q0 = operand(qbuf + r * S::kTile, 16), k0 = operand(kbuf, 16), v0 = operand(vbuf, kBlk);
+    const bool lead = elect_one();  // one thread throughout: a commit speaks for its own thread's products
     Walk<S::R> walk(sh);
     Piece p;
-    uint32_t it = 0, pn[2] = {0, 0}, qn[2] = {0, 0};
+    uint32_t it = 0, done = 0, pieces = 0;
     while (walk.next(a, p)) {
-        int2 on[S::A];
-#pragma unroll
-        for (int r = 0; r < S::A; r++) on[r] = active<S::R>(a, p, r);
-        auto scores = [&](int r, uint32_t stage) {
+        const int2 mine = active<S::R>(a, p, r);
+        for (int t = p.t0; t < p.t1; t++, it++) {
+            const uint32_t stage = it % S::kStages, phase = it / S::kStages & 1;
+            const bool on = t >= mine.x && t < mine.y;
+            if (!warp_wait(&sh.kfull[stage], phase)) return;
+            if (t == mine.x && on && !warp_wait(&sh.qfull[r], pieces++ & 1)) return;
+            fence_after();
             if (lead) {
-                uint32_t q = q0 + (r * S::kTile >> 4), k = k0 + stage * (S::kTile >> 4);
-#pragma unroll 1
-                for (int b = 0; b < D / 64; b++, q += kBlk >> 4, k += kBlk >> 4) {
+                if (on) {
+                    const uint32_t k = k0 + stage * (S::kTile >> 4);
 #pragma unroll
-                    for (int i = 0; i < 4; i++) mma_ss(tmem + 128 * r, q + 2 * i, k + 2 * i, kScores, b + i);
+                    for (int i = 0; i < D / 16; i++) {
+                        const uint32_t at = (i / 4 * kBlk + i % 4 * 32) >> 4;
+                        mma_ss(st, q0 + at, k + at, kScores, i);
+                    }
+                    commit(&sh.sfull[r]);
                 }
-                commit(&sh.sfull[r]);
+                commit(&sh.kempty[stage]);
             }
-        };
-        for (int t = p.t0 - 1; t < p.t1; t++) {
-            const uint32_t stage = it % S::kStages, next = t < p.t0 ? stage : (it + 1) % S::kStages;
-            const uint32_t next_phase = (t < p.t0 ? it : it + 1) / S::kStages & 1;
-            if (t >= p.t0 && !mbar_wait_warp(&sh.vfull[stage], it / S::kStages & 1)) return;
-#pragma unroll 1
-            for (int r = 0; r < S::A; r++) {
-                const int2 mine = on[S::A == 2 ? r : 0];
-                if (t >= mine.x && t < mine.y) {
-                    if (!mbar_wait_warp(&sh.pfull[r], (r ? pn[1] : pn[0]) & 1)) return;
-                    if (r) pn[1]++;
-                    else pn[0]++;
-                    fence_after();
-                    if (lead) {
-                        uint32_t v = v0 + stage * (S::kTile >> 4), s = tmem + 128 * r;
-#pragma unroll 1
-                        for (int b = 0; b < 2; b++, v += 4 * (2048 >> 4), s += 32) {
+            __syncwarp();
+            if (!warp_wait(&sh.vfull[stage], phase)) return;
 #pragma unroll
-                            for (int i = 0; i < 4; i++)
-                                mma_ts(tmem + S::kO + D * r, s + 8 * i, v + i * (2048 >> 4), kOut, b + i + (t - mine.x));
-                        }
-                        if (t == mine.y - 1) commit(&sh.ofull[r]);
+            for (int half = 0; half < 2; half++) {
+                if (on && !warp_wait(&sh.pfull[r][half], done & 1)) return;
+                fence_after();
+                if (lead) {
+                    if (on) {
+                        const uint32_t v = v0 + stage * (S::kTile >> 4);
+#pragma unroll
+                        for (int i = 4 * half; i < 4 * half + 4; i++) mma_ts(ot, st + 8 * i, v + i * (2048 >> 4), kOut, i + (t - mine.x));
+                        if (half && t == mine.y - 1) commit(&sh.ofull[r]);
                     }
-                }
-                if (r == S::A - 1 && t >= p.t0 && lead) commit(&sh.vempty[stage]);
-                if (t + 1 < p.t1) {
-                    if (r == 0 && !mbar_wait_warp(&sh.kfull[next], next_phase)) return;
-                    if (t + 1 >= mine.x && t + 1 < mine.y) {
-                        if (t + 1 == mine.x) {
-                            if (!mbar_wait_warp(&sh.qfull[r], (r ? qn[1] : qn[0]) & 1)) return;
-                            if (r) qn[1]++;
-                            else qn[0]++;
-                        }
-                        fence_after();
-                        scores(r, next);
-                    }
-                    if (r == S::A - 1 && lead) commit(&sh.kempty[next]);
+                    if (half) commit(&sh.vempty[stage]);
                 }
                 __syncwarp();
             }
-            if (t >= p.t0) it++;
+            done += on;
         }
     }
 }
@@ -545,16 +556,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-// The largest of x and v, NaNs aside.
-__device__ __forceinline__ float max_of(const float (&v)[32], float x) {
-    float a = max3(v[0], v[1], x), b = fmaxf(v[2], v[3]);
-#pragma unroll
-    for (int i = 4; i < 32; i += 4) {
-        a = max3(a, v[i], v[i + 1]);
-        b = max3(b, v[i + 2], v[i + 3]);
-    }
-    return fmaxf(a, b);
-}
 // The lowest n bits, none for n <= 0, all for n >= 32.
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
@@ -575,13 +576,65 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return r;
 }
 
+// A warp's 32 rows of a row tile between global and shared memory, where they
+// lie as the operand does: LANES lanes take a row's 16-byte chunks, so that a
+// row's bytes go together.
+template <int D>
+struct Rows {
+    static constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;
+    const int lane = threadIdx.x & 31, chunk = lane % LANES, sub = lane / LANES;
+    __device__ __forceinline__ uint32_t at(uint32_t tile, int row) const {  // of this lane's chunk
+        return tile + chunk / 8 * kBlk + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+    }
+};
+
+// The queries, into the row tile; returns what the scores of this thread's
+// row are to be multiplied by.  A negative scale becomes the queries' sign, so
+// that the largest score stays the largest.
+template <int D, typename T>
+__device__ __forceinline__ float load_queries(const KvAttend &a, const Piece &p, int first, int end, int row0, uint32_t tile) {
+    using W = Rows<D>;
+    const W w;
+    const uint32_t sign = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+    int up = 0;
+#pragma unroll 1
+    for (int i0 = 0; i0 < 32; i0 += 8 * W::AT_ONCE) {
+        uint4 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const int rho = min(first + row0 + i0 + i * W::AT_ONCE + w.sub, end - 1);
+            x[i] = reinterpret_cast<const uint4 *>((const T *)a.q + row_at(a, p.s, p.head, rho, a.q_token, a.q_head))[w.chunk];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            int e = 0;
+            if constexpr (!std::is_same<T, __half>::value) {
+                uint32_t top = top_bits(x[i], 0);
+#pragma unroll
+                for (int m = 1; m < W::LANES; m <<= 1) top = max(top, __shfl_xor_sync(kFull, top, m));
+                e = up_of(top);
+                const int of = __shfl_sync(kFull, e, w.lane % W::AT_ONCE * W::LANES);
+                if (w.lane / W::AT_ONCE == i0 / W::AT_ONCE + i) up = of;
+            }
+            uint4 y[1] = {x[i]};
+            query_codes_order<T, 1>(y, e);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(w.at(tile, row0 + i0 + i * W::AT_ONCE + w.sub)),
+                         "r"(y[0].x ^ sign), "r"(y[0].y ^ sign), "r"(y[0].z ^ sign), "r"(y[0].w ^ sign)
+                         : "memory");
+        }
+    }
+    // not 0: a masked score times it is to stay -inf
+    return fmaxf(fabsf(a.scale_log2) * exponent(-up), 1.17549435e-38f);
+}
+
 template <int D, typename T>
 __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh, uint32_t qbuf, int r) {
     using S = Shape<D>;
     const KvAttend &a = pp.a;
-    const int row = threadIdx.x & 127;
-    const uint32_t lanes = (uint32_t)(row & 96) << 16;  // this warp's quarter of tensor memory
-    const uint32_t st = sh.tmem + 128 * r + lanes, ot = sh.tmem + S::kO + D * r + lanes;
+    const int row = threadIdx.x & 127, row0 = row & 96;
+    const uint32_t lanes = (uint32_t)row0 << 16;  // this warp's quarter of tensor memory
+    const uint32_t st = sh.tmem + 128 * r + lanes, ot = sh.tmem + S::kO + D * r + lanes, tile = qbuf + r * S::kTile;
+    const bool lead = (threadIdx.x & 31) == 0;
     Walk<S::R> walk(sh);
     Piece p;
     uint32_t it0 = 0, sn = 0, on = 0;
@@ -589,48 +642,23 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
         const int2 mine = active<S::R>(a, p, r);
         const int first = p.qt * S::R + 128 * r, rho = first + row;
         const int end = min(first + 128, p.s.rows * a.share);
-        float m = kNoMax, l = 0.0f, o_scale = 0.0f;
+        float m = kNoMax, l = 0.0f;
         if (mine.x < mine.y) {
-            const int my = min(rho, end - 1);
-            const int2 seen = seen_by(a, p.s, my), all = make_int2(seen_by(a, p.s, end - 1).x, seen_by(a, p.s, first).y);
-            // The queries, into the tile's rows.  A negative scale is the
-            // queries' sign, so that the largest score stays the largest.
-            float f = fabsf(a.scale_log2);
-            {
-                const T *src = (const T *)a.q + row_at(a, p.s, p.head, my, a.q_token, a.q_head);
-                const uint32_t sign = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-                const int up = query_exponent<T, D>(src);
-                f = fmaxf(f * exponent(-up), 1.17549435e-38f);  // not 0: a masked score times it is to stay -inf
-#pragma unroll 8
-                for (int i = 0; i < D / 8; i++) {
-                    uint4 x[1] = {reinterpret_cast<const uint4 *>(src)[i]};
-                    query_codes_order<T, 1>(x, up);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                     qbuf + r * S::kTile + i / 8 * kBlk + row * 128 + (((i & 7) ^ (row & 7)) << 4)),
-                                 "r"(x[0].x ^ sign), "r"(x[0].y ^ sign), "r"(x[0].z ^ sign), "r"(x[0].w ^ sign)
-                                 : "memory");
-                }
-            }
+            const int2 seen = seen_by(a, p.s, min(rho, end - 1));
+            const int all_lo = seen_by(a, p.s, end - 1).x, all_hi = seen_by(a, p.s, first).y;
+            const float f = load_queries<D, T>(a, p, first, end, row0, tile);
             fence_async();
             fence_before();
-            mbar_arrive(&sh.qfull[r]);
+            __syncwarp();
+            if (lead) mbar_arrive(&sh.qfull[r]);
 
             for (int t = mine.x; t < mine.y; t++) {
-                if (!mbar_wait_warp(&sh.sfull[r], sn++ & 1)) return;
+                if (!warp_wait(&sh.sfull[r], sn++ & 1)) return;
                 fence_after();
                 const uint32_t flag = (it0 + t - p.t0) % kFlags;
                 const uint4 nans = sh.nans[flag], holes = sh.holes[flag];
-                float x = -INFINITY;
-                if (all.x <= t * kN && all.y >= (t + 1) * kN && !(nans.x | nans.y | nans.z | nans.w | holes.x | holes.y | holes.z | holes.w)) {
-                    float s[2][32];
-                    tmem_ld32(st, s[0]);
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        wait_ld();
-                        if (i < 3) tmem_ld32(st + 32 * (i + 1), s[(i + 1) & 1]);
-                        x = max_of(s[i & 1], x);
-                    }
-                } else {  // some row sees part of the unit: its scores go back masked
+                if (all_lo > t * kN || all_hi < (t + 1) * kN || (nans.x | nans.y | nans.z | nans.w | holes.x | holes.y | holes.z | holes.w)) {
+                    // some row sees part of the unit: its scores go back masked
                     const uint32_t hole = holes.x | holes.y << 2 | holes.z << 4 | holes.w << 6;
                     const int lo = seen.x - t * kN, hi = seen.y - t * kN;
 #pragma unroll 1
@@ -647,82 +675,87 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
                             if (nan >> k & 1u) s[k] = NAN;
                             if (off >> k & 1u) s[k] = -INFINITY;
                         }
-                        x = max_of(s, x);
                         tmem_st32(st + 32 * i, reinterpret_cast<const uint32_t *>(s));
                     }
                     wait_st();
                 }
-                x *= f;
+                float s[kN];
+#pragma unroll
+                for (int i = 0; i < kN; i += 32) tmem_ld32(st + i, s + i);
+                wait_ld();
+                float top[4] = {max3(s[0], s[1], s[2]), max3(s[32], s[33], s[34]), max3(s[64], s[65], s[66]), max3(s[96], s[97], s[98])};
+#pragma unroll
+                for (int i = 3; i < 31; i += 2)
+#pragma unroll
+                    for (int k = 0; k < 4; k++) top[k] = max3(top[k], s[32 * k + i], s[32 * k + i + 1]);
+                const float x = max3(max3(top[0], top[1], top[2]), max3(top[3], s[31], s[63]), fmaxf(s[95], s[127])) * f;
                 if (__any_sync(kFull, x > m + kLazy)) {
                     const float next = fmaxf(m, x), keep = ex2(m - next);
                     m = next;
                     l *= keep;
                     if (t > mine.x) {
 #pragma unroll 1
-                        for (int i = 0; i < D; i += 32) {
-                            float o[32];
-                            tmem_ld32(ot + i, o);
+                        for (int i = 0; i < D; i += 16) {
+                            float o[16];
+                            tmem_ld16(ot + i, o);
                             wait_ld();
 #pragma unroll
-                            for (int k = 0; k < 32; k++) o[k] *= keep;
-                            tmem_st32(ot + i, reinterpret_cast<const uint32_t *>(o));
+                            for (int k = 0; k < 16; k++) o[k] *= keep;
+                            tmem_st16(ot + i, reinterpret_cast<const uint32_t *>(o));
                         }
                     }
                 }
                 float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
-                {
-                    float s[2][32];
-                    tmem_ld32(st, s[0]);
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        wait_ld();
-                        if (i < 3) tmem_ld32(st + 32 * (i + 1), s[(i + 1) & 1]);
-                        uint32_t ph[16];
+                for (int half = 0; half < 2; half++) {  // the product over the first 64 tokens starts meanwhile
+                    uint32_t ph[32];
 #pragma unroll
-                        for (int k = 0; k < 16; k++) {
-                            const float2 y = fma2(make_float2(s[i & 1][2 * k], s[i & 1][2 * k + 1]), make_float2(f, f), make_float2(-m, -m));
-                            const float2 e = make_float2(ex2(y.x), ex2(y.y));
-                            sum[k & 1] = add2(sum[k & 1], e);
-                            ph[k] = pack_h2(e.x, e.y);
-                        }
-                        tmem_st16(st + 16 * i, ph);
+                    for (int k = 0; k < 32; k++) {
+                        const float2 y =
+                            fma2(make_float2(s[64 * half + 2 * k], s[64 * half + 2 * k + 1]), make_float2(f, f), make_float2(-m, -m));
+                        const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                        sum[k & 1] = add2(sum[k & 1], e);
+                        ph[k] = pack_h2(e.x, e.y);
                     }
+                    tmem_st32(st + 32 * half, ph);
+                    wait_st();
+                    fence_before();
+                    __syncwarp();
+                    if (lead) mbar_arrive(&sh.pfull[r][half]);
                 }
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
-                wait_st();
-                fence_before();
-                mbar_arrive(&sh.pfull[r]);
             }
-            if (!mbar_wait_warp(&sh.ofull[r], on++ & 1)) return;
+            if (!warp_wait(&sh.ofull[r], on++ & 1)) return;
             fence_after();
-            o_scale = 1.0f;
         }
         it0 += p.t1 - p.t0;
 
-        // The rows' outputs, or the piece's partial result.
+        // The rows' outputs, by way of the queries' place, or the piece's
+        // partial result.
         const bool whole = p.begins && p.rest == 0;
         float *part = pp.parts + (2 * blockIdx.x + (p.begins ? 1 : 0)) * kv_part_floats<D, S::R>();
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        T *dst = (T *)a.out + (rho < end ? row_at(a, p.s, p.head, rho, a.out_token, a.out_head) : 0);
 #pragma unroll 1
-        for (int i = 0; i < D; i += 32) {
-            float o[32];
-            if (o_scale != 0.0f) {
-                tmem_ld32(ot + i, o);
+        for (int i = 0; i < D; i += 16) {
+            float o[16];
+            if (mine.x < mine.y) {
+                tmem_ld16(ot + i, o);
                 wait_ld();
             } else {
 #pragma unroll
-                for (int k = 0; k < 32; k++) o[k] = 0.0f;
+                for (int k = 0; k < 16; k++) o[k] = 0.0f;
             }
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) {
+            for (int k = 0; k < 16; k += 8) {
                 // columns k .. k + 7 are dimensions 0 4 1 5 2 6 3 7
                 if (whole) {
-                    if (rho < end)
-                        *reinterpret_cast<uint4 *>(dst + i + k) =
-                            make_uint4(pack_out<T>(o[k] * inv, o[k + 2] * inv), pack_out<T>(o[k + 4] * inv, o[k + 6] * inv),
-                                       pack_out<T>(o[k + 1] * inv, o[k + 3] * inv), pack_out<T>(o[k + 5] * inv, o[k + 7] * inv));
+                    const int chunk = (i + k) / 8;
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     tile + chunk / 8 * kBlk + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)),
+                                 "r"(pack_out<T>(o[k] * inv, o[k + 2] * inv)), "r"(pack_out<T>(o[k + 4] * inv, o[k + 6] * inv)),
+                                 "r"(pack_out<T>(o[k + 1] * inv, o[k + 3] * inv)), "r"(pack_out<T>(o[k + 5] * inv, o[k + 7] * inv))
+                                 : "memory");
                 } else {
                     float4 *to = reinterpret_cast<float4 *>(part + (128 * r + row) * D + i + k);
                     to[0] = make_float4(o[k], o[k + 2], o[k + 4], o[k + 6]);
@@ -731,6 +764,17 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
             }
         }
         if (whole) {
+            using W = Rows<D>;
+            const W w;
+            __syncwarp();
+#pragma unroll 4
+            for (int i = 0; i < 32; i += W::AT_ONCE) {
+                const int of = row0 + i + w.sub;
+                const uint4 x = lds128(w.at(tile, of));
+                if (first + of < end)
+                    reinterpret_cast<uint4 *>((T *)a.out + row_at(a, p.s, p.head, first + of, a.out_token, a.out_head))[w.chunk] = x;
+            }
+            __syncwarp();
             if (a.lse && rho < end) a.lse[row_at(a, p.s, p.head, rho, a.q_heads, 1)] = lse_of(m, l);
         } else {
             part[S::R * D + 128 * r + row] = m;
@@ -756,12 +800,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         for (int i = 0; i < 2; i++) {
             mbar_init(&sh.kfull[i], 4);
             mbar_init(&sh.vfull[i], 4);
-            mbar_init(&sh.kempty[i], 1);
-            mbar_init(&sh.vempty[i], 1);
+            mbar_init(&sh.kempty[i], S::A);
+            mbar_init(&sh.vempty[i], S::A);
             mbar_init(&sh.sfull[i], 1);
             mbar_init(&sh.ofull[i], 1);
-            mbar_init(&sh.pfull[i], 128);
-            mbar_init(&sh.qfull[i], 128);
+            mbar_init(&sh.pfull[i][0], 4);
+            mbar_init(&sh.pfull[i][1], 4);
+            mbar_init(&sh.qfull[i], 4);
         }
         fence_mbar_init();
         pp.carries[blockIdx.x].valid = 0;
@@ -775,16 +820,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     __syncthreads();
     fence_after();
 
-    // 512 threads x 128 registers: 2 x 152 + 112 + 96 for the four warpgroups.
+    // 512 threads x 128 registers: 2 x 184 + 88 + 56 for the four warpgroups.
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         if (warp < 4 * S::A) softmax_role<D, T>(pp, sh, qbuf, warp >> 2);
     } else if (warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         load_role<D>(pp.a, sh, kbuf, vbuf, vbuf + S::kStages * S::kTile);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-        if (warp == 12) product_role<D>(pp.a, sh, qbuf, kbuf, vbuf);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp < 12 + S::A) product_role<D>(pp.a, sh, qbuf, kbuf, vbuf, warp - 12);
     }
     fence_before();
     __syncthreads();
