@@ -144,34 +144,60 @@ inline KvCarry *kv_carries(void *workspace) {
     return (KvCarry *)((uint8_t *)workspace + kMaxCtas * 2 * kv_part_floats<D, R>() * 4);
 }
 
-// Joins them, eight rows a block, always in the same order.
-constexpr int kJoinRows = 8;
+// Joins them, a warp a row and up to four rows a warp, always in the same
+// order.
+template <int R>
+__host__ __device__ constexpr int join_rows() { return R >= 32 ? 32 : 8; }  // of a block
 template <int D, int R, typename T>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ KvAttend a, const float *__restrict__ parts,
                                                    const KvCarry *__restrict__ carries) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int E = D / 32, N = join_rows<R>() / 8;  // elements of a lane, rows of a warp
     const KvCarry c = carries[blockIdx.x];
     if (!c.valid) return;
     const KvSeq s = kv_seq(a, c.b);
-    auto part = [&](int i) { return parts + (2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * kv_part_floats<D, R>(); };
-    for (int k = threadIdx.x; k < kJoinRows * D / 2; k += 256) {
-        const int row = blockIdx.y * kJoinRows + k / (D / 2), d = k % (D / 2) * 2, rho = c.qt * R + row;
-        if (rho >= s.rows * a.share) return;
-        float top = kNoMax, sum = 0.0f, x = 0.0f, y = 0.0f;
-        for (int i = 0; i <= c.more; i++) top = fmaxf(top, part(i)[R * D + row]);
-#pragma unroll 4
-        for (int i = 0; i <= c.more; i++) {
-            const float *src = part(i);
-            const float f = ex2(src[R * D + row] - top);
-            const float2 v = *reinterpret_cast<const float2 *>(src + row * D + d);
-            sum += f * src[R * D + R + row];
-            x += f * v.x;
-            y += f * v.y;
+    const int lane = threadIdx.x & 31, row0 = blockIdx.y * join_rows<R>() + (threadIdx.x >> 5);
+    float top[N], sum[N], x[N][E];
+#pragma unroll
+    for (int n = 0; n < N; n++) {
+        top[n] = kNoMax;
+        sum[n] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; e++) x[n][e] = 0.0f;
+    }
+    for (int i = 0; i <= c.more; i++) {
+        const float *part = parts + (2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * kv_part_floats<D, R>();
+        float v[N][E], m[N], l[N];
+#pragma unroll
+        for (int n = 0; n < N; n++) {
+            const int row = row0 + 8 * n;
+            m[n] = part[R * D + row];
+            l[n] = part[R * D + R + row];
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                const float2 f = *reinterpret_cast<const float2 *>(part + row * D + lane * E + e);
+                v[n][e] = f.x;
+                v[n][e + 1] = f.y;
+            }
         }
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        *reinterpret_cast<uint32_t *>((T *)a.out + row_at(a, s, c.head, rho, a.out_token, a.out_head) + d) =
-            pack_out<T>(x * inv, y * inv);
-        if (a.lse && d == 0) a.lse[row_at(a, s, c.head, rho, a.q_heads, 1)] = lse_of(top, sum);
+#pragma unroll
+        for (int n = 0; n < N; n++) {
+            const float next = fmaxf(top[n], m[n]), keep = ex2(top[n] - next), f = ex2(m[n] - next);
+            top[n] = next;
+            sum[n] = sum[n] * keep + l[n] * f;
+#pragma unroll
+            for (int e = 0; e < E; e++) x[n][e] = x[n][e] * keep + v[n][e] * f;
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < N; n++) {
+        const int rho = c.qt * R + row0 + 8 * n;
+        if (rho >= s.rows * a.share) continue;
+        const float inv = sum[n] == 0.0f ? 0.0f : 1.0f / sum[n];
+        T *to = (T *)a.out + row_at(a, s, c.head, rho, a.out_token, a.out_head) + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) reinterpret_cast<uint32_t *>(to)[e / 2] = pack_out<T>(x[n][e] * inv, x[n][e + 1] * inv);
+        if (a.lse && lane == 0) a.lse[row_at(a, s, c.head, rho, a.q_heads, 1)] = lse_of(top[n], sum[n]);
     }
 }
 
@@ -181,7 +207,7 @@ int launch_join(const KvAttend &a, const float *parts, const KvCarry *carries, i
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, R / kJoinRows);
+    cfg.gridDim = dim3(ctas, R / join_rows<R>());
     cfg.blockDim = 256;
     cfg.stream = st;
     cfg.attrs = attr;

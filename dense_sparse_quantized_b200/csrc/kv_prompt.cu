@@ -4,9 +4,10 @@
 //
 // Work.  A job is (sequence, kv head, tile of R query rows), a row being one
 // (query token, query head of the group) pair.  Its tokens are cut into units
-// of 128, of which only those that some row sees count; the units of all
-// jobs, in order, are dealt to the CTAs in equal runs, wherever jobs begin and
-// end.  What a job's runs leave is joined through the workspace, in order.
+// of 128, of which only those that some row sees count.  A job costs its units
+// and kPieceCost more; the costs of all jobs, in order, are dealt to the CTAs
+// in equal runs, wherever jobs begin and end.  What a job's pieces leave is
+// joined through the workspace, in order.
 //
 // A CTA works on two row tiles of 128 at once (one at 256 dimensions), so that
 // one tile's products run under the other's softmax:
@@ -49,6 +50,7 @@ constexpr int kN = 128;          // tokens of a unit
 constexpr int kBlk = 128 * 128;  // bytes of 128 rows x 64 dimensions, swizzled
 constexpr int kThreads = 512;
 constexpr int kFlags = 4;        // units whose flags are kept
+constexpr int kPieceCost = 2;    // units' time that a piece takes besides its units: queries in, outputs out
 
 template <int D_>
 struct Shape {
@@ -79,9 +81,9 @@ struct Shared {
     uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2][2], qfull[2], ofull[2];
     uint4 nans[kFlags], holes[kFlags];  // by loading warp: NaN tokens; sub-tiles without a page
     uint32_t tmem;
-    int b, head, qt, first;  // where this CTA's run begins
-    int left;                // units of it
-    int64_t run, end;        // units of every CTA's run; where this one ends among all units
+    int b, head, qt, first;  // where this CTA's run begins: the job, and how much of its cost lies before
+    int left;                // cost of the run
+    int64_t run, end;        // of every CTA's; where this one ends among all
 };
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -212,18 +214,20 @@ struct Walk {
                 }
                 continue;
             }
+            // [first, end) of the job's cost, kPieceCost of it before its units
             const int2 u = units_of<R>(a, p.s, qt);
+            const int cost = kPieceCost + u.y - u.x, end = min(cost, first + left);
             p.b = b;
             p.head = head;
             p.qt = qt;
-            p.t0 = u.x + first;
-            p.t1 = min(u.y, p.t0 + left);
-            p.rest = u.y - p.t1;
-            p.begins = first == 0;
-            left -= p.t1 - p.t0;
+            p.t0 = u.x + max(0, first - kPieceCost);
+            p.t1 = u.x + max(0, end - kPieceCost);
+            p.rest = cost - end;
+            p.begins = first <= kPieceCost;
+            left -= end - first;
             first = 0;
             qt++;
-            return true;
+            if (p.t0 < p.t1) return true;
         }
         return false;
     }
@@ -242,13 +246,13 @@ __device__ __forceinline__ int2 active(const KvAttend &a, const Piece &p, int r)
 template <int R>
 __device__ __forceinline__ void find_run(const KvAttend &a, Shared &sh) {
     const int lane = threadIdx.x & 31;
-    auto head_units = [&](int b) -> int64_t {  // of one kv head of sequence b
+    auto head_cost = [&](int b) -> int64_t {  // of one kv head of sequence b
         const KvSeq s = kv_seq(a, b);
         const int tiles = tiles_of<R>(a, s);
         int64_t n = 0;
         for (int qt = 0; qt < tiles; qt++) {
             const int2 u = units_of<R>(a, s, qt);
-            n += u.y - u.x;
+            n += kPieceCost + u.y - u.x;
         }
         return n;
     };
@@ -267,11 +271,11 @@ __device__ __forceinline__ void find_run(const KvAttend &a, Shared &sh) {
             const int tiles = tiles_of<R>(a, s);
             for (int qt = lane; qt < tiles; qt += 32) {
                 const int2 u = units_of<R>(a, s, qt);
-                total += (int64_t)(u.y - u.x) * a.c.kv_heads;
+                total += (int64_t)(kPieceCost + u.y - u.x) * a.c.kv_heads;
             }
         }
     } else
-        for (int b = lane; b < a.batch; b += 32) total += head_units(b) * a.c.kv_heads;
+        for (int b = lane; b < a.batch; b += 32) total += head_cost(b) * a.c.kv_heads;
 #pragma unroll
     for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(kFull, total, m);
     const int64_t run = (total + gridDim.x - 1) / gridDim.x;
@@ -279,7 +283,7 @@ __device__ __forceinline__ void find_run(const KvAttend &a, Shared &sh) {
     int64_t before = 0;
     int b = a.batch, head = 0, qt = 0, first = 0;
     for (int b0 = 0; b0 < a.batch && u0 < u1; b0 += 32) {
-        const int64_t w = b0 + lane < a.batch ? head_units(b0 + lane) : 0, sum = scan(w * a.c.kv_heads);
+        const int64_t w = b0 + lane < a.batch ? head_cost(b0 + lane) : 0, sum = scan(w * a.c.kv_heads);
         const uint32_t past = __ballot_sync(kFull, before + sum > u0);
         if (past) {
             const int l = __ffs(past) - 1;
@@ -299,7 +303,7 @@ __device__ __forceinline__ void find_run(const KvAttend &a, Shared &sh) {
             int w = 0;
             if (q0 + lane < tiles) {
                 const int2 u = units_of<R>(a, s, q0 + lane);
-                w = u.y - u.x;
+                w = kPieceCost + u.y - u.x;
             }
             const int64_t sum = scan(w);
             const uint32_t past = __ballot_sync(kFull, before + sum > u0);
@@ -594,19 +598,20 @@ struct Rows {
 template <int D, typename T>
 __device__ __forceinline__ float load_queries(const KvAttend &a, const Piece &p, int first, int end, int row0, uint32_t tile) {
     using W = Rows<D>;
+    constexpr int N = D == 64 ? 8 : 16;  // loads under way
     const W w;
     const uint32_t sign = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
     int up = 0;
 #pragma unroll 1
-    for (int i0 = 0; i0 < 32; i0 += 8 * W::AT_ONCE) {
-        uint4 x[8];
+    for (int i0 = 0; i0 < 32; i0 += N * W::AT_ONCE) {
+        uint4 x[N];
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
+        for (int i = 0; i < N; i++) {
             const int rho = min(first + row0 + i0 + i * W::AT_ONCE + w.sub, end - 1);
             x[i] = reinterpret_cast<const uint4 *>((const T *)a.q + row_at(a, p.s, p.head, rho, a.q_token, a.q_head))[w.chunk];
         }
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
+        for (int i = 0; i < N; i++) {
             int e = 0;
             if constexpr (!std::is_same<T, __half>::value) {
                 uint32_t top = top_bits(x[i], 0);
@@ -651,6 +656,15 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
             fence_before();
             __syncwarp();
             if (lead) mbar_arrive(&sh.qfull[r]);
+            {  // the next piece's queries come to L2 meanwhile
+                Walk<S::R> ahead = walk;
+                Piece q;
+                if (ahead.next(a, q)) {
+                    const int64_t at = row_at(a, q.s, q.head, min(q.qt * S::R + 128 * r + row, q.s.rows * a.share - 1), a.q_token, a.q_head);
+#pragma unroll
+                    for (int i = 0; i < D; i += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"((const T *)a.q + at + i));
+                }
+            }
 
             for (int t = mine.x; t < mine.y; t++) {
                 if (!warp_wait(&sh.sfull[r], sn++ & 1)) return;
@@ -816,6 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     } else if (warp == 8)
         find_run<S::R>(pp.a, sh);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // join_kernel waits for this one's end
     fence_before();
     __syncthreads();
     fence_after();

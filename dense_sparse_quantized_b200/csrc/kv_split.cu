@@ -133,6 +133,8 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
     float *const head_part = reinterpret_cast<float *>(smem + warp * S::kWarp + RING * S::kTile);
     float *const tail_part = reinterpret_cast<float *>(smem + warp * S::kWarp);
 
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // join_kernel waits for this one's end
+
     // Total work, and this warp's run [u, u_end) of it.
     int64_t total = 0;
     for (int b = lane; b < a.batch; b += 32) total += jobs_of<R>(a, b).weight;
