@@ -22,33 +22,6 @@ __host__ __device__ constexpr int kv_tile_bytes(int D) { return kKvTile * (D + D
 __host__ __device__ constexpr int kv_codes(int D, int which) { return which * kKvTile * D / 2; }
 __host__ __device__ constexpr int kv_words(int D, int which) { return kKvTile * D + which * kKvTile * D / 16; }
 
-struct KvView {
-    const uint8_t *cache;
-    int kv_heads, page_tokens, page_tiles, pages;
-    int slots;  // pages * page_tokens < 2^31
-};
-
-inline int kv_check_desc(const dsq_kv_desc *d) {
-    if (!d || d->kv_heads < 1 || d->page_tokens < 1 || d->page_tokens % kKvTile || d->pages < 0 || d->device < 0)
-        return DSQ_ERR_INVALID_ARG;
-    if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256) return DSQ_ERR_UNSUPPORTED;
-    if ((int64_t)d->pages * d->page_tokens >= ((int64_t)1 << 31)) return DSQ_ERR_UNSUPPORTED;
-    return DSQ_OK;
-}
-
-inline KvView kv_view(const dsq_kv_desc *d, const void *cache) {
-    return {(const uint8_t *)cache, d->kv_heads, d->page_tokens, d->page_tokens / kKvTile, d->pages,
-            d->pages * d->page_tokens};
-}
-
-// Where the tile with token offset `off` of (page, head) starts.
-__device__ __forceinline__ int64_t kv_tile_at(const KvView &c, int D, int page, int head, int off) {
-    return (((int64_t)page * c.kv_heads + head) * c.page_tiles + off / kKvTile) * kv_tile_bytes(D);
-}
-
-// A group's word: scale (fp16, low four bits zero) and zero point.
-__device__ __forceinline__ float kv_scale(uint32_t word) { return __half2float(__ushort_as_half((uint16_t)(word & 0xfff0u))); }
-
 // Division of 0 <= n < 2^31 by a number the host knows: with l = ceil(log2 d)
 // and mul = ceil(2^(31 + l) / d), n mul / 2^(31 + l) exceeds n / d by less than
 // n / 2^(31 + l) < 1 / d.
@@ -62,9 +35,37 @@ inline KvDivisor kv_divisor(int d) {
     return {(uint32_t)(((1ull << (31 + l)) + d - 1) / d), 31 + l, (uint32_t)d};
 }
 
+struct KvView {
+    const uint8_t *cache;
+    int kv_heads, page_tokens, page_tiles, pages;
+    int slots;          // pages * page_tokens < 2^31
+    KvDivisor page_by;  // by tokens of a page
+};
+
+inline int kv_check_desc(const dsq_kv_desc *d) {
+    if (!d || d->kv_heads < 1 || d->page_tokens < 1 || d->page_tokens % kKvTile || d->pages < 0 || d->device < 0)
+        return DSQ_ERR_INVALID_ARG;
+    if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256) return DSQ_ERR_UNSUPPORTED;
+    if ((int64_t)d->pages * d->page_tokens >= ((int64_t)1 << 31)) return DSQ_ERR_UNSUPPORTED;
+    return DSQ_OK;
+}
+
+inline KvView kv_view(const dsq_kv_desc *d, const void *cache) {
+    return {(const uint8_t *)cache, d->kv_heads, d->page_tokens, d->page_tokens / kKvTile, d->pages,
+            d->pages * d->page_tokens, kv_divisor(d->page_tokens)};
+}
+
+// Where the tile with token offset `off` of (page, head) starts.
+__device__ __forceinline__ int64_t kv_tile_at(const KvView &c, int D, int page, int head, int off) {
+    return (((int64_t)page * c.kv_heads + head) * c.page_tiles + off / kKvTile) * kv_tile_bytes(D);
+}
+
+// A group's word: scale (fp16, low four bits zero) and zero point.
+__device__ __forceinline__ float kv_scale(uint32_t word) { return __half2float(__ushort_as_half((uint16_t)(word & 0xfff0u))); }
+
 struct KvAttend {
     KvView c;
-    KvDivisor share_by, page_by;  // by heads of a group, by tiles of a page
+    KvDivisor share_by, tiles_by;  // by heads of a group, by tiles of a page
     const void *q;
     void *out;
     float *lse;
@@ -106,6 +107,28 @@ inline bool kv_rows_apart(int64_t tokens, int64_t heads, int64_t token, int64_t 
     if (tokens <= 1) return head >= D;
     if (heads <= 1) return token >= D;
     return (head >= D && token >= (heads - 1) * head + D) || (token >= D && head >= (tokens - 1) * token + D);
+}
+
+// The kernels are launched early, while the one before them in the stream still
+// runs (programmatic dependent launch): they touch no memory of the caller's
+// before kv_after_previous(), which waits until that one has ended, and let
+// the next one be launched as early.
+__device__ __forceinline__ void kv_after_previous() {
+    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+}
+template <typename... Params, typename... Args>
+int kv_launch(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, const Args &...args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? DSQ_OK : DSQ_ERR_CUDA;
 }
 
 // Sets a kernel's shared-memory limit once per device (a call per launch

@@ -65,7 +65,7 @@ extern "C" int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_
     k.q_heads = a->q_heads;
     k.share = a->q_heads / d->kv_heads;
     k.share_by = kv_divisor(k.share);
-    k.page_by = kv_divisor(k.c.page_tiles);
+    k.tiles_by = kv_divisor(k.c.page_tiles);
     k.batch = a->batch;
     k.table_pages = a->table_pages;
     k.causal = a->causal;

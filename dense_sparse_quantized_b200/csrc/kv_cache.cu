@@ -5,7 +5,7 @@
 // one token's head, keys and values both: one 16-byte access of the rows and
 // one 4-byte word of codes each, so a warp's accesses are whole 32-byte
 // sectors on both sides.  Four neighbouring threads share a group of 32.
-#include "kv.h"
+#include "kv_device.h"
 
 namespace dsq {
 
@@ -13,72 +13,118 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// fp16 and bf16 pairs.
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, float (&x)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        float2 f;
-        if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value)
-            f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-        else
-            f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
+struct Pairs;
+template <>
+struct Pairs<__half> {
+    static __device__ __forceinline__ uint32_t min_nan(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
     }
+    static __device__ __forceinline__ uint32_t max_nan(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ float2 floats(uint32_t a) { return __half22float2(*reinterpret_cast<const __half2 *>(&a)); }
+};
+template <>
+struct Pairs<__nv_bfloat16> {
+    static __device__ __forceinline__ uint32_t min_nan(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t max_nan(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ float2 floats(uint32_t a) {
+        return make_float2(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+    }
+};
+
+// The scale of a group: the least multiple n u of u that 15 n u >= hi - lo,
+// u the last of its seven bits.  fp32 finds n to within one and compares
+// 15 n u (12 bits, exact) with the rounded difference: unless the two are
+// equal they differ by more than the rounding did, and where they are equal
+// fp64 decides.  The approximate quotient's binade may be the one below or
+// above the exact one's: below, n comes out as 129, which stands for 65 of
+// twice u; above, as 64, the same scale as 128 of half of u.
+__device__ __forceinline__ float scale_of(float lo, float hi) {
+    const float range = hi - lo, d = range * (1.0f / 15.0f);
+    const int e = max((int)(__float_as_uint(d) >> 23) - 127 - 6, -20);  // u = 2^e
+    const float u = exponent(e);
+    float n = ceilf(d * exponent(-e));
+    auto enough = [&](float k) {
+        const float t = 15.0f * k * u;
+        return t == range ? (double)t >= (double)hi - (double)lo : t > range;
+    };
+    if (!enough(n)) n += 1.0f;
+    else if (n > 1.0f && enough(n - 1.0f)) n -= 1.0f;
+    return fmaxf(n == 129.0f ? 130.0f : n, 1.0f) * u;
 }
 
 // Quantises this thread's eight values of a group held by four neighbouring
 // lanes; returns the eight codes, and the group's word in `word`.
-__device__ __forceinline__ uint32_t encode8(float (&x)[8], uint32_t &word) {
-    bool nan = false;
-    float lo = 0.0f, hi = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        nan |= x[i] != x[i];
-        x[i] = fminf(fmaxf(x[i], -kKvClamp), kKvClamp);
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
-    }
-#pragma unroll
-    for (int m = 1; m <= 2; m <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
-    }
-    const uint32_t votes = __ballot_sync(0xffffffffu, nan);
-    nan = (votes >> (threadIdx.x & 28)) & 15u;
+template <typename T>
+__device__ __forceinline__ uint32_t encode8(uint4 raw, uint32_t &word) {
+    using P = Pairs<T>;
+    // (lowest, -highest) of the group; a NaN stays
+    const uint32_t lo2 = P::min_nan(P::min_nan(raw.x, raw.y), P::min_nan(raw.z, raw.w));
+    const uint32_t hi2 = P::max_nan(P::max_nan(raw.x, raw.y), P::max_nan(raw.z, raw.w)) ^ 0x80008000u;
+    uint32_t ends = P::min_nan(prmt(lo2, hi2, 0x5410), prmt(lo2, hi2, 0x7632));
+    ends = P::min_nan(ends, __shfl_xor_sync(kFull, ends, 1));
+    ends = P::min_nan(ends, __shfl_xor_sync(kFull, ends, 2));
+    const float2 f = P::floats(ends);
+    const bool nan = f.x != f.x || f.y != f.y;
+    const float lo = fmaxf(fminf(f.x, 0.0f), -kKvClamp), hi = fminf(fmaxf(-f.y, 0.0f), kKvClamp);
+    const float s = scale_of(lo, hi), inv = __frcp_rn(s);
 
-    // The scale: the least n * u with 15 n u >= hi - lo, u the last of seven
-    // bits.  fp32 finds n to within one; fp64 decides, since hi - lo of two
-    // 16-bit floats takes up to 40 bits.  d32 of the rounded difference lies
-    // in the same binade as the exact quotient or on its upper border, where
-    // 64 * 2u and 128 * u are the same scale.
-    const double range = (double)hi - (double)lo;
-    const float d32 = (float)range / 15.0f;
-    const int e = max((int)(__float_as_uint(d32) >> 23) - 127 - 6, -20);  // u = 2^e
-    const float u = __uint_as_float((uint32_t)(e + 127) << 23);
-    float n = ceilf(d32 * __uint_as_float((uint32_t)(127 - e) << 23));
-    if ((double)(15.0f * n * u) < range) n += 1.0f;
-    else if (n > 1.0f && (double)(15.0f * (n - 1.0f) * u) >= range) n -= 1.0f;
-    const float s = fmaxf(n, 1.0f) * u;
-
-    // x (11 bits) over s (7 bits) against a border k + 1/2 (5 bits): two
-    // numbers of 16 bits at most that are equal or 2^-16 apart, so the
-    // rounded fp32 quotient lies on the same side as the exact one.
-    const float z = rintf(-lo / s);
+    // Quotients: one Newton step on x times the rounded reciprocal gives the
+    // correctly rounded x / s.  x (11 bits) over s (7 bits) against a border
+    // k + 1/2 (5 bits): two numbers of 16 bits at most that are equal or 2^-16
+    // apart, so the rounded quotient lies on the same side as the exact one.
+    // Adding 3 * 2^22 rounds to an integer, ties to even.  No code is below
+    // lo's, which is 0.
+    constexpr float kRound = 12582912.0f;
+    auto code = [&](float x) {
+        const float y = x * inv;
+        return __float_as_int(fmaf(fmaf(-y, s, x), inv, y) + kRound) - __float_as_int(kRound);
+    };
+    const int z = -code(lo);
+    const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
     uint32_t codes = 0;
+    if (__any_sync(kFull, f.x < -kKvClamp || f.y < -kKvClamp)) {  // infinities have no quotient
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const float q = fminf(fmaxf(rintf(x[i] / s) + z, 0.0f), 15.0f);
-        codes |= (uint32_t)q << (4 * i);
+        for (int i = 0; i < 8; i++) {
+            const float2 x = P::floats(v[i / 2]);
+            codes |= (uint32_t)min(code(fminf(fmaxf(i % 2 ? x.y : x.x, -kKvClamp), kKvClamp)) + z, 15) << (4 * i);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const float2 x = P::floats(v[i / 2]);
+            codes |= (uint32_t)min(code(x.x) + z, 15) << (4 * i);
+            codes |= (uint32_t)min(code(x.y) + z, 15) << (4 * i + 4);
+        }
     }
-    word = (uint32_t)__half_as_ushort(__float2half_rn(s)) | (uint32_t)z;
-    if (nan) {
-        word = 0x7e00u;
-        codes = 0;
-    }
-    return codes;
+    word = nan ? 0x7e00u : (uint32_t)__half_as_ushort(__float2half_rn(s)) | (uint32_t)z;
+    return nan ? 0u : codes;
+}
+
+// Where the slot's token lies: its tile, and its row in it.
+struct Place {
+    int64_t tile;
+    int row;
+};
+template <int D>
+__device__ __forceinline__ Place place_of(const KvView &c, int slot, int head) {
+    const int page = c.page_by.div(slot), off = slot - page * c.page_tokens;
+    return {kv_tile_at(c, D, page, head, off), off % kKvTile};
 }
 
 struct RowsIn {
@@ -87,56 +133,53 @@ struct RowsIn {
 };
 
 template <int D, typename T>
-__global__ void __launch_bounds__(kThreads) append_kernel(KvView c, uint8_t *__restrict__ cache, RowsIn r,
-                                                          const int64_t *__restrict__ slots, int64_t tokens) {
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ KvView c, uint8_t *__restrict__ cache,
+                                                          const __grid_constant__ RowsIn r, const int64_t *__restrict__ slots,
+                                                          int64_t tokens) {
     constexpr int kLanes = D / 8;
+    kv_after_previous();
     const int64_t t = (int64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
     const int dim = (threadIdx.x % kLanes) * 8, head = blockIdx.y;
-    const int64_t slot = t < tokens ? slots[t] : -1;
-    const bool there = slot >= 0 && slot < c.slots;
-    float k[8] = {}, v[8] = {};
-    if (there) {
-        load8((const T *)r.k + t * r.k_token + head * r.k_head + dim, k);
-        load8((const T *)r.v + t * r.v_token + head * r.v_head + dim, v);
+    int64_t slot = -1;
+    uint4 k = make_uint4(0, 0, 0, 0), v = k;
+    if (t < tokens) {
+        k = *reinterpret_cast<const uint4 *>((const T *)r.k + t * r.k_token + head * r.k_head + dim);
+        v = *reinterpret_cast<const uint4 *>((const T *)r.v + t * r.v_token + head * r.v_head + dim);
+        slot = slots[t];
     }
     uint32_t kw, vw;
-    const uint32_t kc = encode8(k, kw), vc = encode8(v, vw);
-    if (!there) return;
-    const int page = (int)slot / c.page_tokens, off = (int)slot % c.page_tokens, row = off % kKvTile;
-    uint8_t *tile = cache + kv_tile_at(c, D, page, head, off);
-    *reinterpret_cast<uint32_t *>(tile + kv_codes(D, 0) + row * (D / 2) + dim / 2) = kc;
-    *reinterpret_cast<uint32_t *>(tile + kv_codes(D, 1) + row * (D / 2) + dim / 2) = vc;
+    const uint32_t kc = encode8<T>(k, kw), vc = encode8<T>(v, vw);
+    if (slot < 0 || slot >= c.slots) return;
+    const Place at = place_of<D>(c, (int)slot, head);
+    uint8_t *codes = cache + at.tile + at.row * (D / 2) + dim / 2;
+    *reinterpret_cast<uint32_t *>(codes + kv_codes(D, 0)) = kc;
+    *reinterpret_cast<uint32_t *>(codes + kv_codes(D, 1)) = vc;
     if (dim % kKvGroup == 0) {
-        const int at = (dim / kKvGroup * kKvTile + row) * 2;
-        *reinterpret_cast<uint16_t *>(tile + kv_words(D, 0) + at) = (uint16_t)kw;
-        *reinterpret_cast<uint16_t *>(tile + kv_words(D, 1) + at) = (uint16_t)vw;
+        uint8_t *words = cache + at.tile + (dim / kKvGroup * kKvTile + at.row) * 2;
+        *reinterpret_cast<uint16_t *>(words + kv_words(D, 0)) = (uint16_t)kw;
+        *reinterpret_cast<uint16_t *>(words + kv_words(D, 1)) = (uint16_t)vw;
     }
 }
 
-__device__ __forceinline__ uint32_t pack2(float a, float b, const __half *) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ uint32_t pack2(float a, float b, const __nv_bfloat16 *) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// Eight values of the cache: each product is exact in fp32.
+// Eight values of the cache, exact as fp16.
 template <typename T>
 __device__ __forceinline__ void decode8(uint32_t codes, uint32_t word, T *to) {
-    const float s = kv_scale(word), z = (float)(word & 15u);
-    float x[8];
+    const Decode d(prmt(word, word, 0x1010));
+    const uint32_t x[4] = {d.low(codes), d.high(codes), d.low(codes >> 8), d.high(codes >> 8)};  // (0, 4) (1, 5) (2, 6) (3, 7)
+    uint32_t h[4] = {prmt(x[0], x[1], 0x5410), prmt(x[2], x[3], 0x5410), prmt(x[0], x[1], 0x7632), prmt(x[2], x[3], 0x7632)};
+    if constexpr (!std::is_same<T, __half>::value) {
+        float2 f[4];
 #pragma unroll
-    for (int i = 0; i < 8; i++) x[i] = s * ((float)((codes >> (4 * i)) & 15u) - z);
-    if constexpr (sizeof(T) == 4) {
-        float4 *f = reinterpret_cast<float4 *>(to);
-        f[0] = make_float4(x[0], x[1], x[2], x[3]);
-        f[1] = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-        *reinterpret_cast<uint4 *>(to) =
-            make_uint4(pack2(x[0], x[1], to), pack2(x[2], x[3], to), pack2(x[4], x[5], to), pack2(x[6], x[7], to));
+        for (int i = 0; i < 4; i++) f[i] = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+        if constexpr (sizeof(T) == 4) {
+            reinterpret_cast<float4 *>(to)[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+            reinterpret_cast<float4 *>(to)[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) h[i] = pack_out<__nv_bfloat16>(f[i].x, f[i].y);
     }
+    *reinterpret_cast<uint4 *>(to) = make_uint4(h[0], h[1], h[2], h[3]);
 }
 
 struct RowsOut {
@@ -144,25 +187,37 @@ struct RowsOut {
     int64_t k_token, k_head, v_token, v_head;
 };
 
+// kReadTokens tokens a thread: their loads are under way together.
+constexpr int kReadTokens = 4;
 template <int D, typename T>
-__global__ void __launch_bounds__(kThreads) read_kernel(KvView c, RowsOut r, const int64_t *__restrict__ slots,
-                                                        int64_t tokens) {
-    constexpr int kLanes = D / 8;
-    const int64_t t = (int64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
+__global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ KvView c, const __grid_constant__ RowsOut r,
+                                                        const int64_t *__restrict__ slots, int64_t tokens) {
+    constexpr int kLanes = D / 8, kStep = kThreads / kLanes, N = kReadTokens;
+    kv_after_previous();
+    const int64_t t0 = (int64_t)blockIdx.x * (kStep * N) + threadIdx.x / kLanes;
     const int dim = (threadIdx.x % kLanes) * 8, head = blockIdx.y;
-    const int64_t slot = t < tokens ? slots[t] : -1;
-    if (slot < 0 || slot >= c.slots) return;
-    const int page = (int)slot / c.page_tokens, off = (int)slot % c.page_tokens, row = off % kKvTile;
-    const uint8_t *tile = c.cache + kv_tile_at(c, D, page, head, off);
-    const int code_at = row * (D / 2) + dim / 2, word_at = (dim / kKvGroup * kKvTile + row) * 2;
-    if (r.k)
-        decode8(*reinterpret_cast<const uint32_t *>(tile + kv_codes(D, 0) + code_at),
-                *reinterpret_cast<const uint16_t *>(tile + kv_words(D, 0) + word_at),
-                (T *)r.k + t * r.k_token + head * r.k_head + dim);
-    if (r.v)
-        decode8(*reinterpret_cast<const uint32_t *>(tile + kv_codes(D, 1) + code_at),
-                *reinterpret_cast<const uint16_t *>(tile + kv_words(D, 1) + word_at),
-                (T *)r.v + t * r.v_token + head * r.v_head + dim);
+    int64_t slot[N];
+    uint32_t kc[N], vc[N], kw[N], vw[N];
+#pragma unroll
+    for (int i = 0; i < N; i++) slot[i] = t0 + i * kStep < tokens ? slots[t0 + i * kStep] : -1;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        if (slot[i] < 0 || slot[i] >= c.slots) continue;
+        const Place at = place_of<D>(c, (int)slot[i], head);
+        const uint8_t *codes = c.cache + at.tile + at.row * (D / 2) + dim / 2;
+        const uint8_t *words = c.cache + at.tile + (dim / kKvGroup * kKvTile + at.row) * 2;
+        kc[i] = *reinterpret_cast<const uint32_t *>(codes + kv_codes(D, 0));
+        vc[i] = *reinterpret_cast<const uint32_t *>(codes + kv_codes(D, 1));
+        kw[i] = *reinterpret_cast<const uint16_t *>(words + kv_words(D, 0));
+        vw[i] = *reinterpret_cast<const uint16_t *>(words + kv_words(D, 1));
+    }
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        if (slot[i] < 0 || slot[i] >= c.slots) continue;
+        const int64_t t = t0 + i * kStep;
+        if (r.k) decode8(kc[i], kw[i], (T *)r.k + t * r.k_token + head * r.k_head + dim);
+        if (r.v) decode8(vc[i], vw[i], (T *)r.v + t * r.v_token + head * r.v_head + dim);
+    }
 }
 
 int check_rows(const dsq_kv_rows *r, bool both) {
@@ -174,34 +229,31 @@ int check_rows(const dsq_kv_rows *r, bool both) {
     return DSQ_OK;
 }
 
-// The grid of both kernels: tokens along x, kv heads along y.
-int grid_for(int64_t tokens, int heads, int D, dim3 *grid) {
-    const int64_t blocks = (tokens + kThreads / (D / 8) - 1) / (kThreads / (D / 8));
+// The grid of both kernels: `step` tokens a block along x, kv heads along y.
+int grid_for(int64_t tokens, int heads, int step, dim3 *grid) {
+    const int64_t blocks = (tokens + step - 1) / step;
     if (blocks >= ((int64_t)1 << 31) || heads > 65535) return DSQ_ERR_UNSUPPORTED;
     *grid = dim3((unsigned)blocks, (unsigned)heads);
     return DSQ_OK;
 }
 
 template <int D>
-void launch_append(dim3 grid, const KvView &c, void *cache, const dsq_kv_rows *r, const int64_t *slots, int64_t tokens,
-                   cudaStream_t st) {
+int launch_append(dim3 grid, const KvView &c, void *cache, const dsq_kv_rows *r, const int64_t *slots, int64_t tokens,
+                  cudaStream_t st) {
     const RowsIn in = {r->k, r->v, r->k_token, r->k_head, r->v_token, r->v_head};
     if (r->dtype == DSQ_DTYPE_F16)
-        append_kernel<D, __half><<<grid, kThreads, 0, st>>>(c, (uint8_t *)cache, in, slots, tokens);
-    else
-        append_kernel<D, __nv_bfloat16><<<grid, kThreads, 0, st>>>(c, (uint8_t *)cache, in, slots, tokens);
+        return kv_launch(append_kernel<D, __half>, grid, kThreads, 0, st, c, (uint8_t *)cache, in, slots, tokens);
+    return kv_launch(append_kernel<D, __nv_bfloat16>, grid, kThreads, 0, st, c, (uint8_t *)cache, in, slots, tokens);
 }
 
 template <int D>
-void launch_read(dim3 grid, const KvView &c, const dsq_kv_rows *r, const int64_t *slots, int64_t tokens,
-                 cudaStream_t st) {
+int launch_read(dim3 grid, const KvView &c, const dsq_kv_rows *r, const int64_t *slots, int64_t tokens,
+                cudaStream_t st) {
     const RowsOut out = {r->k, r->v, r->k_token, r->k_head, r->v_token, r->v_head};
-    if (r->dtype == DSQ_DTYPE_F16)
-        read_kernel<D, __half><<<grid, kThreads, 0, st>>>(c, out, slots, tokens);
-    else if (r->dtype == DSQ_DTYPE_BF16)
-        read_kernel<D, __nv_bfloat16><<<grid, kThreads, 0, st>>>(c, out, slots, tokens);
-    else
-        read_kernel<D, float><<<grid, kThreads, 0, st>>>(c, out, slots, tokens);
+    if (r->dtype == DSQ_DTYPE_F16) return kv_launch(read_kernel<D, __half>, grid, kThreads, 0, st, c, out, slots, tokens);
+    if (r->dtype == DSQ_DTYPE_BF16)
+        return kv_launch(read_kernel<D, __nv_bfloat16>, grid, kThreads, 0, st, c, out, slots, tokens);
+    return kv_launch(read_kernel<D, float>, grid, kThreads, 0, st, c, out, slots, tokens);
 }
 
 }  // namespace
@@ -228,15 +280,14 @@ extern "C" int dsq_kv_append(const dsq_kv_desc *d, void *cache, const dsq_kv_row
     if ((rc = check_rows(rows, true)) != DSQ_OK) return rc;
     if (rows->dtype == DSQ_DTYPE_F32) return DSQ_ERR_UNSUPPORTED;
     dim3 grid;
-    if ((rc = grid_for(tokens, d->kv_heads, d->head_dim, &grid)) != DSQ_OK) return rc;
+    if ((rc = grid_for(tokens, d->kv_heads, kThreads * 8 / d->head_dim, &grid)) != DSQ_OK) return rc;
     DeviceGuard guard(d->device);
     if (!guard.ok) return DSQ_ERR_CUDA;
     const KvView c = kv_view(d, cache);
     const cudaStream_t st = (cudaStream_t)stream;
-    if (d->head_dim == 64) launch_append<64>(grid, c, cache, rows, slots, tokens, st);
-    else if (d->head_dim == 128) launch_append<128>(grid, c, cache, rows, slots, tokens, st);
-    else launch_append<256>(grid, c, cache, rows, slots, tokens, st);
-    return cudaGetLastError() == cudaSuccess ? DSQ_OK : DSQ_ERR_CUDA;
+    if (d->head_dim == 64) return launch_append<64>(grid, c, cache, rows, slots, tokens, st);
+    if (d->head_dim == 128) return launch_append<128>(grid, c, cache, rows, slots, tokens, st);
+    return launch_append<256>(grid, c, cache, rows, slots, tokens, st);
 }
 
 extern "C" int dsq_kv_read(const dsq_kv_desc *d, const void *cache, const dsq_kv_rows *rows, const int64_t *slots,
@@ -251,13 +302,12 @@ extern "C" int dsq_kv_read(const dsq_kv_desc *d, const void *cache, const dsq_kv
         (rows->v && !kv_rows_apart(tokens, d->kv_heads, rows->v_token, rows->v_head, d->head_dim)))
         return DSQ_ERR_INVALID_ARG;
     dim3 grid;
-    if ((rc = grid_for(tokens, d->kv_heads, d->head_dim, &grid)) != DSQ_OK) return rc;
+    if ((rc = grid_for(tokens, d->kv_heads, kReadTokens * kThreads * 8 / d->head_dim, &grid)) != DSQ_OK) return rc;
     DeviceGuard guard(d->device);
     if (!guard.ok) return DSQ_ERR_CUDA;
     const KvView c = kv_view(d, cache);
     const cudaStream_t st = (cudaStream_t)stream;
-    if (d->head_dim == 64) launch_read<64>(grid, c, rows, slots, tokens, st);
-    else if (d->head_dim == 128) launch_read<128>(grid, c, rows, slots, tokens, st);
-    else launch_read<256>(grid, c, rows, slots, tokens, st);
-    return cudaGetLastError() == cudaSuccess ? DSQ_OK : DSQ_ERR_CUDA;
+    if (d->head_dim == 64) return launch_read<64>(grid, c, rows, slots, tokens, st);
+    if (d->head_dim == 128) return launch_read<128>(grid, c, rows, slots, tokens, st);
+    return launch_read<256>(grid, c, rows, slots, tokens, st);
 }

@@ -151,7 +151,7 @@ __host__ __device__ constexpr int join_rows() { return R >= 32 ? 32 : 8; }  // o
 template <int D, int R, typename T>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ KvAttend a, const float *__restrict__ parts,
                                                    const KvCarry *__restrict__ carries) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    kv_after_previous();
     constexpr int E = D / 32, N = join_rows<R>() / 8;  // elements of a lane, rows of a warp
     const KvCarry c = carries[blockIdx.x];
     if (!c.valid) return;
@@ -203,16 +203,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ KvAtt
 
 template <int D, int R, typename T>
 int launch_join(const KvAttend &a, const float *parts, const KvCarry *carries, int ctas, cudaStream_t st) {
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, R / join_rows<R>());
-    cfg.blockDim = 256;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<D, R, T>, a, parts, carries) == cudaSuccess ? DSQ_OK : DSQ_ERR_CUDA;
+    return kv_launch(join_kernel<D, R, T>, dim3(ctas, R / join_rows<R>()), 256, 0, st, a, parts, carries);
 }
 
 }  // namespace dsq

@@ -367,7 +367,7 @@ struct Loader {
         const int32_t *row = a.page_table + (int64_t)p.b * a.table_pages;
 #pragma unroll
         for (int i = 0; i < 2; i++) {
-            const int tile = t * (kN / kKvTile) + 2 * warp + i, col = a.page_by.div(tile);
+            const int tile = t * (kN / kKvTile) + 2 * warp + i, col = a.tiles_by.div(tile);
             u.in_page[i] = tile - col * a.c.page_tiles;
             if (col < a.table_pages && u.hi > (2 * warp + i) * kKvTile) u.page[i] = row[col];
         }
@@ -823,14 +823,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             mbar_init(&sh.qfull[i], 4);
         }
         fence_mbar_init();
-        pp.carries[blockIdx.x].valid = 0;
     }
     if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    } else if (warp == 8)
-        find_run<S::R>(pp.a, sh);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // join_kernel waits for this one's end
+    }
+    kv_after_previous();
+    if (threadIdx.x == 0) pp.carries[blockIdx.x].valid = 0;
+    if (warp == 8) find_run<S::R>(pp.a, sh);
     fence_before();
     __syncthreads();
     fence_after();
@@ -862,9 +862,8 @@ int launch_prompt(const KvAttend &a, void *workspace, int sms, cudaStream_t st) 
     static KvOnce once;
     if (!once.set_smem((const void *)kernel, S::kSmem)) return DSQ_ERR_CUDA;
     const int grid = std::min(sms, kMaxCtas);
-    kernel<<<grid, kThreads, S::kSmem, st>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return DSQ_ERR_CUDA;
-    return launch_join<D, S::R, T>(a, p.parts, p.carries, grid, st);
+    const int rc = kv_launch(kernel, grid, kThreads, S::kSmem, st, p);
+    return rc != DSQ_OK ? rc : launch_join<D, S::R, T>(a, p.parts, p.carries, grid, st);
 }
 
 template <typename T>

@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
     float *const head_part = reinterpret_cast<float *>(smem + warp * S::kWarp + RING * S::kTile);
     float *const tail_part = reinterpret_cast<float *>(smem + warp * S::kWarp);
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // join_kernel waits for this one's end
+    kv_after_previous();
 
     // Total work, and this warp's run [u, u_end) of it.
     int64_t total = 0;
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
         const int tile1 = min((unit0 + last) * 2, (max(hi_any, 0) + 15) / 16);
 
         // Page numbers of the next 64 table columns, one per lane and register.
-        int col = a.page_by.div(tile0), in_page = tile0 - col * a.c.page_tiles, col0 = col;
+        int col = a.tiles_by.div(tile0), in_page = tile0 - col * a.c.page_tiles, col0 = col;
         const int32_t *row = a.page_table + (int64_t)b * a.table_pages;
         auto pages_from = [&](int c) { return c + lane < a.table_pages ? row[c + lane] : -1; };
         int pages = pages_from(col0), pages_next = pages_from(col0 + 32);
@@ -600,9 +600,8 @@ int launch_split(const KvAttend &a, void *workspace, int sms, cudaStream_t st) {
     static KvOnce once;
     if (!once.set_smem((const void *)kernel, S::kSmem)) return DSQ_ERR_CUDA;
     const int grid = std::min(sms, kMaxCtas);
-    kernel<<<grid, S::NW * 32, S::kSmem, st>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return DSQ_ERR_CUDA;
-    return launch_join<S::D, S::R, T>(a, p.parts, p.carries, grid, st);
+    const int rc = kv_launch(kernel, grid, S::NW * 32, S::kSmem, st, p);
+    return rc != DSQ_OK ? rc : launch_join<S::D, S::R, T>(a, p.parts, p.carries, grid, st);
 }
 
 template <typename T>
