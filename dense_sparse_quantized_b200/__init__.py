@@ -397,7 +397,8 @@ class KVCache:
         self.device = data.device
         self.kv_heads, self.head_dim = int(kv_heads), int(head_dim)
         self.page_tokens, self.pages = int(page_tokens), int(pages)
-        self._d = ctypes.byref(self.desc)
+        self._lib, self._torch = library(), torch
+        self._d, self._data = ctypes.byref(self.desc), data.data_ptr()
         self._dtypes = {torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
 
     @staticmethod
@@ -409,73 +410,68 @@ class KVCache:
         return size.value
 
     def _stream(self, stream):
-        import torch
-        return _stream_ptr(torch.cuda.current_stream(self.device) if stream is None else stream)
+        # a decode step makes these calls by the dozen: the raw handle costs a
+        # tenth of a torch.cuda.Stream object
+        if stream is None:
+            return self._torch._C._cuda_getCurrentRawStream(self.desc.device)
+        return _stream_ptr(stream)
 
-    def _rows(self, t, name, heads, tokens):
-        if t.device != self.device or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.head_dim:
-            raise ValueError(f"{name} must be [tokens, {heads}, {self.head_dim}] on {self.device}")
-        if t.stride(2) != 1:
+    def _rows(self, t, name, tokens, heads):
+        if t.device != self.device or t.shape != (tokens, heads, self.head_dim):
+            raise ValueError(f"{name} must be [{tokens}, {heads}, {self.head_dim}] on {self.device}")
+        strides = t.stride()
+        if strides[2] != 1:
             raise ValueError(f"{name} must be contiguous in its last dimension")
-        if tokens is not None and t.shape[0] != tokens:
-            raise ValueError(f"{name} has {t.shape[0]} rows, not {tokens}")
-        if t.dtype not in self._dtypes:
-            raise ValueError(f"{name} must be float16, bfloat16 or float32")
+        return strides
 
-    def _slots(self, slots):
-        import torch
-        if slots.dtype != torch.int64 or slots.device != self.device or slots.dim() != 1 or not slots.is_contiguous():
+    def _kv_rows(self, k, v, slots):
+        if (slots.dtype != self._torch.int64 or slots.device != self.device or slots.dim() != 1
+                or not slots.is_contiguous()):
             raise ValueError(f"slots must be a contiguous 1-D int64 tensor on {self.device}")
+        n = slots.shape[0]
+        ks, vs = self._rows(k, "k", n, self.kv_heads), self._rows(v, "v", n, self.kv_heads)
+        dtype = self._dtypes.get(k.dtype)
+        if dtype is None or k.dtype != v.dtype:
+            raise ValueError("k and v must have the same dtype: float16, bfloat16 or float32")
+        return n, ctypes.byref(KVRows(k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1], dtype))
 
     def append(self, k, v, slots, stream=None):
         """Quantise k, v [tokens, kv_heads, head_dim] (float16 or bfloat16, any
         strides that are multiples of 8) into ``slots`` (int64 [tokens]; a
         negative slot passes its token over; no slot twice)."""
-        self._slots(slots)
-        n = slots.shape[0]
-        self._rows(k, "k", self.kv_heads, n)
-        self._rows(v, "v", self.kv_heads, n)
-        if k.dtype != v.dtype:
-            raise ValueError("k and v must have the same dtype")
-        rows = KVRows(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
-                      self._dtypes[k.dtype])
-        _check(library().dsq_kv_append(self._d, self.data.data_ptr(), ctypes.byref(rows), slots.data_ptr(), n,
-                                       self._stream(stream)), "dsq_kv_append")
+        n, rows = self._kv_rows(k, v, slots)
+        rc = self._lib.dsq_kv_append(self._d, self._data, rows, slots.data_ptr(), n, self._stream(stream))
+        if rc:
+            _check(rc, "dsq_kv_append")
 
     def read(self, slots, dtype=None, k=None, v=None, stream=None):
         """(k, v): the values at ``slots``, [tokens, kv_heads, head_dim] in
         ``dtype`` (default float16) or in the given k and v, whose rows of
         negative slots stay as they are (new ones hold 0 there)."""
-        import torch
-        self._slots(slots)
-        n = slots.shape[0]
         if k is None or v is None:
             like = k if k is not None else v
-            dtype = dtype or (like.dtype if like is not None else torch.float16)
-            shape = (n, self.kv_heads, self.head_dim)
-            k = torch.zeros(shape, dtype=dtype, device=self.device) if k is None else k
-            v = torch.zeros(shape, dtype=dtype, device=self.device) if v is None else v
-        self._rows(k, "k", self.kv_heads, n)
-        self._rows(v, "v", self.kv_heads, n)
-        if k.dtype != v.dtype or (dtype is not None and k.dtype != dtype):
-            raise ValueError("k and v must have the same dtype, the one asked for")
-        rows = KVRows(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
-                      self._dtypes[k.dtype])
-        _check(library().dsq_kv_read(self._d, self.data.data_ptr(), ctypes.byref(rows), slots.data_ptr(), n,
-                                     self._stream(stream)), "dsq_kv_read")
+            dtype = dtype or (like.dtype if like is not None else self._torch.float16)
+            shape = (slots.shape[0], self.kv_heads, self.head_dim)
+            k = self._torch.zeros(shape, dtype=dtype, device=self.device) if k is None else k
+            v = self._torch.zeros(shape, dtype=dtype, device=self.device) if v is None else v
+        if dtype is not None and k.dtype != dtype:
+            raise ValueError("k and v must have the dtype asked for")
+        n, rows = self._kv_rows(k, v, slots)
+        rc = self._lib.dsq_kv_read(self._d, self._data, rows, slots.data_ptr(), n, self._stream(stream))
+        if rc:
+            _check(rc, "dsq_kv_read")
         return k, v
 
     def attend_workspace(self, q_tokens: int, q_heads: int, batch: int):
-        """Scratch for attend() calls of up to these sizes that follow one
-        another; calls that may overlap need one each."""
-        import torch
+        """Scratch for attend() calls of these sizes that follow one another;
+        calls that may overlap need one each."""
         size = ctypes.c_size_t(0)
         a = KVQueries(q_tokens=int(q_tokens), q_heads=int(q_heads), batch=int(batch))
         a.q_tokens = a.q_tokens // max(a.batch, 1) * a.batch
         rc = library().dsq_kv_attend(self._d, None, ctypes.byref(a), None, ctypes.byref(size), None)
         if rc != DSQ_ERR_BUFFER_TOO_SMALL:
             _check(rc, "dsq_kv_attend")
-        return torch.empty(max(size.value, 1), dtype=torch.uint8, device=self.device)
+        return self._torch.empty(max(size.value, 1), dtype=self._torch.uint8, device=self.device)
 
     def attend(self, q, page_table, kv_lens, q_start=None, scale=None, causal=True, window=0, out=None, lse=None,
                return_lse=False, workspace=None, stream=None):
@@ -490,38 +486,43 @@ class KVCache:
         ``return_lse`` or ``lse`` also the fp32 log-sum-exp [q_tokens,
         q_heads].  Rows of no sequence stay as they are in a given out and
         lse, and hold 0 in new ones."""
-        import torch
-        self._rows(q, "q", q.shape[1] if q.dim() == 3 else 0, None)
+        torch, device = self._torch, self.device
+        if q.dim() != 3:
+            raise ValueError(f"q must be [q_tokens, q_heads, {self.head_dim}]")
         n, heads = q.shape[0], q.shape[1]
+        qs = self._rows(q, "q", n, heads)
+        dtype = self._dtypes.get(q.dtype)
+        if dtype is None:
+            raise ValueError("q must be float16 or bfloat16")
         if page_table.dim() != 2 or kv_lens.dim() != 1 or kv_lens.shape[0] != page_table.shape[0]:
             raise ValueError("page_table must be [batch, pages] and kv_lens [batch]")
-        batch = kv_lens.shape[0]
-        for name, t in (("page_table", page_table), ("kv_lens", kv_lens), ("q_start", q_start)):
-            if t is not None and (t.dtype != torch.int32 or t.device != self.device or not t.is_contiguous()):
-                raise ValueError(f"{name} must be a contiguous int32 tensor on {self.device}")
-        if q_start is not None and tuple(q_start.shape) != (batch + 1,):
+        batch, columns = page_table.shape
+        for t in (page_table, kv_lens) if q_start is None else (page_table, kv_lens, q_start):
+            if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+                raise ValueError(f"page_table, kv_lens and q_start must be contiguous int32 tensors on {device}")
+        if q_start is not None and q_start.shape != (batch + 1,):
             raise ValueError("q_start must be [batch + 1]")
         if out is None:
-            out = (torch.empty if q_start is None else torch.zeros)(q.shape, dtype=q.dtype, device=self.device)
-        else:
-            self._rows(out, "out", heads, n)
-            if out.dtype != q.dtype:
-                raise ValueError("out must have q's dtype")
+            out = (torch.empty if q_start is None else torch.zeros)(q.shape, dtype=q.dtype, device=device)
+        elif out.dtype != q.dtype:
+            raise ValueError("out must have q's dtype")
+        os = self._rows(out, "out", n, heads)
         if lse is None:
             if return_lse:
-                lse = torch.zeros((n, heads), dtype=torch.float32, device=self.device)
-        elif (lse.dtype != torch.float32 or lse.device != self.device or tuple(lse.shape) != (n, heads)
-              or not lse.is_contiguous()):
-            raise ValueError(f"lse must be a contiguous float32 tensor [{n}, {heads}] on {self.device}")
+                lse = torch.zeros((n, heads), dtype=torch.float32, device=device)
+        elif lse.dtype != torch.float32 or lse.device != device or lse.shape != (n, heads) or not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous float32 tensor [{n}, {heads}] on {device}")
         if workspace is None:
             workspace = self.attend_workspace(n, heads, batch)
-        elif workspace.device != self.device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
-        a = KVQueries(q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), q.stride(0), q.stride(1),
-                      out.stride(0), out.stride(1), n, self._dtypes[q.dtype], heads, batch, page_table.shape[1],
-                      int(causal), int(window), self.head_dim ** -0.5 if scale is None else scale,
-                      page_table.data_ptr(), kv_lens.data_ptr(), None if q_start is None else q_start.data_ptr())
+        elif workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        a = KVQueries(q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), qs[0], qs[1], os[0], os[1],
+                      n, dtype, heads, batch, columns, causal, window,
+                      self.head_dim ** -0.5 if scale is None else scale, page_table.data_ptr(), kv_lens.data_ptr(),
+                      None if q_start is None else q_start.data_ptr())
         size = ctypes.c_size_t(workspace.numel() * workspace.element_size())
-        _check(library().dsq_kv_attend(self._d, self.data.data_ptr(), ctypes.byref(a), workspace.data_ptr(),
-                                       ctypes.byref(size), self._stream(stream)), "dsq_kv_attend")
+        rc = self._lib.dsq_kv_attend(self._d, self._data, ctypes.byref(a), workspace.data_ptr(), ctypes.byref(size),
+                                     self._stream(stream))
+        if rc:
+            _check(rc, "dsq_kv_attend")
         return out if lse is None else (out, lse)
