@@ -50,7 +50,7 @@ struct Split {
     static constexpr int D = D_, NT = NT_, NW = NW_, RING = RING_;
     static constexpr int R = 8 * NT;
     static constexpr int kTile = kv_tile_bytes(D);
-    static constexpr int kPart = (R * (D + 2) * 4 + 15) / 16 * 16;
+    static constexpr int kPart = (R * (D + 2) * 4 + 127) / 128 * 128;  // the swizzles count on 128-byte rings
     static constexpr int kWarp = RING * kTile + kPart;
     static constexpr int kSmem = NW * kWarp;
     static_assert(RING * kTile >= kPart && RING % 2 == 0 && kSmem <= 224 * 1024, "shared memory of a CTA");
@@ -69,6 +69,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t a) {
     uint32_t r;
@@ -89,18 +96,29 @@ __device__ __forceinline__ int value_at(int t, int c) {
     return kv_codes(D, 1) + row * (D / 2) + (D == 256 ? c ^ (2 * (t >> 2)) : D == 128 ? c ^ (2 * (t >> 3)) : c) * 16;
 }
 
+// A lane's part in copying tiles to the ring, 16-byte chunk `lane` of every 512
+// bytes: where it goes in a tile.
 template <int D>
-__device__ __forceinline__ void issue_tile(uint32_t dst, const uint8_t *src, int lane) {
-    constexpr int kRow = D / 32;          // chunks of a token's row
-    constexpr int kCodes = 16 * kRow;     // of K or V codes
+struct Copy {
+    static constexpr int kRow = D / 32, N = D / 64;  // chunks of a token's row; of a lane's in K, and in V
+    uint32_t key[N], value[N], words;
+    __device__ __forceinline__ Copy(uint32_t ring, int lane) {
 #pragma unroll
-    for (int i = lane; i < kCodes; i += 32) {
-        cp_async16(dst + key_at<D>(i / kRow, i % kRow), src + i * 16);
-        cp_async16(dst + value_at<D>(i / kRow, i % kRow), src + kv_codes(D, 1) + i * 16);
+        for (int i = 0; i < N; i++) {
+            key[i] = ring + key_at<D>((lane + 32 * i) / kRow, lane % kRow);
+            value[i] = ring + value_at<D>((lane + 32 * i) / kRow, lane % kRow);
+        }
+        words = ring + kv_words(D, 0) + lane * 16;
     }
-    constexpr int kWords = D / 8;         // of K and V words: 16 tokens x D/32 groups x 2 bytes each
-    if (lane < kWords) cp_async16(dst + kv_words(D, 0) + lane * 16, src + kv_words(D, 0) + lane * 16);
-}
+    __device__ __forceinline__ void start(uint32_t at, const uint8_t *src, int lane) const {
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            cp_async16(key[i] + at, src + i * 512);
+            cp_async16(value[i] + at, src + kv_codes(D, 1) + i * 512);
+        }
+        if (lane < D / 8) cp_async16(words + at, src + kv_words(D, 0));
+    }
+};
 
 // The jobs of a sequence.
 struct Jobs : KvSeq {
@@ -131,6 +149,13 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, jj = lane & 3;
     const uint32_t ring = smem_u32(smem) + warp * S::kWarp;
     float *const head_part = reinterpret_cast<float *>(smem + warp * S::kWarp + RING * S::kTile);
+    const Copy<D> copy(ring, lane);
+    // This lane's fragments in a ring tile.
+    const uint32_t key_row = ring + r * (D / 2) + (D == 256 ? 2 * jj ^ (r & 1) : jj) * (D == 64 ? 8 : 16);
+    const uint32_t key_word = ring + kv_words(D, 0) + jj * (D / 4) / kKvGroup * 32 + (4 * (r >> 1) + (r & 1)) * 2;
+    const uint32_t value_row = ring + kv_codes(D, 1) + jj * (D / 2) +
+                               (D == 64 ? r * 4 : D == 128 ? ((r >> 1) ^ (2 * (jj >> 1))) * 16 + (r & 1) * 8 : (r ^ (2 * jj)) * 16);
+    const uint32_t value_word = ring + kv_words(D, 1) + r * (D / 8) / kKvGroup * 32 + jj * 8;
     float *const tail_part = reinterpret_cast<float *>(smem + warp * S::kWarp);
 
     kv_after_previous();
@@ -193,39 +218,43 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
         const int tile1 = min((unit0 + last) * 2, (max(hi_any, 0) + 15) / 16);
 
         // Page numbers of the next 64 table columns, one per lane and register.
-        int col = a.tiles_by.div(tile0), in_page = tile0 - col * a.c.page_tiles, col0 = col;
+        int col = a.tiles_by.div(tile0), col0 = col, in_page = tile0 - col * a.c.page_tiles;
         const int32_t *row = a.page_table + (int64_t)b * a.table_pages;
         auto pages_from = [&](int c) { return c + lane < a.table_pages ? row[c + lane] : -1; };
         int pages = pages_from(col0), pages_next = pages_from(col0 + 32);
-        const uint8_t *const base = a.c.cache + (int64_t)head * a.c.page_tiles * S::kTile;
-        uint32_t valid = 0;  // bit i: ring tile i holds a tile of the cache
-        int slot = 0, next = tile0;
-        auto issue = [&] {
+        const uint8_t *const base = a.c.cache + (int64_t)head * a.c.page_tiles * S::kTile + lane * 16;
+        const uint8_t *src = nullptr;     // this lane's chunk of the next tile
+        int left = tile1 - tile0, rest = 0;  // tiles to copy; of them on this page
+        bool exists = false;              // the page
+        auto turn = [&] {
             const int page = __shfl_sync(kFull, pages, col - col0);
-            const bool there = next < tile1 && (uint32_t)page < (uint32_t)a.c.pages;
-            if (there)
-                issue_tile<D>(ring + slot * S::kTile,
-                              base + ((int64_t)page * a.c.kv_heads * a.c.page_tiles + in_page) * S::kTile, lane);
-            cp_async_commit();
-            valid = (valid & ~(1u << slot)) | ((uint32_t)there << slot);
-            slot = slot + 1 == RING ? 0 : slot + 1;
-            next++;
-            if (++in_page == a.c.page_tiles) {
-                in_page = 0;
-                if (++col - col0 == 32) {
-                    col0 += 32;
-                    pages = pages_next;
-                    pages_next = pages_from(col0 + 32);
-                }
+            exists = (uint32_t)page < (uint32_t)a.c.pages;
+            if (exists) src = base + ((int64_t)page * a.c.kv_heads * a.c.page_tiles + in_page) * S::kTile;
+            rest = a.c.page_tiles - in_page;
+            in_page = 0;
+            if (++col - col0 == 32) {
+                col0 += 32;
+                pages = pages_next;
+                pages_next = pages_from(col0 + 32);
             }
         };
+        bool there[RING];  // whether a ring tile holds a tile of the cache
+        auto issue = [&](int slot) {
+            if (rest == 0 && left > 0) turn();
+            there[slot] = exists && left > 0;
+            if (there[slot]) copy.start(slot * S::kTile, src, lane);
+            cp_async_commit();
+            src += S::kTile;
+            rest--;
+            left--;
+        };
 #pragma unroll
-        for (int i = 0; i < RING; i++) issue();
+        for (int i = 0; i < RING; i++) issue(i);
 
         // Queries: the B operand of the scores, column n = r.
         uint32_t q[D / 16][NT][2];
-        float scale[NT][2];  // of the accumulator's columns 2 jj, 2 jj + 1
-        int2 seen[NT][2];
+        float scale[NT][2];  // of the accumulator's columns 2 jj, 2 jj + 1; positive, the sign is the queries'
+        const uint32_t sign = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
         for (int n = 0; n < NT; n++) {
             const int rho = min(rho0 + 8 * n + r, rho1);
@@ -243,18 +272,17 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
                 up = up_of(max(top, __shfl_xor_sync(kFull, top, 2)));
             }
             query_codes_order<T, KW>(x, up);
-            const float factor = a.scale_log2 * exponent(-up);
+            const float factor = fmaxf(fabsf(a.scale_log2) * exponent(-up), 1.17549435e-38f);  // not 0: -inf times it is -inf
 #pragma unroll
             for (int w = 0; w < KW; w++) {
-                q[2 * w][n][0] = x[w].x;
-                q[2 * w][n][1] = x[w].y;
-                q[2 * w + 1][n][0] = x[w].z;
-                q[2 * w + 1][n][1] = x[w].w;
+                q[2 * w][n][0] = x[w].x ^ sign;
+                q[2 * w][n][1] = x[w].y ^ sign;
+                q[2 * w + 1][n][0] = x[w].z ^ sign;
+                q[2 * w + 1][n][1] = x[w].w ^ sign;
             }
 #pragma unroll
             for (int c = 0; c < 2; c++) {
                 scale[n][c] = __shfl_sync(kFull, factor, (2 * jj + c) * 4);
-                seen[n][c] = seen_by(a, j, min(rho0 + 8 * n + 2 * jj + c, rho1));
             }
         }
 
@@ -273,31 +301,25 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
                 l[n][c] = 0.0f;
             }
 
-        int at = 0;  // ring tile of the next unit
-        for (int tile = tile0; tile < tile1; tile += 2) {
+        auto unit = [&](int tile, int at) {  // tiles `tile`, + 1, in the ring from `at` on
             cp_async_wait<RING - 2>();
             __syncwarp();
             const int t0 = tile * 16;
-            const bool masked = t0 < lo_all || t0 + 32 > hi_all || ((valid >> at) & 3u) != 3u;
+            const bool masked = t0 < lo_all || t0 + 32 > hi_all || !there[at] || !there[at + 1];
             float s[2][NT][4];
 #pragma unroll
             for (int h = 0; h < 2; h++) {
-                const uint32_t buf = ring + (at + h) * S::kTile;
-#pragma unroll
-                for (int n = 0; n < NT; n++)
-#pragma unroll
-                    for (int k = 0; k < 4; k++) s[h][n][k] = 0.0f;
+                const uint32_t buf = (at + h) * S::kTile;
                 uint32_t kw[2][KW];
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
-                    const uint32_t at_row = buf + (r + 8 * e) * (D / 2);
+                    const uint32_t at_row = key_row + buf + 8 * e * (D / 2);
                     if constexpr (D == 64)
-                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(kw[e][0]), "=r"(kw[e][1]) : "r"(at_row + jj * 8));
+                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(kw[e][0]), "=r"(kw[e][1]) : "r"(at_row));
                     else {
 #pragma unroll
-                        for (int c = 0; c < KW / 4; c++) {
-                            const int chunk = jj * (KW / 4) + c;
-                            const uint4 v = lds128(at_row + (D == 256 ? chunk ^ (r & 1) : chunk) * 16);
+                        for (int c = 0; c < KW / 4; c++) {  // at 256 dimensions chunk 2 jj + c, in odd rows 2 jj + 1 - c
+                            const uint4 v = lds128(c == 0 ? at_row : (at_row ^ 16));
                             kw[e][4 * c] = v.x;
                             kw[e][4 * c + 1] = v.y;
                             kw[e][4 * c + 2] = v.z;
@@ -308,11 +330,9 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
                 constexpr int G = D == 256 ? 2 : 1;  // groups of a lane's key dimensions
 #pragma unroll
                 for (int g = 0; g < G; g++) {
-                    const int tok = 4 * (r >> 1) + (r & 1);
-                    const uint32_t word_at = buf + kv_words(D, 0) + (jj * (D / 4) / 32 + g) * 32 + tok * 2;
                     uint16_t p0, p1;
-                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(p0) : "r"(word_at));
-                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(p1) : "r"(word_at + 4));
+                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(p0) : "r"(key_word + buf + g * 32));
+                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(p1) : "r"(key_word + buf + g * 32 + 4));
                     const Decode d0(prmt(p0, p0, 0x1010)), d1(prmt(p1, p1, 0x1010));
 #pragma unroll
                     for (int w = g * (KW / G); w < (g + 1) * (KW / G); w++) {
@@ -321,43 +341,60 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
                         const uint32_t f1[4] = {d0.low(x >> 8), d1.low(y >> 8), d0.high(x >> 8), d1.high(y >> 8)};
 #pragma unroll
                         for (int n = 0; n < NT; n++) {
-                            mma16816(s[h][n], f0, q[2 * w][n][0], q[2 * w][n][1]);
+                            if (w == 0) mma16816_zero(s[h][n], f0, q[0][n][0], q[0][n][1]);
+                            else mma16816(s[h][n], f0, q[2 * w][n][0], q[2 * w][n][1]);
                             mma16816(s[h][n], f1, q[2 * w + 1][n][0], q[2 * w + 1][n][1]);
                         }
                     }
                 }
             }
-            // Scores in powers of two; column c of s is k % 2, its token tok + 2 (k / 2).
+            uint2 vp[2];
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                             : "=r"(vp[h].x), "=r"(vp[h].y)
+                             : "r"(value_word + (at + h) * S::kTile));
+            if (masked) {
+                // Column c of s is k % 2, its token tok + 2 (k / 2).  A NaN
+                // value must reach the rows that see it alone: its scale
+                // becomes 0 and those rows' scores NaN.  Tokens that no row
+                // sees, which may be anything, get scale 0.
+                int2 seen[NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; n++)
+#pragma unroll
+                    for (int c = 0; c < 2; c++) seen[n][c] = seen_by(a, j, min(rho0 + 8 * n + 2 * jj + c, rho1));
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    uint32_t bad = 0;
+                    uint32_t w[2] = {vp[h].x, vp[h].y};
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const int t = t0 + 16 * h + 4 * jj + i;
+                        const bool use = there[at + h] && t >= lo_any && t < hi_any;
+                        const bool nan = ((w[i / 2] >> (16 * (i % 2))) & 0x7c00u) == 0x7c00u;
+                        if (!use || nan) w[i / 2] &= i % 2 ? 0x0000ffffu : 0xffff0000u;
+                        if (use && nan) bad |= 1u << (4 * jj + i);
+                    }
+                    vp[h] = make_uint2(w[0], w[1]);
+                    bad = __reduce_or_sync(kFull, bad);
+#pragma unroll
+                    for (int n = 0; n < NT; n++)
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            const int i = 4 * (r >> 1) + (r & 1) + (k & 2), t = t0 + 16 * h + i;
+                            if (!there[at + h] || t < seen[n][k & 1].x || t >= seen[n][k & 1].y) s[h][n][k] = -INFINITY;
+                            else if (bad >> i & 1u) s[h][n][k] = NAN;
+                        }
+                }
+            }
             bool raise = false;
             float top[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; n++)
 #pragma unroll
                 for (int c = 0; c < 2; c++) {
-#pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        s[h][n][c] *= scale[n][c];
-                        s[h][n][2 + c] *= scale[n][c];
-                    }
-                }
-            if (masked) {
-#pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const bool there = (valid >> (at + h)) & 1u;
-#pragma unroll
-                    for (int n = 0; n < NT; n++)
-#pragma unroll
-                        for (int k = 0; k < 4; k++) {
-                            const int t = t0 + 16 * h + 4 * (r >> 1) + (r & 1) + (k & 2);
-                            if (!there || t < seen[n][k & 1].x || t >= seen[n][k & 1].y) s[h][n][k] = -INFINITY;
-                        }
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < NT; n++)
-#pragma unroll
-                for (int c = 0; c < 2; c++) {
-                    top[n][c] = fmaxf(fmaxf(s[0][n][c], s[0][n][2 + c]), fmaxf(s[1][n][c], s[1][n][2 + c]));
+                    top[n][c] = scale[n][c] * fmaxf(fmaxf(s[0][n][c], s[0][n][2 + c]), fmaxf(s[1][n][c], s[1][n][2 + c]));
                     raise |= top[n][c] > m[n][c] + kLazy;
                 }
             if (__any_sync(kFull, raise)) {
@@ -387,63 +424,24 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
                 for (int n = 0; n < NT; n++) {
 #pragma unroll
                     for (int k = 0; k < 4; k++) {
-                        s[h][n][k] = ex2(s[h][n][k] - m[n][k & 1]);
+                        s[h][n][k] = ex2(fmaf(s[h][n][k], scale[n][k & 1], -m[n][k & 1]));
                         l[n][k & 1] += s[h][n][k];
                     }
-                }
-            // Values.  In a unit whose rows see different tokens, a NaN value
-            // must reach the rows that see it alone: its scale becomes 0 and
-            // those rows' numerators NaN.  Tokens that no row sees, which may
-            // be anything, get scale 0.
-            uint2 vp[2];
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const uint32_t word_at = ring + (at + h) * S::kTile + kv_words(D, 1) + (r * (D / 8) / 32) * 32 + jj * 8;
-                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(vp[h].x), "=r"(vp[h].y) : "r"(word_at));
-                if (masked) {
-                    const bool there = (valid >> (at + h)) & 1u;
-                    uint32_t bad = 0;
-                    uint32_t w[2] = {vp[h].x, vp[h].y};
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const int t = t0 + 16 * h + 4 * jj + i;
-                        const bool use = there && t >= lo_any && t < hi_any;
-                        const bool nan = ((w[i / 2] >> (16 * (i % 2))) & 0x7c00u) == 0x7c00u;
-                        if (!use || nan) w[i / 2] &= i % 2 ? 0x0000ffffu : 0xffff0000u;
-                        if (use && nan) bad |= 1u << (4 * jj + i);
-                    }
-                    vp[h] = make_uint2(w[0], w[1]);
-                    bad = __reduce_or_sync(kFull, bad);
-                    if (bad) {
-#pragma unroll
-                        for (int n = 0; n < NT; n++)
-#pragma unroll
-                            for (int k = 0; k < 4; k++) {
-                                const int t = 4 * (r >> 1) + (r & 1) + (k & 2);
-                                if (((bad >> t) & 1u) && t0 + 16 * h + t >= seen[n][k & 1].x && t0 + 16 * h + t < seen[n][k & 1].y)
-                                    s[h][n][k] = NAN;
-                            }
-                    }
-                }
-#pragma unroll
-                for (int n = 0; n < NT; n++) {
                     pb[h][n][0] = movmatrix_t(pack_h2(s[h][n][0], s[h][n][1]));
                     pb[h][n][1] = movmatrix_t(pack_h2(s[h][n][2], s[h][n][3]));
                 }
-            }
 #pragma unroll
             for (int h = 0; h < 2; h++) {
-                const uint32_t buf = ring + (at + h) * S::kTile;
                 uint32_t vw[4][VW];
 #pragma unroll
                 for (int i = 0; i < 4; i++) {  // token 4 jj + i: row jj + 4 i
-                    const uint32_t at_row = buf + kv_codes(D, 1) + (jj + 4 * i) * (D / 2);
+                    const uint32_t at_row = value_row + (at + h) * S::kTile + 4 * i * (D / 2);
                     if constexpr (D == 64)
-                        vw[i][0] = lds32(at_row + r * 4);
+                        vw[i][0] = lds32(at_row);
                     else if constexpr (D == 128)
-                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(vw[i][0]), "=r"(vw[i][1]) : "r"(at_row + ((r >> 1) ^ (2 * (jj >> 1))) * 16 + (r & 1) * 8));
+                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(vw[i][0]), "=r"(vw[i][1]) : "r"(at_row));
                     else {
-                        const uint4 v = lds128(at_row + (r ^ (2 * jj)) * 16);
+                        const uint4 v = lds128(at_row);
                         vw[i][0] = v.x;
                         vw[i][1] = v.y;
                         vw[i][2] = v.z;
@@ -468,9 +466,13 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
                 }
             }
             __syncwarp();
-            at = at + 2 == RING ? 0 : at + 2;
-            issue();
-            issue();
+            issue(at);
+            issue(at + 1);
+        };
+        for (int tile = tile0; tile < tile1; tile += RING) {
+#pragma unroll
+            for (int i = 0; i < RING; i += 2)
+                if (tile + i < tile1) unit(tile + i, i);
         }
         cp_async_wait<0>();
         __syncwarp();
@@ -610,10 +612,10 @@ int launch_of(const KvAttend &a, int head_dim, void *workspace, int sms, cudaStr
     // and unpacked half as often.
     const bool wide = a.q_tokens / a.batch * a.share > 8;
     if (head_dim == 64)
-        return wide ? launch_split<Split<64, 2, 16, 8>, T>(a, workspace, sms, st)
-                    : launch_split<Split<64, 1, 16, 8>, T>(a, workspace, sms, st);
+        return wide ? launch_split<Split<64, 2, 12, 4>, T>(a, workspace, sms, st)
+                    : launch_split<Split<64, 1, 16, 4>, T>(a, workspace, sms, st);
     if (head_dim == 128)
-        return wide ? launch_split<Split<128, 2, 12, 4>, T>(a, workspace, sms, st)
+        return wide ? launch_split<Split<128, 2, 8, 4>, T>(a, workspace, sms, st)
                     : launch_split<Split<128, 1, 16, 4>, T>(a, workspace, sms, st);
     return launch_split<Split<256, 1, 8, 4>, T>(a, workspace, sms, st);
 }
