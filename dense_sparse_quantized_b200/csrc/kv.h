@@ -69,32 +69,29 @@ struct KvAttend {
     const void *q;
     void *out;
     float *lse;
-    int64_t q_token, q_head, out_token, out_head, q_tokens;
+    int64_t q_token, q_head, out_token, out_head;
+    int q_tokens, rows_each;  // rows_each: of a sequence, without q_start
+    int most_tokens;          // that a sequence's pages hold
     int q_heads, share, batch, table_pages, causal, window;
     float scale_log2;  // scale * log2(e): the softmax runs in powers of two
     const int32_t *page_table, *kv_lens, *q_start;
 };
 
 // Rows and cached tokens of sequence b, clamped to what the buffers hold.
+// (Rows, and rows times heads, are below 2^31.)
 struct KvSeq {
-    int64_t row0;
-    int rows, len;
+    int row0, rows, len;
 };
 __device__ __forceinline__ KvSeq kv_seq(const KvAttend &a, int b) {
     KvSeq s;
-    int64_t r0, r1;
     if (a.q_start) {
-        r0 = min(max((int64_t)a.q_start[b], (int64_t)0), a.q_tokens);
-        r1 = min(max((int64_t)a.q_start[b + 1], r0), a.q_tokens);
+        s.row0 = min(max(a.q_start[b], 0), a.q_tokens);
+        s.rows = min(max(a.q_start[b + 1], s.row0), a.q_tokens) - s.row0;
     } else {
-        const int64_t n = a.q_tokens / a.batch;
-        r0 = b * n;
-        r1 = r0 + n;
+        s.row0 = b * a.rows_each;
+        s.rows = a.rows_each;
     }
-    s.row0 = r0;
-    s.rows = (int)(r1 - r0);
-    const int64_t most = (int64_t)a.table_pages * a.c.page_tokens;
-    s.len = (int)min(max((int64_t)a.kv_lens[b], (int64_t)0), most);
+    s.len = min(max(a.kv_lens[b], 0), a.most_tokens);
     return s;
 }
 

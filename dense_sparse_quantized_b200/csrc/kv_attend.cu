@@ -61,7 +61,9 @@ extern "C" int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_
     k.q_head = a->q_head;
     k.out_token = a->out_token;
     k.out_head = a->out_head;
-    k.q_tokens = a->q_tokens;
+    k.q_tokens = (int)a->q_tokens;
+    k.rows_each = a->q_start ? 0 : (int)(a->q_tokens / a->batch);
+    k.most_tokens = (int)((int64_t)a->table_pages * d->page_tokens);
     k.q_heads = a->q_heads;
     k.share = a->q_heads / d->kv_heads;
     k.share_by = kv_divisor(k.share);

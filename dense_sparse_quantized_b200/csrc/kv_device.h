@@ -120,7 +120,7 @@ __device__ __forceinline__ int2 seen_by(const KvAttend &a, const KvSeq &s, int r
 __device__ __forceinline__ int64_t row_at(const KvAttend &a, const KvSeq &s, int head, int rho, int64_t token_stride,
                                           int64_t head_stride) {
     const int i = a.share_by.div(rho);
-    return (s.row0 + i) * token_stride + (int64_t)(head * a.share + rho - i * a.share) * head_stride;
+    return (int64_t)(s.row0 + i) * token_stride + (int64_t)(head * a.share + rho - i * a.share) * head_stride;
 }
 
 __device__ __forceinline__ float lse_of(float top, float sum) {

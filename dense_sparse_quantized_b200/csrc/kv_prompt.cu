@@ -189,7 +189,7 @@ __device__ __forceinline__ int2 units_of(const KvAttend &a, const KvSeq &s, int 
 }
 template <int R>
 __device__ __forceinline__ int tiles_of(const KvAttend &a, const KvSeq &s) {
-    return (int)(((int64_t)s.rows * a.share + R - 1) / R);
+    return (int)(((uint32_t)(s.rows * a.share) + R - 1) / R);
 }
 
 // A piece of a CTA's run: units [t0, t1) of one job.

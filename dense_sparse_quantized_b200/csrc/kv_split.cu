@@ -7,7 +7,7 @@
 // head share its bytes.  A job's tokens are cut into units of 32; the units of
 // all jobs, in order, are dealt to the CTAs in equal runs, and a CTA's run to
 // its warps in equal runs, wherever the jobs begin and end: long and short
-// sequences and any number of heads fill the GPU alike.  Each warp finds its
+// sequences and any number of heads fill the GPU alike.  Each CTA finds its
 // place from kv_lens and q_start itself, so nothing is planned on the host
 // and a captured call follows the lengths.
 //
@@ -60,7 +60,7 @@ struct SplitParams {
     KvAttend a;
     float *parts;
     KvCarry *carries;
-    int min_run;  // least units of a CTA's run
+    int min_run;  // least units of a CTA's run; 0: a job a CTA
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -131,10 +131,78 @@ __device__ __forceinline__ Jobs jobs_of(const KvAttend &a, int b) {
     static_cast<KvSeq &>(j) = kv_seq(a, b);
     j.lo = a.window ? max(0, j.len - j.rows - a.window + 1) : 0;
     j.units = max(1, (j.len + 31) / 32 - j.lo / 32);
-    j.tiles = (int)(((int64_t)j.rows * a.share + R - 1) / R);
+    j.tiles = (int)(((uint32_t)(j.rows * a.share) + R - 1) / R);
     j.weight = (int64_t)a.c.kv_heads * j.tiles * j.units;
     return j;
 }
+
+__device__ __forceinline__ int64_t divide(int64_t n, int d) {  // n >= 0, d > 0
+    return n >> 32 ? n / d : (int64_t)((uint32_t)n / (uint32_t)d);
+}
+
+// A CTA's run: `size` units from unit `first` on, in or behind sequence b, the
+// units before which are `before`; all runs but the last are `of` units long.
+struct Run {
+    int64_t first, before, of;
+    int b, size;
+};
+
+// Finds it (one warp).  Where a CTA takes one job, job numbers are searched
+// instead of unit numbers, and units counted from the sequence's first.
+template <int R>
+__device__ __forceinline__ void find_run(const KvAttend &a, int min_run, Run &run) {
+    const int lane = threadIdx.x & 31;
+    auto weight = [&](int b) -> int64_t {
+        if (b >= a.batch) return 0;
+        const Jobs j = jobs_of<R>(a, b);
+        return min_run ? j.weight : (int64_t)a.c.kv_heads * j.tiles;
+    };
+    const int64_t w0 = weight(lane);  // of the first 32 sequences, for both passes
+    int64_t first = blockIdx.x, of = 1, total = 0;
+    if (min_run) {
+        total = w0;
+        for (int b = lane + 32; b < a.batch; b += 32) total += weight(b);
+#pragma unroll
+        for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(kFull, total, m);
+        of = max(divide(total + gridDim.x - 1, gridDim.x), (int64_t)min_run);
+        first *= of;
+    }
+    int b = a.batch;
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+        const int64_t w = b0 == 0 ? w0 : weight(b0 + lane);
+        int64_t sum = w;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int64_t up = __shfl_up_sync(kFull, sum, m);
+            if (lane >= m) sum += up;
+        }
+        const uint32_t past = __ballot_sync(kFull, before + sum > first);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            b = b0 + l;
+            before += __shfl_sync(kFull, sum - w, l);
+            break;
+        }
+        before += __shfl_sync(kFull, sum, 31);
+    }
+    int64_t size = 0;
+    if (b < a.batch) {
+        size = min(of, total - first);
+        if (!min_run) {
+            const int units = jobs_of<R>(a, b).units;
+            first = (first - before) * units;
+            before = 0;
+            size = units;
+        }
+    }
+    if (lane == 0) run = {first, before, of, b, (int)size};
+}
+
+// A partial result in shared memory: a warp's accumulators as they are, two
+// floats a lane, then the rows' maxima and sums.
+template <int D>
+__device__ __forceinline__ int part_at(int nc, int i, int lane) { return ((nc * (D / 16) + i) * 32 + lane) * 2; }
 
 template <typename S, typename T>
 __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_constant__ SplitParams p) {
@@ -143,7 +211,8 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
     constexpr int VW = D / 64;   // and of its value dimensions
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int head_valid[NW], head_ended[NW], tail_valid[NW];
-    __shared__ int job_id[NW + 1][3];  // (b, kv head, row tile) of each warp's last job; [NW]: of the CTA's first
+    __shared__ int job_id[NW][3];      // (b, kv head, row tile) of each warp's last job
+    __shared__ Run run;
     __shared__ int64_t job_end[NW];    // unit behind the last job's last
     const KvAttend &a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, jj = lane & 3;
@@ -160,53 +229,28 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
 
     kv_after_previous();
 
-    // Total work, and this warp's run [u, u_end) of it.
-    int64_t total = 0;
-    for (int b = lane; b < a.batch; b += 32) total += jobs_of<R>(a, b).weight;
-#pragma unroll
-    for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(kFull, total, m);
-    const int64_t run = max((total + gridDim.x - 1) / gridDim.x, (int64_t)p.min_run);
-    const int64_t cta0 = min(total, run * blockIdx.x), cta1 = min(total, cta0 + run);
-    const int64_t mine = (cta1 - cta0 + NW - 1) / NW;
-    int64_t u = min(cta1, cta0 + warp * mine);
-    const int64_t u_end = min(cta1, u + mine);
+    if (threadIdx.x == 0 && p.min_run) p.carries[blockIdx.x].valid = 0;
+    if (warp == 0) find_run<R>(a, p.min_run, run);
     if (lane == 0) head_valid[warp] = head_ended[warp] = tail_valid[warp] = 0;
-    if (threadIdx.x == 0) p.carries[blockIdx.x].valid = 0;
+    __syncthreads();
 
-    // The sequence u lies in, and the units before that sequence.
-    int b = 0;
-    int64_t before = 0;
-    if (u < u_end) {
-        for (int b0 = 0; b0 < a.batch; b0 += 32) {
-            const int64_t w = b0 + lane < a.batch ? jobs_of<R>(a, b0 + lane).weight : 0;
-            int64_t sum = w;
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const int64_t up = __shfl_up_sync(kFull, sum, m);
-                if (lane >= m) sum += up;
-            }
-            const uint32_t past = __ballot_sync(kFull, before + sum > u);
-            if (past) {
-                const int l = __ffs(past) - 1;
-                b = b0 + l;
-                before += __shfl_sync(kFull, sum - w, l);
-                break;
-            }
-            before += __shfl_sync(kFull, sum, 31);
-        }
-    }
-
+    // This warp's run [u, u_end) of the units of all jobs; `before` of them are
+    // those of the sequences before b.
+    int b = run.b;
+    int64_t before = run.before;
+    const int mine = (run.size + NW - 1) / NW, skip = min(run.size, warp * mine);
+    int64_t u = run.first + skip;
+    const int64_t u_end = u + min(mine, run.size - skip);
     while (u < u_end && b < a.batch) {
-        Jobs j = jobs_of<R>(a, b);
+        const Jobs j = jobs_of<R>(a, b);
         if (u >= before + j.weight) {
             before += j.weight;
             b++;
             continue;
         }
         // The job, and the units of it that are in this run.
-        const int64_t rel = u - before;
-        const int64_t job = rel / j.units;
-        const int head = (int)(job / j.tiles), qt = (int)(job % j.tiles);
+        const int64_t rel = u - before, job = divide(rel, j.units);
+        const int head = (int)divide(job, j.tiles), qt = (int)(job - (int64_t)head * j.tiles);
         const int first = (int)(rel - job * j.units);
         const int last = (int)min((int64_t)j.units, first + (u_end - u));  // units [first, last) of the job
         const int rho0 = qt * R, rho1 = min(rho0 + R, j.rows * a.share) - 1;
@@ -515,7 +559,7 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
                     const int row_n = 8 * n + 2 * jj + c;
 #pragma unroll
                     for (int i = 0; i < D / 16; i++)
-                        *reinterpret_cast<float2 *>(dst + row_n * D + r * (D / 8) + 2 * i) = make_float2(o[i][n][c], o[i][n][2 + c]);
+                        *reinterpret_cast<float2 *>(dst + part_at<D>(2 * n + c, i, lane)) = make_float2(o[i][n][c], o[i][n][2 + c]);
                     if (r == 0) {
                         dst[R * D + row_n] = m[n][c];
                         dst[R * D + R + row_n] = l[n][c];
@@ -560,30 +604,31 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
         } else {
             to = p.parts + (2 * blockIdx.x + (w < 0 ? 0 : 1)) * kv_part_floats<D, R>();
             if (w >= 0 && threadIdx.x == 0) {
-                const KvCarry mt = {1, (int)((job_end[w] - 1) / run) - (int)blockIdx.x, job_id[w][0], job_id[w][1], job_id[w][2], {}};
+                const KvCarry mt = {1, (int)divide(job_end[w] - 1, (int)run.of) - (int)blockIdx.x, job_id[w][0], job_id[w][1], job_id[w][2], {}};
                 p.carries[blockIdx.x] = mt;
             }
         }
         for (int i = threadIdx.x; i < R * D / 2; i += NW * 32) {
-            const int row = i / (D / 2), d = i % (D / 2) * 2;
+            // the i-th pair of the accumulators: lane i % 32's
+            const int nc = i / (32 * (D / 16)), l = i % 32;
+            const int row = nc / 2 * 8 + 2 * (l & 3) + nc % 2, d = (l >> 2) * (D / 8) + i / 32 % (D / 16) * 2;
             float top = kNoMax, sum = 0.0f, x = 0.0f, y = 0.0f;
-            for (int k2 = 0; k2 < n; k2++) top = fmaxf(top, part(k2)[R * D + row]);
+#pragma unroll 4
             for (int k2 = 0; k2 < n; k2++) {
                 const float *src = part(k2);
-                const float f = ex2(src[R * D + row] - top);
-                const float2 v = *reinterpret_cast<const float2 *>(src + row * D + d);
-                sum += f * src[R * D + R + row];
-                x += f * v.x;
-                y += f * v.y;
+                const float m = src[R * D + row], next = fmaxf(top, m), keep = ex2(top - next), f = ex2(m - next);
+                const float2 v = *reinterpret_cast<const float2 *>(src + 2 * i);
+                top = next;
+                sum = sum * keep + f * src[R * D + R + row];
+                x = x * keep + f * v.x;
+                y = y * keep + f * v.y;
             }
             if (whole) {
                 if (rho0 + row >= j.rows * a.share) continue;
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                 *reinterpret_cast<uint32_t *>((T *)a.out + row_at(a, j, head, rho0 + row, a.out_token, a.out_head) + d) =
                     pack_out<T>(x * inv, y * inv);
-                if (a.lse && d == 0)
-                    a.lse[row_at(a, j, head, rho0 + row, a.q_heads, 1)] =
-                        lse_of(top, sum);
+                if (a.lse && d == 0) a.lse[row_at(a, j, head, rho0 + row, a.q_heads, 1)] = lse_of(top, sum);
             } else {
                 *reinterpret_cast<float2 *>(to + row * D + d) = make_float2(x, y);
                 if (d == 0) {
@@ -597,13 +642,21 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
 
 template <typename S, typename T>
 int launch_split(const KvAttend &a, void *workspace, int sms, cudaStream_t st) {
-    const SplitParams p = {a, (float *)workspace, kv_carries<S::D, S::R>(workspace), 4};
+    // A job a CTA where every job has an SM and at most four units a warp: no
+    // joining, one launch (32 jobs of 333 tokens: 12 us dealt out evenly).
+    const int64_t most_rows = a.q_start ? a.q_tokens : a.rows_each;
+    const int64_t jobs = a.c.kv_heads * (a.q_start ? a.batch + (int64_t)a.q_tokens * a.share / S::R
+                                                    : a.batch * ((most_rows * a.share + S::R - 1) / S::R));
+    int64_t tokens = (int64_t)a.table_pages * a.c.page_tokens;
+    if (a.window) tokens = std::min(tokens, a.window + most_rows);
+    const bool one_each = jobs <= sms && tokens / 32 + 2 <= 4 * S::NW;
+    const SplitParams p = {a, (float *)workspace, kv_carries<S::D, S::R>(workspace), one_each ? 0 : 4};
     auto kernel = split_kernel<S, T>;
     static KvOnce once;
     if (!once.set_smem((const void *)kernel, S::kSmem)) return DSQ_ERR_CUDA;
-    const int grid = std::min(sms, kMaxCtas);
+    const int grid = one_each ? (int)jobs : std::min(sms, kMaxCtas);
     const int rc = kv_launch(kernel, grid, S::NW * 32, S::kSmem, st, p);
-    return rc != DSQ_OK ? rc : launch_join<S::D, S::R, T>(a, p.parts, p.carries, grid, st);
+    return rc != DSQ_OK || one_each ? rc : launch_join<S::D, S::R, T>(a, p.parts, p.carries, grid, st);
 }
 
 template <typename T>
