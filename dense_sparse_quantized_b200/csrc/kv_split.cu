@@ -61,6 +61,7 @@ struct SplitParams {
     float *parts;
     KvCarry *carries;
     int min_run;  // least units of a CTA's run; 0: a job a CTA
+    int shift;    // units of 32 << shift tokens: 0 unless their number could pass 31 bits
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -123,58 +124,54 @@ struct Copy {
 // The jobs of a sequence.
 struct Jobs : KvSeq {
     int lo, units, tiles;  // first token any query sees, units of a job, row tiles
-    int64_t weight;        // units of all of the sequence's jobs
+    int weight;            // units of all of the sequence's jobs
 };
 template <int R>
-__device__ __forceinline__ Jobs jobs_of(const KvAttend &a, int b) {
+__device__ __forceinline__ Jobs jobs_of(const KvAttend &a, int b, int shift) {
     Jobs j;
     static_cast<KvSeq &>(j) = kv_seq(a, b);
     j.lo = a.window ? max(0, j.len - j.rows - a.window + 1) : 0;
-    j.units = max(1, (j.len + 31) / 32 - j.lo / 32);
+    j.units = max(1, ((j.len + (32 << shift) - 1) >> (5 + shift)) - (j.lo >> (5 + shift)));
     j.tiles = (int)(((uint32_t)(j.rows * a.share) + R - 1) / R);
-    j.weight = (int64_t)a.c.kv_heads * j.tiles * j.units;
+    j.weight = a.c.kv_heads * j.tiles * j.units;
     return j;
-}
-
-__device__ __forceinline__ int64_t divide(int64_t n, int d) {  // n >= 0, d > 0
-    return n >> 32 ? n / d : (int64_t)((uint32_t)n / (uint32_t)d);
 }
 
 // A CTA's run: `size` units from unit `first` on, in or behind sequence b, the
 // units before which are `before`; all runs but the last are `of` units long.
 struct Run {
-    int64_t first, before, of;
-    int b, size;
+    int first, before, of, b, size;
 };
 
 // Finds it (one warp).  Where a CTA takes one job, job numbers are searched
 // instead of unit numbers, and units counted from the sequence's first.
 template <int R>
-__device__ __forceinline__ void find_run(const KvAttend &a, int min_run, Run &run) {
+__device__ __forceinline__ void find_run(const SplitParams &p, Run &run) {
+    const KvAttend &a = p.a;
     const int lane = threadIdx.x & 31;
-    auto weight = [&](int b) -> int64_t {
+    auto weight = [&](int b) {
         if (b >= a.batch) return 0;
-        const Jobs j = jobs_of<R>(a, b);
-        return min_run ? j.weight : (int64_t)a.c.kv_heads * j.tiles;
+        const Jobs j = jobs_of<R>(a, b, p.shift);
+        return p.min_run ? j.weight : a.c.kv_heads * j.tiles;
     };
-    const int64_t w0 = weight(lane);  // of the first 32 sequences, for both passes
-    int64_t first = blockIdx.x, of = 1, total = 0;
-    if (min_run) {
+    const int w0 = weight(lane);  // of the first 32 sequences, for both passes
+    int first = blockIdx.x, of = 1, total = 0;
+    if (p.min_run) {
         total = w0;
+#pragma unroll 1
         for (int b = lane + 32; b < a.batch; b += 32) total += weight(b);
-#pragma unroll
-        for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(kFull, total, m);
-        of = max(divide(total + gridDim.x - 1, gridDim.x), (int64_t)min_run);
-        first *= of;
+        total = (int)__reduce_add_sync(kFull, (uint32_t)total);
+        of = max((int)(((uint32_t)total + gridDim.x - 1) / gridDim.x), p.min_run);
+        first = (int)min((uint32_t)total, (uint32_t)first * (uint32_t)of);
     }
-    int b = a.batch;
-    int64_t before = 0;
+    int b = a.batch, before = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
-        const int64_t w = b0 == 0 ? w0 : weight(b0 + lane);
-        int64_t sum = w;
+        const int w = b0 == 0 ? w0 : weight(b0 + lane);
+        int sum = w;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
-            const int64_t up = __shfl_up_sync(kFull, sum, m);
+            const int up = __shfl_up_sync(kFull, sum, m);
             if (lane >= m) sum += up;
         }
         const uint32_t past = __ballot_sync(kFull, before + sum > first);
@@ -186,17 +183,16 @@ __device__ __forceinline__ void find_run(const KvAttend &a, int min_run, Run &ru
         }
         before += __shfl_sync(kFull, sum, 31);
     }
-    int64_t size = 0;
+    int size = 0;
     if (b < a.batch) {
         size = min(of, total - first);
-        if (!min_run) {
-            const int units = jobs_of<R>(a, b).units;
-            first = (first - before) * units;
+        if (!p.min_run) {
+            size = jobs_of<R>(a, b, p.shift).units;
+            first = (first - before) * size;
             before = 0;
-            size = units;
         }
     }
-    if (lane == 0) run = {first, before, of, b, (int)size};
+    if (lane == 0) run = {first, before, of, b, size};
 }
 
 // A partial result in shared memory: a warp's accumulators as they are, two
@@ -213,7 +209,7 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
     __shared__ int head_valid[NW], head_ended[NW], tail_valid[NW];
     __shared__ int job_id[NW][3];      // (b, kv head, row tile) of each warp's last job
     __shared__ Run run;
-    __shared__ int64_t job_end[NW];    // unit behind the last job's last
+    __shared__ int job_end[NW];        // unit behind the last job's last
     const KvAttend &a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, jj = lane & 3;
     const uint32_t ring = smem_u32(smem) + warp * S::kWarp;
@@ -230,42 +226,49 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
     kv_after_previous();
 
     if (threadIdx.x == 0 && p.min_run) p.carries[blockIdx.x].valid = 0;
-    if (warp == 0) find_run<R>(a, p.min_run, run);
+    if (warp == 0) find_run<R>(p, run);
     if (lane == 0) head_valid[warp] = head_ended[warp] = tail_valid[warp] = 0;
     __syncthreads();
 
     // This warp's run [u, u_end) of the units of all jobs; `before` of them are
     // those of the sequences before b.
-    int b = run.b;
-    int64_t before = run.before;
+    int b = run.b, before = run.before;
     const int mine = (run.size + NW - 1) / NW, skip = min(run.size, warp * mine);
-    int64_t u = run.first + skip;
-    const int64_t u_end = u + min(mine, run.size - skip);
+    int u = run.first + skip;
+    const int u_end = u + min(mine, run.size - skip);
     while (u < u_end && b < a.batch) {
-        const Jobs j = jobs_of<R>(a, b);
+        const Jobs j = jobs_of<R>(a, b, p.shift);
         if (u >= before + j.weight) {
             before += j.weight;
             b++;
             continue;
         }
         // The job, and the units of it that are in this run.
-        const int64_t rel = u - before, job = divide(rel, j.units);
-        const int head = (int)divide(job, j.tiles), qt = (int)(job - (int64_t)head * j.tiles);
-        const int first = (int)(rel - job * j.units);
-        const int last = (int)min((int64_t)j.units, first + (u_end - u));  // units [first, last) of the job
+        const int rel = u - before, job = (int)((uint32_t)rel / (uint32_t)j.units);
+        const int head = j.tiles == 1 ? job : (int)((uint32_t)job / (uint32_t)j.tiles), qt = job - head * j.tiles;
+        const int first = rel - job * j.units;
+        const int last = min(j.units, first + (u_end - u));  // units [first, last) of the job
         const int rho0 = qt * R, rho1 = min(rho0 + R, j.rows * a.share) - 1;
         const int2 seen0 = seen_by(a, j, rho0), seen1 = seen_by(a, j, rho1);
         const int lo_any = seen0.x, hi_any = seen1.y, lo_all = seen1.x, hi_all = seen0.y;
         // Tiles of 16 tokens: those of the units, less what no row sees.
-        const int unit0 = j.lo / 32;
-        const int tile0 = max((unit0 + first) * 2, lo_any / 32 * 2);
-        const int tile1 = min((unit0 + last) * 2, (max(hi_any, 0) + 15) / 16);
+        const int unit0 = j.lo >> (5 + p.shift);
+        const int tile0 = max((unit0 + first) << (1 + p.shift), lo_any / 32 * 2);
+        const int tile1 = min((unit0 + last) << (1 + p.shift), (max(hi_any, 0) + 15) / 16);
 
         // Page numbers of the next 64 table columns, one per lane and register.
         int col = a.tiles_by.div(tile0), col0 = col, in_page = tile0 - col * a.c.page_tiles;
         const int32_t *row = a.page_table + (int64_t)b * a.table_pages;
         auto pages_from = [&](int c) { return c + lane < a.table_pages ? row[c + lane] : -1; };
         int pages = pages_from(col0), pages_next = pages_from(col0 + 32);
+        uint4 raw[NT][KW];
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            const uint4 *from = reinterpret_cast<const uint4 *>(
+                (const T *)a.q + row_at(a, j, head, min(rho0 + 8 * n + r, rho1), a.q_token, a.q_head) + jj * (D / 4));
+#pragma unroll
+            for (int w = 0; w < KW; w++) raw[n][w] = from[w];
+        }
         const uint8_t *const base = a.c.cache + (int64_t)head * a.c.page_tiles * S::kTile + lane * 16;
         const uint8_t *src = nullptr;     // this lane's chunk of the next tile
         int left = tile1 - tile0, rest = 0;  // tiles to copy; of them on this page
@@ -301,12 +304,7 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
         const uint32_t sign = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
         for (int n = 0; n < NT; n++) {
-            const int rho = min(rho0 + 8 * n + r, rho1);
-            uint4 x[KW];
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                (const T *)a.q + row_at(a, j, head, rho, a.q_token, a.q_head) + jj * (D / 4));
-#pragma unroll
-            for (int w = 0; w < KW; w++) x[w] = src[w];
+            uint4(&x)[KW] = raw[n];
             int up = 0;
             if constexpr (!std::is_same<T, __half>::value) {  // four lanes share the row
                 uint32_t top = 0;
@@ -582,46 +580,53 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
     }
     __syncthreads();
 
-    // What spans warps: every chain of partial results, first to last.
-    for (int w = -1; w < NW; w++) {
-        if (w < 0 ? !head_valid[0] : !tail_valid[w]) continue;
-        int n = w < 0 ? 0 : 1, k = w + 1;  // partial results: warp w's last, then the first ones of warps w + 1 .. w + n
-        bool ended = false;
-        for (; k < NW && head_valid[k] && !ended; k++, n++) ended = head_ended[k];
+    // What spans warps: chains of partial results, a warp's last (or the CTA's
+    // very first) and the first ones of the warps behind it.  The warps share
+    // out the chains.
+    const uint32_t hv = __ballot_sync(kFull, lane < NW && head_valid[lane % NW]);
+    const uint32_t he = __ballot_sync(kFull, lane < NW && head_ended[lane % NW]);
+    const uint32_t tv = __ballot_sync(kFull, lane < NW && tail_valid[lane % NW]);
+    const int chains = (int)(hv & 1u) + __popc(tv), group = max(1, NW / max(1, chains));
+#pragma unroll 1
+    for (int c = warp / group; c < chains; c += (NW + group - 1) / group) {
+        uint32_t later = tv;
+        for (int i = (int)(hv & 1u); i < c; i++) later &= later - 1;
+        const int w = (hv & 1u) && c == 0 ? -1 : __ffs(later) - 1;
+        const uint32_t heads = hv >> (w + 1), ends = he >> (w + 1);
+        const int run_of = __ffs(~heads) - 1, end = __ffs(ends & heads) - 1;
+        const bool ended = end >= 0 && end < run_of;
+        const int n = (w < 0 ? 0 : 1) + (ended ? end + 1 : run_of);
         auto part = [&](int i) {
             const bool tail = w >= 0 && i == 0;
             const int of = w < 0 ? i : w + i;
             return reinterpret_cast<const float *>(smem + of * S::kWarp + (tail ? 0 : RING * S::kTile));
         };
         const bool whole = w >= 0 && ended;
-        Jobs j;
+        KvSeq j = {};
         int head = 0, rho0 = 0;
-        float *to = nullptr;
+        float *const to = p.parts + (2 * blockIdx.x + (w < 0 ? 0 : 1)) * kv_part_floats<D, R>();
         if (whole) {
-            j = jobs_of<R>(a, job_id[w][0]);
+            j = kv_seq(a, job_id[w][0]);
             head = job_id[w][1];
             rho0 = job_id[w][2] * R;
-        } else {
-            to = p.parts + (2 * blockIdx.x + (w < 0 ? 0 : 1)) * kv_part_floats<D, R>();
-            if (w >= 0 && threadIdx.x == 0) {
-                const KvCarry mt = {1, (int)divide(job_end[w] - 1, (int)run.of) - (int)blockIdx.x, job_id[w][0], job_id[w][1], job_id[w][2], {}};
-                p.carries[blockIdx.x] = mt;
-            }
+        } else if (w >= 0 && warp % group == 0 && lane == 0) {
+            const KvCarry mt = {1, (int)((uint32_t)(job_end[w] - 1) / (uint32_t)run.of) - (int)blockIdx.x, job_id[w][0], job_id[w][1], job_id[w][2], {}};
+            p.carries[blockIdx.x] = mt;
         }
-        for (int i = threadIdx.x; i < R * D / 2; i += NW * 32) {
-            // the i-th pair of the accumulators: lane i % 32's
-            const int nc = i / (32 * (D / 16)), l = i % 32;
-            const int row = nc / 2 * 8 + 2 * (l & 3) + nc % 2, d = (l >> 2) * (D / 8) + i / 32 % (D / 16) * 2;
+#pragma unroll 1
+        for (int at = warp % group; at < R * D / 64; at += group) {  // the accumulators' pairs, 32 lanes at a time
+            const int nc = at / (D / 16), row = nc / 2 * 8 + 2 * jj + nc % 2, d = r * (D / 8) + at % (D / 16) * 2;
             float top = kNoMax, sum = 0.0f, x = 0.0f, y = 0.0f;
 #pragma unroll 4
-            for (int k2 = 0; k2 < n; k2++) {
-                const float *src = part(k2);
-                const float m = src[R * D + row], next = fmaxf(top, m), keep = ex2(top - next), f = ex2(m - next);
-                const float2 v = *reinterpret_cast<const float2 *>(src + 2 * i);
-                top = next;
-                sum = sum * keep + f * src[R * D + R + row];
-                x = x * keep + f * v.x;
-                y = y * keep + f * v.y;
+            for (int k = 0; k < n; k++) top = fmaxf(top, part(k)[R * D + row]);
+#pragma unroll 4
+            for (int k = 0; k < n; k++) {
+                const float *src = part(k);
+                const float f = ex2(src[R * D + row] - top);
+                const float2 v = *reinterpret_cast<const float2 *>(src + (at * 32 + lane) * 2);
+                sum += f * src[R * D + R + row];
+                x += f * v.x;
+                y += f * v.y;
             }
             if (whole) {
                 if (rho0 + row >= j.rows * a.share) continue;
@@ -650,7 +655,10 @@ int launch_split(const KvAttend &a, void *workspace, int sms, cudaStream_t st) {
     int64_t tokens = (int64_t)a.table_pages * a.c.page_tokens;
     if (a.window) tokens = std::min(tokens, a.window + most_rows);
     const bool one_each = jobs <= sms && tokens / 32 + 2 <= 4 * S::NW;
-    const SplitParams p = {a, (float *)workspace, kv_carries<S::D, S::R>(workspace), one_each ? 0 : 4};
+    int shift = 0;
+    while ((double)a.c.kv_heads * (a.batch + (double)a.q_tokens * a.share / S::R) * ((a.most_tokens >> (5 + shift)) + 2) >= 2147483648.0)
+        shift++;
+    const SplitParams p = {a, (float *)workspace, kv_carries<S::D, S::R>(workspace), one_each ? 0 : 4, shift};
     auto kernel = split_kernel<S, T>;
     static KvOnce once;
     if (!once.set_smem((const void *)kernel, S::kSmem)) return DSQ_ERR_CUDA;
