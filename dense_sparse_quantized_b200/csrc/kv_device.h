@@ -165,28 +165,33 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ KvAtt
 #pragma unroll
         for (int e = 0; e < E; e++) x[n][e] = 0.0f;
     }
+    auto part_of = [&](int i) { return parts + (2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * kv_part_floats<D, R>() + row0 * D; };
+    const int maxima = (R - row0) * D + row0;  // from there on
+#pragma unroll 4
+    for (int i = 0; i <= c.more; i++)
+#pragma unroll
+        for (int n = 0; n < N; n++) top[n] = fmaxf(top[n], part_of(i)[maxima + 8 * n]);
+#pragma unroll 2
     for (int i = 0; i <= c.more; i++) {
-        const float *part = parts + (2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * kv_part_floats<D, R>();
+        const float *part = part_of(i);
         float v[N][E], m[N], l[N];
 #pragma unroll
         for (int n = 0; n < N; n++) {
-            const int row = row0 + 8 * n;
-            m[n] = part[R * D + row];
-            l[n] = part[R * D + R + row];
+            m[n] = part[maxima + 8 * n];
+            l[n] = part[maxima + R + 8 * n];
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
-                const float2 f = *reinterpret_cast<const float2 *>(part + row * D + lane * E + e);
+                const float2 f = *reinterpret_cast<const float2 *>(part + 8 * n * D + lane * E + e);
                 v[n][e] = f.x;
                 v[n][e + 1] = f.y;
             }
         }
 #pragma unroll
         for (int n = 0; n < N; n++) {
-            const float next = fmaxf(top[n], m[n]), keep = ex2(top[n] - next), f = ex2(m[n] - next);
-            top[n] = next;
-            sum[n] = sum[n] * keep + l[n] * f;
+            const float f = ex2(m[n] - top[n]);
+            sum[n] += l[n] * f;
 #pragma unroll
-            for (int e = 0; e < E; e++) x[n][e] = x[n][e] * keep + v[n][e] * f;
+            for (int e = 0; e < E; e++) x[n][e] += v[n][e] * f;
         }
     }
 #pragma unroll

@@ -613,29 +613,39 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
             const KvCarry mt = {1, (int)((uint32_t)(job_end[w] - 1) / (uint32_t)run.of) - (int)blockIdx.x, job_id[w][0], job_id[w][1], job_id[w][2], {}};
             p.carries[blockIdx.x] = mt;
         }
+        // Accumulators 4 i0 .. 4 i0 + 3 of row group nc at a time: they share
+        // the rows' factors.
+        constexpr int kSub = D / 64;
 #pragma unroll 1
-        for (int at = warp % group; at < R * D / 64; at += group) {  // the accumulators' pairs, 32 lanes at a time
-            const int nc = at / (D / 16), row = nc / 2 * 8 + 2 * jj + nc % 2, d = r * (D / 8) + at % (D / 16) * 2;
-            float top = kNoMax, sum = 0.0f, x = 0.0f, y = 0.0f;
+        for (int item = warp % group; item < 2 * NT * kSub; item += group) {
+            const int nc = item / kSub, i0 = item % kSub * 4, row = nc / 2 * 8 + 2 * jj + nc % 2, d = r * (D / 8) + i0 * 2;
+            float top = kNoMax, sum = 0.0f;
+            float2 x[4] = {};
 #pragma unroll 4
             for (int k = 0; k < n; k++) top = fmaxf(top, part(k)[R * D + row]);
 #pragma unroll 4
             for (int k = 0; k < n; k++) {
                 const float *src = part(k);
                 const float f = ex2(src[R * D + row] - top);
-                const float2 v = *reinterpret_cast<const float2 *>(src + (at * 32 + lane) * 2);
                 sum += f * src[R * D + R + row];
-                x += f * v.x;
-                y += f * v.y;
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const float2 v = *reinterpret_cast<const float2 *>(src + part_at<D>(nc, i0 + i, lane));
+                    x[i].x += f * v.x;
+                    x[i].y += f * v.y;
+                }
             }
             if (whole) {
                 if (rho0 + row >= j.rows * a.share) continue;
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                *reinterpret_cast<uint32_t *>((T *)a.out + row_at(a, j, head, rho0 + row, a.out_token, a.out_head) + d) =
-                    pack_out<T>(x * inv, y * inv);
+                *reinterpret_cast<uint4 *>((T *)a.out + row_at(a, j, head, rho0 + row, a.out_token, a.out_head) + d) =
+                    make_uint4(pack_out<T>(x[0].x * inv, x[0].y * inv), pack_out<T>(x[1].x * inv, x[1].y * inv),
+                               pack_out<T>(x[2].x * inv, x[2].y * inv), pack_out<T>(x[3].x * inv, x[3].y * inv));
                 if (a.lse && d == 0) a.lse[row_at(a, j, head, rho0 + row, a.q_heads, 1)] = lse_of(top, sum);
             } else {
-                *reinterpret_cast<float2 *>(to + row * D + d) = make_float2(x, y);
+                float4 *dst = reinterpret_cast<float4 *>(to + row * D + d);
+                dst[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+                dst[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
                 if (d == 0) {
                     to[R * D + row] = top;
                     to[R * D + R + row] = sum;
@@ -647,14 +657,14 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
 
 template <typename S, typename T>
 int launch_split(const KvAttend &a, void *workspace, int sms, cudaStream_t st) {
-    // A job a CTA where every job has an SM and at most four units a warp: no
+    // A job a CTA where every job has an SM and at most six units a warp: no
     // joining, one launch (32 jobs of 333 tokens: 12 us dealt out evenly).
     const int64_t most_rows = a.q_start ? a.q_tokens : a.rows_each;
     const int64_t jobs = a.c.kv_heads * (a.q_start ? a.batch + (int64_t)a.q_tokens * a.share / S::R
                                                     : a.batch * ((most_rows * a.share + S::R - 1) / S::R));
     int64_t tokens = (int64_t)a.table_pages * a.c.page_tokens;
     if (a.window) tokens = std::min(tokens, a.window + most_rows);
-    const bool one_each = jobs <= sms && tokens / 32 + 2 <= 4 * S::NW;
+    const bool one_each = jobs <= sms && tokens / 32 + 2 <= 6 * S::NW;
     int shift = 0;
     while ((double)a.c.kv_heads * (a.batch + (double)a.q_tokens * a.share / S::R) * ((a.most_tokens >> (5 + shift)) + 2) >= 2147483648.0)
         shift++;
