@@ -10,7 +10,8 @@
 // joined through the workspace, in order.
 //
 // A CTA works on two row tiles of 128 at once (one at 256 dimensions), so that
-// one tile's products run under the other's softmax:
+// one tile's products run under the other's softmax; a job of one row tile is
+// worked on twice, in every other unit, and put together at its end:
 //   warps 0-3, 4-7  softmax of row tile 0, 1: thread = row.  Reads its 128
 //                   scores from tensor memory, raises the running maximum if
 //                   one exceeds it by more than 2^8 in the numerator (then the
@@ -78,8 +79,9 @@ struct PromptParams {
 };
 
 struct Shared {
-    uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2][2], qfull[2], ofull[2];
+    uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2][2], qfull[2], ofull[2], other, joined;
     uint4 nans[kFlags], holes[kFlags];  // by loading warp: NaN tokens; sub-tiles without a page
+    float other_m[128], other_l[128];   // of a shared job, the second pair's maxima and sums
     uint32_t tmem;
     int b, head, qt, first;  // where this CTA's run begins: the job, and how much of its cost lies before
     int left;                // cost of the run
@@ -233,13 +235,28 @@ struct Walk {
     }
 };
 
-// Units of the piece that row tile r of it works on: none if it has no rows.
+// What the r-th pair of softmax and product warps does of a piece: rows
+// [first, end) of the job's kv head, units x, x + step, ... below y (none: y =
+// x).  A job of 128 rows or fewer is shared by units, else by row tiles.
+struct Share {
+    int first, end, x, y, step;
+    bool shared;
+};
 template <int R>
-__device__ __forceinline__ int2 active(const KvAttend &a, const Piece &p, int r) {
-    const int first = p.qt * R + 128 * r, last = min(min(first + 128, (p.qt + 1) * R), p.s.rows * a.share) - 1;
-    if (first > last) return make_int2(p.t0, p.t0);
-    const int lo = max(p.t0, seen_by(a, p.s, first).x / kN);
-    return make_int2(lo, max(lo, min(p.t1, (max(seen_by(a, p.s, last).y, 0) + kN - 1) / kN)));
+__device__ __forceinline__ Share share_of(const KvAttend &a, const Piece &p, int r) {
+    Share w;
+    const int rows = min((p.qt + 1) * R, p.s.rows * a.share);
+    w.shared = R > 128 && rows - p.qt * R <= 128;
+    w.step = w.shared ? 2 : 1;
+    w.first = p.qt * R + (w.shared ? 0 : 128 * r);
+    w.end = min(w.first + 128, rows);
+    w.x = w.y = p.t0;
+    if (w.first < w.end) {
+        w.x = max(p.t0, seen_by(a, p.s, w.first).x / kN);
+        w.y = max(w.x, min(p.t1, (max(seen_by(a, p.s, w.end - 1).y, 0) + kN - 1) / kN));
+        if (w.shared) w.x = min(w.x + r, w.y);
+    }
+    return w;
 }
 
 // Finds this CTA's run (one warp).
@@ -512,10 +529,10 @@ __device__ __forceinline__ void product_role(const KvAttend &a, Shared &sh, uint
     Piece p;
     uint32_t it = 0, done = 0, pieces = 0;
     while (walk.next(a, p)) {
-        const int2 mine = active<S::R>(a, p, r);
+        const Share mine = share_of<S::R>(a, p, r);
         for (int t = p.t0; t < p.t1; t++, it++) {
             const uint32_t stage = it % S::kStages, phase = it / S::kStages & 1;
-            const bool on = t >= mine.x && t < mine.y;
+            const bool on = t >= mine.x && t < mine.y && !((t - mine.x) & (mine.step - 1));
             if (!warp_wait(&sh.kfull[stage], phase)) return;
             if (t == mine.x && on && !warp_wait(&sh.qfull[r], pieces++ & 1)) return;
             fence_after();
@@ -542,7 +559,7 @@ __device__ __forceinline__ void product_role(const KvAttend &a, Shared &sh, uint
                         const uint32_t v = v0 + stage * (S::kTile >> 4);
 #pragma unroll
                         for (int i = 4 * half; i < 4 * half + 4; i++) mma_ts(ot, st + 8 * i, v + i * (2048 >> 4), kOut, i + (t - mine.x));
-                        if (half && t == mine.y - 1) commit(&sh.ofull[r]);
+                        if (half && t + mine.step >= mine.y) commit(&sh.ofull[r]);
                     }
                     if (half) commit(&sh.vempty[stage]);
                 }
@@ -642,11 +659,11 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
     const bool lead = (threadIdx.x & 31) == 0;
     Walk<S::R> walk(sh);
     Piece p;
-    uint32_t it0 = 0, sn = 0, on = 0;
+    uint32_t it0 = 0, sn = 0, on = 0, joins = 0;
     while (walk.next(a, p)) {
-        const int2 mine = active<S::R>(a, p, r);
-        const int first = p.qt * S::R + 128 * r, rho = first + row;
-        const int end = min(first + 128, p.s.rows * a.share);
+        const Share mine = share_of<S::R>(a, p, r);
+        const int first = mine.first, end = mine.end, rho = first + row;
+        const bool idle = first + row0 >= end;  // no rows for this warp
         float m = kNoMax, l = 0.0f;
         if (mine.x < mine.y) {
             const int2 seen = seen_by(a, p.s, min(rho, end - 1));
@@ -660,15 +677,22 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
                 Walk<S::R> ahead = walk;
                 Piece q;
                 if (ahead.next(a, q)) {
-                    const int64_t at = row_at(a, q.s, q.head, min(q.qt * S::R + 128 * r + row, q.s.rows * a.share - 1), a.q_token, a.q_head);
+                    const int64_t at = row_at(a, q.s, q.head, min(share_of<S::R>(a, q, r).first + row, q.s.rows * a.share - 1), a.q_token, a.q_head);
 #pragma unroll
                     for (int i = 0; i < D; i += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"((const T *)a.q + at + i));
                 }
             }
 
-            for (int t = mine.x; t < mine.y; t++) {
+            for (int t = mine.x; t < mine.y; t += mine.step) {
                 if (!warp_wait(&sh.sfull[r], sn++ & 1)) return;
                 fence_after();
+                if (idle) {
+                    if (lead) {
+                        mbar_arrive(&sh.pfull[r][0]);
+                        mbar_arrive(&sh.pfull[r][1]);
+                    }
+                    continue;
+                }
                 const uint32_t flag = (it0 + t - p.t0) % kFlags;
                 const uint4 nans = sh.nans[flag], holes = sh.holes[flag];
                 if (all_lo > t * kN || all_hi < (t + 1) * kN || (nans.x | nans.y | nans.z | nans.w | holes.x | holes.y | holes.z | holes.w)) {
@@ -745,13 +769,40 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
         }
         it0 += p.t1 - p.t0;
 
+        // A shared job: the first pair takes in what the second found.
+        float f0 = 1.0f, f1 = 0.0f;
+        bool two = false;
+        if (mine.shared) {
+            if (r == 1) {
+                sh.other_m[row] = m;
+                sh.other_l[row] = l;
+                fence_before();
+                __syncwarp();
+                if (lead) mbar_arrive(&sh.other);
+                if (!warp_wait(&sh.joined, joins++ & 1)) return;
+                continue;
+            }
+            if (!warp_wait(&sh.other, joins++ & 1)) return;
+            fence_after();
+            const Share theirs = share_of<S::R>(a, p, 1);
+            two = theirs.x < theirs.y;
+            if (two) {
+                const float m1 = sh.other_m[row], top = fmaxf(m, m1);
+                f0 = ex2(m - top);
+                f1 = ex2(m1 - top);
+                l = l * f0 + sh.other_l[row] * f1;
+                m = top;
+            }
+        }
+
         // The rows' outputs, by way of the queries' place, or the piece's
         // partial result.
         const bool whole = p.begins && p.rest == 0;
         float *part = pp.parts + (2 * blockIdx.x + (p.begins ? 1 : 0)) * kv_part_floats<D, S::R>();
+        const int part_row = first - p.qt * S::R + row;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
-        for (int i = 0; i < D; i += 16) {
+        for (int i = 0; i < D && !idle; i += 16) {
             float o[16];
             if (mine.x < mine.y) {
                 tmem_ld16(ot + i, o);
@@ -759,6 +810,13 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
             } else {
 #pragma unroll
                 for (int k = 0; k < 16; k++) o[k] = 0.0f;
+            }
+            if (two) {
+                float o1[16];
+                tmem_ld16(ot + D + i, o1);
+                wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; k++) o[k] = o[k] * f0 + o1[k] * f1;
             }
 #pragma unroll
             for (int k = 0; k < 16; k += 8) {
@@ -771,7 +829,7 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
                                  "r"(pack_out<T>(o[k + 1] * inv, o[k + 3] * inv)), "r"(pack_out<T>(o[k + 5] * inv, o[k + 7] * inv))
                                  : "memory");
                 } else {
-                    float4 *to = reinterpret_cast<float4 *>(part + (128 * r + row) * D + i + k);
+                    float4 *to = reinterpret_cast<float4 *>(part + part_row * D + i + k);
                     to[0] = make_float4(o[k], o[k + 2], o[k + 4], o[k + 6]);
                     to[1] = make_float4(o[k + 1], o[k + 3], o[k + 5], o[k + 7]);
                 }
@@ -790,15 +848,19 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
             }
             __syncwarp();
             if (a.lse && rho < end) a.lse[row_at(a, p.s, p.head, rho, a.q_heads, 1)] = lse_of(m, l);
-        } else {
-            part[S::R * D + 128 * r + row] = m;
-            part[S::R * D + S::R + 128 * r + row] = l;
+        } else if (!idle) {
+            part[S::R * D + part_row] = m;
+            part[S::R * D + S::R + part_row] = l;
             if (p.begins && r == 0 && row == 0) {
                 const KvCarry c = {1, (int)((sh.end + p.rest - 1) / sh.run) - (int)blockIdx.x, p.b, p.head, p.qt, {}};
                 pp.carries[blockIdx.x] = c;
             }
         }
         fence_before();
+        if (mine.shared) {
+            __syncwarp();
+            if (lead) mbar_arrive(&sh.joined);
+        }
     }
 }
 
@@ -822,6 +884,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             mbar_init(&sh.pfull[i][1], 4);
             mbar_init(&sh.qfull[i], 4);
         }
+        mbar_init(&sh.other, 4);
+        mbar_init(&sh.joined, 4);
         fence_mbar_init();
     }
     if (warp == 12) {
