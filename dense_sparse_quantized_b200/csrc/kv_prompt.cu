@@ -79,7 +79,7 @@ struct PromptParams {
 };
 
 struct Shared {
-    uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2][2], qfull[2], ofull[2], other, joined;
+    uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2][2], qfull[2], ofull[2], turn[2], other, joined;
     uint4 nans[kFlags], holes[kFlags];  // by loading warp: NaN tokens; sub-tiles without a page
     float other_m[128], other_l[128];   // of a shared job, the second pair's maxima and sums
     uint32_t tmem;
@@ -435,29 +435,39 @@ struct Loader {
         return bad;
     }
     // Unpacks them into the operand at `tile`.  Lane: token lane / 2, groups of
-    // 32 dimensions lane % 2, + 2, ...
+    // 32 dimensions lane % 2, + 2, ...; four of them at a time.
     __device__ __forceinline__ void unpack(const Unit &u, int which, uint32_t raw, uint32_t value_words, uint32_t tile) const {
         const int tok = lane >> 1, pair = lane & 1;
+        constexpr int G = D / 64, N = G < 2 ? 2 : 4;  // groups of a lane's token; groups at a time
+        const uint32_t codes = raw + S::raw_codes(which) + tok * (D / 2) + pair * 16;
+        const uint32_t words = (which ? value_words : raw + S::kRawWords) + (pair * kKvTile + tok) * 2;
+        const uint32_t words_tile = which ? D : S::kRawTile, to = tile + (2 * warp * kKvTile + tok) * 128;
+        uint32_t swizzle[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) swizzle[k] = ((pair * 4 + k) ^ (tok & 7)) << 4;
 #pragma unroll 1
-        for (int i = 0; i < 2; i++) {
-            const int at = (2 * warp + i) * kKvTile + tok;
-            const bool use = there(u, i) && at >= u.lo && at < u.hi;
-            uint32_t from = raw + i * S::kRawTile + S::raw_codes(which) + tok * (D / 2) + pair * 16;
-            uint32_t word_at = (which ? value_words + i * D : raw + i * S::kRawTile + S::kRawWords) + (pair * kKvTile + tok) * 2;
-            uint32_t to = tile + at * 128;
-#pragma unroll 2
-            for (int g = 0; g < D / 64; g++, from += 32, word_at += 4 * kKvTile, to += kBlk) {
+        for (int c0 = 0; c0 < 2 * G; c0 += N) {
+            uint4 x[N];
+            uint32_t w[N];
+#pragma unroll
+            for (int c = 0; c < N; c++) {
+                const int i = (c0 + c) / G, g = (c0 + c) % G, at = (2 * warp + i) * kKvTile + tok;
                 uint16_t word;
-                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(word) : "r"(word_at));
-                const uint4 x = lds128(from);
-                const uint32_t w = use && !(which == 1 && (word & 0x7c00u) == 0x7c00u) ? word : 0u;
-                const Decode d(prmt(w, w, 0x1010));
-                const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(word) : "r"(words + i * words_tile + g * 4 * kKvTile));
+                x[c] = lds128(codes + i * S::kRawTile + g * 32);
+                const bool use = there(u, i) && at >= u.lo && at < u.hi && !(which == 1 && (word & 0x7c00u) == 0x7c00u);
+                w[c] = use ? word : 0u;
+            }
+#pragma unroll
+            for (int c = 0; c < N; c++) {
+                const int i = (c0 + c) / G, g = (c0 + c) % G;
+                const Decode d(prmt(w[c], w[c], 0x1010));
+                const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w}, row = to + i * kKvTile * 128 + g * kBlk;
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
                     const uint32_t y = v[k] >> 8;
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((pair * 4 + k) ^ (tok & 7)) << 4)),
-                                 "r"(d.low(v[k])), "r"(d.high(v[k])), "r"(d.low(y)), "r"(d.high(y))
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + swizzle[k]), "r"(d.low(v[k])),
+                                 "r"(d.high(v[k])), "r"(d.low(y)), "r"(d.high(y))
                                  : "memory");
                 }
             }
@@ -659,11 +669,17 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
     const bool lead = (threadIdx.x & 31) == 0;
     Walk<S::R> walk(sh);
     Piece p;
-    uint32_t it0 = 0, sn = 0, on = 0, joins = 0;
+    uint32_t it0 = 0, sn = 0, on = 0, joins = 0, turns = 0;
     while (walk.next(a, p)) {
         const Share mine = share_of<S::R>(a, p, r);
         const int first = mine.first, end = mine.end, rho = first + row;
         const bool idle = first + row0 >= end;  // no rows for this warp
+        // Units that both pairs work on: they take turns at the exponentials.
+        int2 both = make_int2(0, 0);
+        if (S::A == 2 && !mine.shared) {
+            const Share theirs = share_of<S::R>(a, p, r ^ 1);
+            both = make_int2(max(mine.x, theirs.x), min(mine.y, theirs.y));
+        }
         float m = kNoMax, l = 0.0f;
         if (mine.x < mine.y) {
             const int2 seen = seen_by(a, p.s, min(rho, end - 1));
@@ -686,8 +702,14 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
             for (int t = mine.x; t < mine.y; t += mine.step) {
                 if (!warp_wait(&sh.sfull[r], sn++ & 1)) return;
                 fence_after();
+                const bool in_turn = t >= both.x && t < both.y;
                 if (idle) {
+                    if (in_turn) {
+                        if (!warp_wait(&sh.turn[r], (turns ^ r ^ 1) & 1)) return;
+                        turns++;
+                    }
                     if (lead) {
+                        if (in_turn) mbar_arrive(&sh.turn[r ^ 1]);
                         mbar_arrive(&sh.pfull[r][0]);
                         mbar_arrive(&sh.pfull[r][1]);
                     }
@@ -743,6 +765,11 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
                         }
                     }
                 }
+                // The first pair's first turn is there from the start.
+                if (in_turn) {
+                    if (!warp_wait(&sh.turn[r], (turns ^ r ^ 1) & 1)) return;
+                    turns++;
+                }
                 float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
 #pragma unroll
                 for (int half = 0; half < 2; half++) {  // the product over the first 64 tokens starts meanwhile
@@ -761,6 +788,7 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
                     __syncwarp();
                     if (lead) mbar_arrive(&sh.pfull[r][half]);
                 }
+                if (in_turn && lead) mbar_arrive(&sh.turn[r ^ 1]);
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
             }
@@ -883,6 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             mbar_init(&sh.pfull[i][0], 4);
             mbar_init(&sh.pfull[i][1], 4);
             mbar_init(&sh.qfull[i], 4);
+            mbar_init(&sh.turn[i], 4);
         }
         mbar_init(&sh.other, 4);
         mbar_init(&sh.joined, 4);
