@@ -109,6 +109,10 @@ __device__ __forceinline__ void query_codes_order(uint4 (&x)[N], int up) {
     }
 }
 
+__device__ __forceinline__ int64_t divide(int64_t n, int d) {  // n >= 0, d > 0
+    return n >> 32 ? n / d : (int64_t)((uint32_t)n / (uint32_t)d);
+}
+
 // Tokens [x, y) that query row `rho` of a kv head (of the sequence's rows
 // times the heads of a group) sees.
 __device__ __forceinline__ int2 seen_by(const KvAttend &a, const KvSeq &s, int rho) {

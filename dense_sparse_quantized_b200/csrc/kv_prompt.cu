@@ -22,6 +22,7 @@
 //                   128-byte-swizzled tiles of a ring in shared memory.  Eight
 //                   dimensions come out as 0 4 1 5 2 6 3 7; the queries are
 //                   stored in that order, the output's columns renamed.
+//   warp 14         works out the run and its pieces, ahead of the others.
 //   warps 12, 13    issue the products of row tile 0, 1: S = Q K^T (K-major),
 //                   then O += P V with P from tensor memory and V token-major
 //                   (MN-major B).
@@ -76,16 +77,34 @@ struct PromptParams {
     KvAttend a;
     float *parts;
     KvCarry *carries;
+    int one_each;  // a job a CTA
 };
 
+// What the r-th pair of softmax and product warps does of a piece: rows
+// [first, end) of the job's kv head, units x, x + step, ... below y (none: y =
+// x).  A job of 128 rows or fewer is shared by units, else by row tiles.
+struct Share {
+    int first, end, x, y, step, shared;
+};
+
+// A piece of a CTA's run: units [t0, t1) of one job.
+struct Piece {
+    KvSeq s;
+    int b, head, qt, t0, t1, rest;  // rest: the job's cost behind t1
+    int begins, valid;
+    int lo, hi;                     // tokens that some row of the job sees
+    Share share[2];
+};
+
+constexpr int kPieces = 4;  // worked out ahead
 struct Shared {
     uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2][2], qfull[2], ofull[2], turn[2], other, joined;
+    uint64_t piece_full[kPieces], piece_empty[kPieces];
+    Piece piece[kPieces];
     uint4 nans[kFlags], holes[kFlags];  // by loading warp: NaN tokens; sub-tiles without a page
     float other_m[128], other_l[128];   // of a shared job, the second pair's maxima and sums
     uint32_t tmem;
-    int b, head, qt, first;  // where this CTA's run begins: the job, and how much of its cost lies before
-    int left;                // cost of the run
-    int64_t run, end;        // of every CTA's; where this one ends among all
+    int64_t run, end;                   // cost of every CTA's run; where this one ends among all
 };
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -194,54 +213,6 @@ __device__ __forceinline__ int tiles_of(const KvAttend &a, const KvSeq &s) {
     return (int)(((uint32_t)(s.rows * a.share) + R - 1) / R);
 }
 
-// A piece of a CTA's run: units [t0, t1) of one job.
-struct Piece {
-    KvSeq s;
-    int b, head, qt, t0, t1, rest;  // rest: the job's units behind t1
-    bool begins;
-};
-template <int R>
-struct Walk {
-    int b, head, qt, first, left;
-    __device__ __forceinline__ explicit Walk(const Shared &sh) : b(sh.b), head(sh.head), qt(sh.qt), first(sh.first), left(sh.left) {}
-    __device__ __forceinline__ bool next(const KvAttend &a, Piece &p) {
-        while (left > 0 && b < a.batch) {
-            p.s = kv_seq(a, b);
-            const int tiles = tiles_of<R>(a, p.s);
-            if (qt >= tiles) {
-                qt = 0;
-                if (tiles == 0 || ++head >= a.c.kv_heads) {
-                    head = 0;
-                    b++;
-                }
-                continue;
-            }
-            // [first, end) of the job's cost, kPieceCost of it before its units
-            const int2 u = units_of<R>(a, p.s, qt);
-            const int cost = kPieceCost + u.y - u.x, end = min(cost, first + left);
-            p.b = b;
-            p.head = head;
-            p.qt = qt;
-            p.t0 = u.x + max(0, first - kPieceCost);
-            p.t1 = u.x + max(0, end - kPieceCost);
-            p.rest = cost - end;
-            p.begins = first <= kPieceCost;
-            left -= end - first;
-            first = 0;
-            qt++;
-            if (p.t0 < p.t1) return true;
-        }
-        return false;
-    }
-};
-
-// What the r-th pair of softmax and product warps does of a piece: rows
-// [first, end) of the job's kv head, units x, x + step, ... below y (none: y =
-// x).  A job of 128 rows or fewer is shared by units, else by row tiles.
-struct Share {
-    int first, end, x, y, step;
-    bool shared;
-};
 template <int R>
 __device__ __forceinline__ Share share_of(const KvAttend &a, const Piece &p, int r) {
     Share w;
@@ -259,18 +230,26 @@ __device__ __forceinline__ Share share_of(const KvAttend &a, const Piece &p, int
     return w;
 }
 
-// Finds this CTA's run (one warp).
+// ----------------------------------------------------------------- warp 14
+// Where a CTA's run begins -- a job, and how much of its cost lies before --
+// and its cost.
+struct Start {
+    int b, head, qt, first, left;
+};
 template <int R>
-__device__ __forceinline__ void find_run(const KvAttend &a, Shared &sh) {
+__device__ __forceinline__ Start find_run(const KvAttend &a, bool one_each, Shared &sh) {
     const int lane = threadIdx.x & 31;
+    auto cost = [&](const KvSeq &s, int qt) {
+        const int2 u = units_of<R>(a, s, qt);
+        return one_each ? 1 : kPieceCost + u.y - u.x;
+    };
     auto head_cost = [&](int b) -> int64_t {  // of one kv head of sequence b
         const KvSeq s = kv_seq(a, b);
         const int tiles = tiles_of<R>(a, s);
+        if (one_each) return tiles;
         int64_t n = 0;
-        for (int qt = 0; qt < tiles; qt++) {
-            const int2 u = units_of<R>(a, s, qt);
-            n += kPieceCost + u.y - u.x;
-        }
+#pragma unroll 1
+        for (int qt = 0; qt < tiles; qt++) n += cost(s, qt);
         return n;
     };
     auto scan = [&](int64_t w) {
@@ -281,68 +260,148 @@ __device__ __forceinline__ void find_run(const KvAttend &a, Shared &sh) {
         }
         return w;
     };
-    int64_t total = 0;
-    if (a.batch < 8) {  // few sequences: the lanes take row tiles, else sequences
-        for (int b = 0; b < a.batch; b++) {
-            const KvSeq s = kv_seq(a, b);
-            const int tiles = tiles_of<R>(a, s);
-            for (int qt = lane; qt < tiles; qt += 32) {
-                const int2 u = units_of<R>(a, s, qt);
-                total += (int64_t)(kPieceCost + u.y - u.x) * a.c.kv_heads;
+    int64_t run = 1, u0 = blockIdx.x, u1 = u0 + 1;
+    if (!one_each) {
+        int64_t total = 0;
+        if (a.batch < 8) {  // few sequences: the lanes take row tiles, else sequences
+#pragma unroll 1
+            for (int b = 0; b < a.batch; b++) {
+                const KvSeq s = kv_seq(a, b);
+                const int tiles = tiles_of<R>(a, s);
+#pragma unroll 1
+                for (int qt = lane; qt < tiles; qt += 32) total += (int64_t)cost(s, qt) * a.c.kv_heads;
             }
-        }
-    } else
-        for (int b = lane; b < a.batch; b += 32) total += head_cost(b) * a.c.kv_heads;
+        } else
+#pragma unroll 1
+            for (int b = lane; b < a.batch; b += 32) total += head_cost(b) * a.c.kv_heads;
 #pragma unroll
-    for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(kFull, total, m);
-    const int64_t run = (total + gridDim.x - 1) / gridDim.x;
-    const int64_t u0 = min(total, run * blockIdx.x), u1 = min(total, u0 + run);
+        for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(kFull, total, m);
+        run = divide(total + gridDim.x - 1, gridDim.x);
+        u0 = min(total, run * blockIdx.x);
+        u1 = min(total, u0 + run);
+    }
     int64_t before = 0;
-    int b = a.batch, head = 0, qt = 0, first = 0;
+    Start at = {a.batch, 0, 0, 0, (int)(u1 - u0)};
+#pragma unroll 1
     for (int b0 = 0; b0 < a.batch && u0 < u1; b0 += 32) {
         const int64_t w = b0 + lane < a.batch ? head_cost(b0 + lane) : 0, sum = scan(w * a.c.kv_heads);
         const uint32_t past = __ballot_sync(kFull, before + sum > u0);
         if (past) {
             const int l = __ffs(past) - 1;
-            b = b0 + l;
+            at.b = b0 + l;
             before += __shfl_sync(kFull, sum - w * a.c.kv_heads, l);
             const int64_t per_head = max((int64_t)1, __shfl_sync(kFull, w, l));
-            head = (int)((u0 - before) / per_head);
-            before += head * per_head;
+            at.head = (int)divide(u0 - before, (int)min(per_head, (int64_t)0x7fffffff));
+            before += at.head * per_head;
             break;
         }
         before += __shfl_sync(kFull, sum, 31);
     }
-    if (b < a.batch) {
-        const KvSeq s = kv_seq(a, b);
+    if (at.b < a.batch) {
+        const KvSeq s = kv_seq(a, at.b);
         const int tiles = tiles_of<R>(a, s);
+#pragma unroll 1
         for (int q0 = 0; q0 < tiles; q0 += 32) {
-            int w = 0;
-            if (q0 + lane < tiles) {
-                const int2 u = units_of<R>(a, s, q0 + lane);
-                w = kPieceCost + u.y - u.x;
-            }
+            const int w = q0 + lane < tiles ? cost(s, q0 + lane) : 0;
             const int64_t sum = scan(w);
             const uint32_t past = __ballot_sync(kFull, before + sum > u0);
             if (past) {
                 const int l = __ffs(past) - 1;
-                qt = q0 + l;
-                first = (int)(u0 - before - __shfl_sync(kFull, sum - w, l));
+                at.qt = q0 + l;
+                at.first = (int)(u0 - before - __shfl_sync(kFull, sum - w, l));
                 break;
             }
             before += __shfl_sync(kFull, sum, 31);
         }
+        if (one_each) {
+            const int2 u = units_of<R>(a, s, at.qt);
+            at.left = kPieceCost + u.y - u.x;
+        }
     }
     if (lane == 0) {
-        sh.b = b;
-        sh.head = head;
-        sh.qt = qt;
-        sh.first = first;
-        sh.left = (int)(u1 - u0);
         sh.run = run;
         sh.end = u1;
     }
+    return at;
 }
+
+// Finds the run and works its pieces out, ahead of the warps that use them.
+template <int D, typename T>
+__device__ __forceinline__ void piece_role(const KvAttend &a, bool one_each, Shared &sh) {
+    using S = Shape<D>;
+    constexpr int R = S::R;
+    const int lane = threadIdx.x & 31;
+    Start at = find_run<R>(a, one_each, sh);
+    for (uint32_t n = 0;; n++) {
+        Piece p = {};
+#pragma unroll 1
+        while (at.left > 0 && at.b < a.batch) {
+            p.s = kv_seq(a, at.b);
+            const int tiles = tiles_of<R>(a, p.s);
+            if (at.qt >= tiles) {
+                at.qt = 0;
+                if (tiles == 0 || ++at.head >= a.c.kv_heads) {
+                    at.head = 0;
+                    at.b++;
+                }
+                continue;
+            }
+            // [first, end) of the job's cost, kPieceCost of it before its units
+            const int2 u = units_of<R>(a, p.s, at.qt);
+            const int cost = kPieceCost + u.y - u.x, end = min(cost, at.first + at.left);
+            p.b = at.b;
+            p.head = at.head;
+            p.qt = at.qt;
+            p.t0 = u.x + max(0, at.first - kPieceCost);
+            p.t1 = u.x + max(0, end - kPieceCost);
+            p.rest = cost - end;
+            p.begins = at.first <= kPieceCost;
+            at.left -= end - at.first;
+            at.first = 0;
+            at.qt++;
+            if (p.t0 < p.t1) {
+                p.valid = 1;
+                break;
+            }
+        }
+        const int last = min((p.qt + 1) * R, p.s.rows * a.share) - 1;
+        if (p.valid) {
+            p.lo = seen_by(a, p.s, p.qt * R).x;
+            p.hi = seen_by(a, p.s, last).y;
+            p.share[0] = share_of<R>(a, p, 0);
+            p.share[1] = share_of<R>(a, p, 1);
+        }
+        if (!warp_wait(&sh.piece_empty[n % kPieces], (n / kPieces & 1) ^ 1)) return;
+        if (lane == 0) {
+            sh.piece[n % kPieces] = p;
+            mbar_arrive(&sh.piece_full[n % kPieces]);
+        }
+        __syncwarp();
+        if (!p.valid) return;
+        for (int rho = p.qt * R + lane; rho <= last; rho += 32) {  // its queries come to L2 meanwhile
+            const T *q = (const T *)a.q + row_at(a, p.s, p.head, rho, a.q_token, a.q_head);
+#pragma unroll
+            for (int i = 0; i < D; i += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + i));
+        }
+    }
+}
+
+// The pieces, for a warp of the other roles.
+struct Pieces {
+    uint32_t n = 0;
+    Share mine, theirs;  // the r-th pair's, and the other's
+    __device__ __forceinline__ bool next(Shared &sh, Piece &p, int r) {
+        const uint32_t at = n % kPieces;
+        if (!warp_wait(&sh.piece_full[at], n / kPieces & 1)) return false;
+        p = sh.piece[at];
+        mine = sh.piece[at].share[r];
+        theirs = sh.piece[at].share[r ^ 1];
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.piece_empty[at]);
+        n++;
+        return p.valid;
+    }
+};
 
 // ------------------------------------------------------------ warps 8-11
 // Each warp brings tiles 2 w and 2 w + 1 of a unit's eight: by cp.async as they
@@ -355,7 +414,8 @@ template <int D>
 struct Loader {
     using S = Shape<D>;
     const KvAttend &a;
-    Walk<S::R> walk;
+    Shared &sh;
+    Pieces pieces;
     Piece p;
     int t;
     bool more;
@@ -367,9 +427,9 @@ struct Loader {
         int lo, hi, page[2], in_page[2], head;
         bool there;
     };
-    __device__ __forceinline__ Loader(const KvAttend &a_, const Shared &sh)
-        : a(a_), walk(sh), lane(threadIdx.x & 31), warp((threadIdx.x >> 5) & 3) {
-        more = walk.next(a, p);
+    __device__ __forceinline__ Loader(const KvAttend &a_, Shared &sh_)
+        : a(a_), sh(sh_), lane(threadIdx.x & 31), warp((threadIdx.x >> 5) & 3) {
+        more = pieces.next(sh, p, 0);
         t = p.t0;
     }
     __device__ __forceinline__ Unit next() {
@@ -377,9 +437,8 @@ struct Loader {
         u.there = more;
         u.page[0] = u.page[1] = -1;
         if (!more) return u;
-        const int last = min((p.qt + 1) * S::R, p.s.rows * a.share) - 1;
-        u.lo = seen_by(a, p.s, p.qt * S::R).x - t * kN;
-        u.hi = seen_by(a, p.s, last).y - t * kN;
+        u.lo = p.lo - t * kN;
+        u.hi = p.hi - t * kN;
         u.head = p.head;
         const int32_t *row = a.page_table + (int64_t)p.b * a.table_pages;
 #pragma unroll
@@ -389,7 +448,7 @@ struct Loader {
             if (col < a.table_pages && u.hi > (2 * warp + i) * kKvTile) u.page[i] = row[col];
         }
         if (++t == p.t1) {
-            more = walk.next(a, p);
+            more = pieces.next(sh, p, 0);
             t = p.t0;
         }
         return u;
@@ -529,22 +588,22 @@ __device__ __forceinline__ void load_role(const KvAttend &a, Shared &sh, uint32_
 // One for each row tile, so that neither waits for the other's softmax.  All
 // lanes walk, one issues.
 template <int D>
-__device__ __forceinline__ void product_role(const KvAttend &a, Shared &sh, uint32_t qbuf, uint32_t kbuf, uint32_t vbuf, int r) {
+__device__ __forceinline__ void product_role(Shared &sh, uint32_t qbuf, uint32_t kbuf, uint32_t vbuf, int r) {
     using S = Shape<D>;
     constexpr uint32_t kScores = instruction(kN, false), kOut = instruction(D, true);
     const uint32_t st = sh.tmem + 128 * r, ot = sh.tmem + S::kO + D * r;
     const uint32_t q0 = operand(qbuf + r * S::kTile, 16), k0 = operand(kbuf, 16), v0 = operand(vbuf, kBlk);
     const bool lead = elect_one();  // one thread throughout: a commit speaks for its own thread's products
-    Walk<S::R> walk(sh);
+    Pieces pieces;
     Piece p;
-    uint32_t it = 0, done = 0, pieces = 0;
-    while (walk.next(a, p)) {
-        const Share mine = share_of<S::R>(a, p, r);
+    uint32_t it = 0, done = 0, queries = 0;
+    while (pieces.next(sh, p, r)) {
+        const Share &mine = pieces.mine;
         for (int t = p.t0; t < p.t1; t++, it++) {
             const uint32_t stage = it % S::kStages, phase = it / S::kStages & 1;
             const bool on = t >= mine.x && t < mine.y && !((t - mine.x) & (mine.step - 1));
             if (!warp_wait(&sh.kfull[stage], phase)) return;
-            if (t == mine.x && on && !warp_wait(&sh.qfull[r], pieces++ & 1)) return;
+            if (t == mine.x && on && !warp_wait(&sh.qfull[r], queries++ & 1)) return;
             fence_after();
             if (lead) {
                 if (on) {
@@ -667,17 +726,17 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
     const uint32_t lanes = (uint32_t)row0 << 16;  // this warp's quarter of tensor memory
     const uint32_t st = sh.tmem + 128 * r + lanes, ot = sh.tmem + S::kO + D * r + lanes, tile = qbuf + r * S::kTile;
     const bool lead = (threadIdx.x & 31) == 0;
-    Walk<S::R> walk(sh);
+    Pieces pieces;
     Piece p;
     uint32_t it0 = 0, sn = 0, on = 0, joins = 0, turns = 0;
-    while (walk.next(a, p)) {
-        const Share mine = share_of<S::R>(a, p, r);
+    while (pieces.next(sh, p, r)) {
+        const Share &mine = pieces.mine;
         const int first = mine.first, end = mine.end, rho = first + row;
         const bool idle = first + row0 >= end;  // no rows for this warp
         // Units that both pairs work on: they take turns at the exponentials.
         int2 both = make_int2(0, 0);
         if (S::A == 2 && !mine.shared) {
-            const Share theirs = share_of<S::R>(a, p, r ^ 1);
+            const Share &theirs = pieces.theirs;
             both = make_int2(max(mine.x, theirs.x), min(mine.y, theirs.y));
         }
         float m = kNoMax, l = 0.0f;
@@ -689,16 +748,6 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
             fence_before();
             __syncwarp();
             if (lead) mbar_arrive(&sh.qfull[r]);
-            {  // the next piece's queries come to L2 meanwhile
-                Walk<S::R> ahead = walk;
-                Piece q;
-                if (ahead.next(a, q)) {
-                    const int64_t at = row_at(a, q.s, q.head, min(share_of<S::R>(a, q, r).first + row, q.s.rows * a.share - 1), a.q_token, a.q_head);
-#pragma unroll
-                    for (int i = 0; i < D; i += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"((const T *)a.q + at + i));
-                }
-            }
-
             for (int t = mine.x; t < mine.y; t += mine.step) {
                 if (!warp_wait(&sh.sfull[r], sn++ & 1)) return;
                 fence_after();
@@ -812,7 +861,7 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
             }
             if (!warp_wait(&sh.other, joins++ & 1)) return;
             fence_after();
-            const Share theirs = share_of<S::R>(a, p, 1);
+            const Share &theirs = pieces.theirs;
             two = theirs.x < theirs.y;
             if (two) {
                 const float m1 = sh.other_m[row], top = fmaxf(m, m1);
@@ -880,7 +929,7 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
             part[S::R * D + part_row] = m;
             part[S::R * D + S::R + part_row] = l;
             if (p.begins && r == 0 && row == 0) {
-                const KvCarry c = {1, (int)((sh.end + p.rest - 1) / sh.run) - (int)blockIdx.x, p.b, p.head, p.qt, {}};
+                const KvCarry c = {1, (int)divide(sh.end + p.rest - 1, (int)sh.run) - (int)blockIdx.x, p.b, p.head, p.qt, {}};
                 pp.carries[blockIdx.x] = c;
             }
         }
@@ -913,6 +962,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             mbar_init(&sh.qfull[i], 4);
             mbar_init(&sh.turn[i], 4);
         }
+        for (int i = 0; i < kPieces; i++) {
+            mbar_init(&sh.piece_full[i], 1);
+            mbar_init(&sh.piece_empty[i], 4 * S::A + 4 + S::A);  // all warps but this one's
+        }
         mbar_init(&sh.other, 4);
         mbar_init(&sh.joined, 4);
         fence_mbar_init();
@@ -922,8 +975,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     kv_after_previous();
-    if (threadIdx.x == 0) pp.carries[blockIdx.x].valid = 0;
-    if (warp == 8) find_run<S::R>(pp.a, sh);
+    if (threadIdx.x == 0 && !pp.one_each) pp.carries[blockIdx.x].valid = 0;
     fence_before();
     __syncthreads();
     fence_after();
@@ -937,7 +989,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         load_role<D>(pp.a, sh, kbuf, vbuf, vbuf + S::kStages * S::kTile);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (warp < 12 + S::A) product_role<D>(pp.a, sh, qbuf, kbuf, vbuf, warp - 12);
+        if (warp == 14) piece_role<D, T>(pp.a, pp.one_each, sh);
+        else if (warp < 12 + S::A) product_role<D>(sh, qbuf, kbuf, vbuf, warp - 12);
     }
     fence_before();
     __syncthreads();
@@ -950,13 +1003,20 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 template <int D, typename T>
 int launch_prompt(const KvAttend &a, void *workspace, int sms, cudaStream_t st) {
     using S = Shape<D>;
-    const PromptParams p = {a, (float *)workspace, kv_carries<D, S::R>(workspace)};
+    // A job a CTA where every job has an SM and six units at most: no joining,
+    // one launch.
+    const int64_t jobs = a.c.kv_heads * (a.q_start ? a.batch + (int64_t)a.q_tokens * a.share / S::R
+                                                    : a.batch * (((int64_t)a.rows_each * a.share + S::R - 1) / S::R));
+    int64_t tokens = a.most_tokens;
+    if (a.window) tokens = std::min<int64_t>(tokens, (int64_t)a.window + S::R / a.share + 1);
+    const bool one_each = jobs <= sms && tokens / kN + 2 <= 6;
+    const PromptParams p = {a, (float *)workspace, kv_carries<D, S::R>(workspace), one_each};
     auto kernel = prompt_kernel<D, T>;
     static KvOnce once;
     if (!once.set_smem((const void *)kernel, S::kSmem)) return DSQ_ERR_CUDA;
-    const int grid = std::min(sms, kMaxCtas);
+    const int grid = one_each ? (int)jobs : std::min(sms, kMaxCtas);
     const int rc = kv_launch(kernel, grid, kThreads, S::kSmem, st, p);
-    return rc != DSQ_OK ? rc : launch_join<D, S::R, T>(a, p.parts, p.carries, grid, st);
+    return rc != DSQ_OK || one_each ? rc : launch_join<D, S::R, T>(a, p.parts, p.carries, grid, st);
 }
 
 template <typename T>
