@@ -820,8 +820,14 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
                     turns++;
                 }
                 float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+                auto hand_over = [&](int half) {  // the product over 64 tokens starts while the others are worked on
+                    wait_st();
+                    fence_before();
+                    __syncwarp();
+                    if (lead) mbar_arrive(&sh.pfull[r][half]);
+                };
 #pragma unroll
-                for (int half = 0; half < 2; half++) {  // the product over the first 64 tokens starts meanwhile
+                for (int half = 0; half < 2; half++) {
                     uint32_t ph[32];
 #pragma unroll
                     for (int k = 0; k < 32; k++) {
@@ -830,14 +836,12 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
                         const float2 e = make_float2(ex2(y.x), ex2(y.y));
                         sum[k & 1] = add2(sum[k & 1], e);
                         ph[k] = pack_h2(e.x, e.y);
+                        if (half == 1 && k == 7) hand_over(0);  // its store has had time to end
                     }
+                    if (half == 1 && in_turn && lead) mbar_arrive(&sh.turn[r ^ 1]);
                     tmem_st32(st + 32 * half, ph);
-                    wait_st();
-                    fence_before();
-                    __syncwarp();
-                    if (lead) mbar_arrive(&sh.pfull[r][half]);
                 }
-                if (in_turn && lead) mbar_arrive(&sh.turn[r ^ 1]);
+                hand_over(1);
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
             }
