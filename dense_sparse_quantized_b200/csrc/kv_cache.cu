@@ -68,52 +68,66 @@ __device__ __forceinline__ float scale_of(float lo, float hi) {
     return fmaxf(n == 129.0f ? 130.0f : n, 1.0f) * u;
 }
 
-// Quantises this thread's eight values of a group held by four neighbouring
-// lanes; returns the eight codes, and the group's word in `word`.
+// (lowest, -highest) of a group's values, held eight each by four neighbouring
+// lanes; a NaN stays.
 template <typename T>
-__device__ __forceinline__ uint32_t encode8(uint4 raw, uint32_t &word) {
+__device__ __forceinline__ uint32_t ends_of(uint4 raw) {
     using P = Pairs<T>;
-    // (lowest, -highest) of the group; a NaN stays
     const uint32_t lo2 = P::min_nan(P::min_nan(raw.x, raw.y), P::min_nan(raw.z, raw.w));
     const uint32_t hi2 = P::max_nan(P::max_nan(raw.x, raw.y), P::max_nan(raw.z, raw.w)) ^ 0x80008000u;
     uint32_t ends = P::min_nan(prmt(lo2, hi2, 0x5410), prmt(lo2, hi2, 0x7632));
     ends = P::min_nan(ends, __shfl_xor_sync(kFull, ends, 1));
-    ends = P::min_nan(ends, __shfl_xor_sync(kFull, ends, 2));
-    const float2 f = P::floats(ends);
-    const bool nan = f.x != f.x || f.y != f.y;
-    const float lo = fmaxf(fminf(f.x, 0.0f), -kKvClamp), hi = fminf(fmaxf(-f.y, 0.0f), kKvClamp);
-    const float s = scale_of(lo, hi), inv = __frcp_rn(s);
+    return P::min_nan(ends, __shfl_xor_sync(kFull, ends, 2));
+}
 
-    // Quotients: one Newton step on x times the rounded reciprocal gives the
-    // correctly rounded x / s.  x (11 bits) over s (7 bits) against a border
-    // k + 1/2 (5 bits): two numbers of 16 bits at most that are equal or 2^-16
-    // apart, so the rounded quotient lies on the same side as the exact one.
-    // Adding 3 * 2^22 rounds to an integer, ties to even.  No code is below
-    // lo's, which is 0.
-    constexpr float kRound = 12582912.0f;
-    auto code = [&](float x) {
-        const float y = x * inv;
-        return __float_as_int(fmaf(fmaf(-y, s, x), inv, y) + kRound) - __float_as_int(kRound);
-    };
-    const int z = -code(lo);
-    const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
-    uint32_t codes = 0;
-    if (__any_sync(kFull, f.x < -kKvClamp || f.y < -kKvClamp)) {  // infinities have no quotient
+// x / s rounded to an integer, ties to even, as a float above 3 * 2^22.  One
+// Newton step on x times the rounded reciprocal gives the correctly rounded
+// quotient.  x (11 bits) over s (7 bits) against a border k + 1/2 (5 bits):
+// two numbers of 16 bits at most that are equal or 2^-16 apart, so it lies on
+// the same side as the exact one.  `most`: an integer not to be passed.
+constexpr float kRound = 12582912.0f;
+__device__ __forceinline__ float rounded(float x, float s, float inv, float most) {
+    const float y = x * inv;
+    return fminf(fmaf(fmaf(-y, s, x), inv, y), most) + kRound;
+}
+
+struct Group {
+    float s, inv;
+    uint32_t word;
+};
+template <typename T>
+__device__ __forceinline__ Group group_of(uint32_t ends) {
+    const float2 f = Pairs<T>::floats(ends);
+    const float lo = fmaxf(fminf(f.x, 0.0f), -kKvClamp), hi = fminf(fmaxf(-f.y, 0.0f), kKvClamp);
+    Group g;
+    g.s = scale_of(lo, hi);
+    g.inv = __frcp_rn(g.s);
+    const uint32_t zero = (uint32_t)(__float_as_int(rounded(-lo, g.s, g.inv, 15.0f)) - __float_as_int(kRound));
+    g.word = f.x != f.x || f.y != f.y ? 0x7e00u : (uint32_t)__half_as_ushort(__float2half_rn(g.s)) | zero;
+    return g;
+}
+
+// The codes of this thread's eight values.  lo's is 0 and none is below;
+// rounding up can bring one to 16, which becomes 15.  The floats' bits,
+// 16^i times the i-th, are added up as they are: what kRound and zero add to
+// them is the same for all.
+template <typename T>
+__device__ __forceinline__ uint32_t codes_of(uint4 raw, const Group &g, bool clamp) {
+    if (g.word == 0x7e00u) return 0;
+    const uint32_t zero = g.word & 15u, v[4] = {raw.x, raw.y, raw.z, raw.w};
+    const float most = 15.0f - (float)zero;
+    uint32_t codes = (zero - (uint32_t)__float_as_int(kRound)) * 0x11111111u;
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const float2 x = P::floats(v[i / 2]);
-            codes |= (uint32_t)min(code(fminf(fmaxf(i % 2 ? x.y : x.x, -kKvClamp), kKvClamp)) + z, 15) << (4 * i);
+    for (int i = 0; i < 8; i += 2) {
+        float2 x = Pairs<T>::floats(v[i / 2]);
+        if (clamp) {  // infinities have no quotient
+            x.x = fminf(fmaxf(x.x, -kKvClamp), kKvClamp);
+            x.y = fminf(fmaxf(x.y, -kKvClamp), kKvClamp);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            const float2 x = P::floats(v[i / 2]);
-            codes |= (uint32_t)min(code(x.x) + z, 15) << (4 * i);
-            codes |= (uint32_t)min(code(x.y) + z, 15) << (4 * i + 4);
-        }
+        codes += (uint32_t)__float_as_int(rounded(x.x, g.s, g.inv, most)) << (4 * i);
+        codes += (uint32_t)__float_as_int(rounded(x.y, g.s, g.inv, most)) << (4 * i + 4);
     }
-    word = nan ? 0x7e00u : (uint32_t)__half_as_ushort(__float2half_rn(s)) | (uint32_t)z;
-    return nan ? 0u : codes;
+    return codes;
 }
 
 // Where the slot's token lies: its tile, and its row in it.
@@ -147,8 +161,29 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         v = *reinterpret_cast<const uint4 *>((const T *)r.v + t * r.v_token + head * r.v_head + dim);
         slot = slots[t];
     }
-    uint32_t kw, vw;
-    const uint32_t kc = encode8<T>(k, kw), vc = encode8<T>(v, vw);
+    // Even lanes work out the key group's scale and zero, odd ones the value
+    // group's, for both.
+    const uint32_t ke = ends_of<T>(k), ve = ends_of<T>(v);
+    const bool odd = threadIdx.x & 1;
+    const Group mine = group_of<T>(odd ? ve : ke);
+    Group theirs;
+    theirs.s = __shfl_xor_sync(kFull, mine.s, 1);
+    theirs.inv = __shfl_xor_sync(kFull, mine.inv, 1);
+    theirs.word = __shfl_xor_sync(kFull, mine.word, 1);
+    const Group kg = odd ? theirs : mine, vg = odd ? mine : theirs;
+    const uint32_t kw = kg.word, vw = vg.word;
+    auto outside = [](uint32_t ends) {
+        const float2 f = Pairs<T>::floats(ends);
+        return f.x < -kKvClamp || f.y < -kKvClamp;
+    };
+    uint32_t kc, vc;
+    if (__any_sync(kFull, outside(ke) || outside(ve))) {
+        kc = codes_of<T>(k, kg, true);
+        vc = codes_of<T>(v, vg, true);
+    } else {
+        kc = codes_of<T>(k, kg, false);
+        vc = codes_of<T>(v, vg, false);
+    }
     if (slot < 0 || slot >= c.slots) return;
     const Place at = place_of<D>(c, (int)slot, head);
     uint8_t *codes = cache + at.tile + at.row * (D / 2) + dim / 2;
