@@ -372,7 +372,8 @@ class KVCache:
     stored cache, or a host program's own pool); allocated and zeroed
     otherwise.  A token's slot is page * page_tokens + offset.  Calls are
     asynchronous on ``stream`` (default: the current torch stream of the
-    cache's device) and work on the cache's device, whichever is current.
+    cache's device) and work on the cache's device, whichever is current; new
+    tensors that they return are made on that stream.
 
         kv = KVCache(kv_heads=8, head_dim=128, pages=1024)
         kv.append(k, v, slots)                    # k, v: [tokens, kv_heads, head_dim]
@@ -416,6 +417,17 @@ class KVCache:
             return self._torch._C._cuda_getCurrentRawStream(self.desc.device)
         return _stream_ptr(stream)
 
+    def _new(self, stream, fill, shape, dtype):
+        """A tensor made on ``stream``, so that what fills it and what may get
+        its memory next is in order with the call."""
+        if stream is None:
+            return fill(shape, dtype=dtype, device=self.device)
+        cuda = self._torch.cuda
+        if not isinstance(stream, cuda.Stream):
+            stream = cuda.ExternalStream(int(stream), device=self.device)
+        with cuda.stream(stream):
+            return fill(shape, dtype=dtype, device=self.device)
+
     def _rows(self, t, name, tokens, heads):
         if t.device != self.device or t.shape != (tokens, heads, self.head_dim):
             raise ValueError(f"{name} must be [{tokens}, {heads}, {self.head_dim}] on {self.device}")
@@ -452,8 +464,8 @@ class KVCache:
             like = k if k is not None else v
             dtype = dtype or (like.dtype if like is not None else self._torch.float16)
             shape = (slots.shape[0], self.kv_heads, self.head_dim)
-            k = self._torch.zeros(shape, dtype=dtype, device=self.device) if k is None else k
-            v = self._torch.zeros(shape, dtype=dtype, device=self.device) if v is None else v
+            k = self._new(stream, self._torch.zeros, shape, dtype) if k is None else k
+            v = self._new(stream, self._torch.zeros, shape, dtype) if v is None else v
         if dtype is not None and k.dtype != dtype:
             raise ValueError("k and v must have the dtype asked for")
         n, rows = self._kv_rows(k, v, slots)
@@ -462,7 +474,7 @@ class KVCache:
             _check(rc, "dsq_kv_read")
         return k, v
 
-    def attend_workspace(self, q_tokens: int, q_heads: int, batch: int):
+    def attend_workspace(self, q_tokens: int, q_heads: int, batch: int, stream=None):
         """Scratch for attend() calls of these sizes that follow one another;
         calls that may overlap need one each."""
         size = ctypes.c_size_t(0)
@@ -471,7 +483,7 @@ class KVCache:
         rc = library().dsq_kv_attend(self._d, None, ctypes.byref(a), None, ctypes.byref(size), None)
         if rc != DSQ_ERR_BUFFER_TOO_SMALL:
             _check(rc, "dsq_kv_attend")
-        return self._torch.empty(max(size.value, 1), dtype=self._torch.uint8, device=self.device)
+        return self._new(stream, self._torch.empty, max(size.value, 1), self._torch.uint8)
 
     def attend(self, q, page_table, kv_lens, q_start=None, scale=None, causal=True, window=0, out=None, lse=None,
                return_lse=False, workspace=None, stream=None):
@@ -503,17 +515,17 @@ class KVCache:
         if q_start is not None and q_start.shape != (batch + 1,):
             raise ValueError("q_start must be [batch + 1]")
         if out is None:
-            out = (torch.empty if q_start is None else torch.zeros)(q.shape, dtype=q.dtype, device=device)
+            out = self._new(stream, torch.empty if q_start is None else torch.zeros, q.shape, q.dtype)
         elif out.dtype != q.dtype:
             raise ValueError("out must have q's dtype")
         os = self._rows(out, "out", n, heads)
         if lse is None:
             if return_lse:
-                lse = torch.zeros((n, heads), dtype=torch.float32, device=device)
+                lse = self._new(stream, torch.zeros, (n, heads), torch.float32)
         elif lse.dtype != torch.float32 or lse.device != device or lse.shape != (n, heads) or not lse.is_contiguous():
             raise ValueError(f"lse must be a contiguous float32 tensor [{n}, {heads}] on {device}")
         if workspace is None:
-            workspace = self.attend_workspace(n, heads, batch)
+            workspace = self.attend_workspace(n, heads, batch, stream)
         elif workspace.device != device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {device}")
         a = KVQueries(q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), qs[0], qs[1], os[0], os[1],

@@ -32,8 +32,9 @@ extern "C" int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_
         return DSQ_ERR_INVALID_ARG;
     if (a->dtype != DSQ_DTYPE_F16 && a->dtype != DSQ_DTYPE_BF16)
         return a->dtype == DSQ_DTYPE_F32 ? DSQ_ERR_UNSUPPORTED : DSQ_ERR_INVALID_ARG;
-    if (a->batch > 0 && !a->q_start && a->q_tokens % a->batch) return DSQ_ERR_INVALID_ARG;
-    if ((int64_t)a->table_pages * d->page_tokens >= ((int64_t)1 << 31) || a->q_tokens * a->q_heads >= ((int64_t)1 << 31))
+    if (!a->q_start && (a->batch == 0 ? a->q_tokens > 0 : a->q_tokens % a->batch != 0)) return DSQ_ERR_INVALID_ARG;
+    if ((int64_t)a->table_pages * d->page_tokens >= ((int64_t)1 << 30) ||
+        a->q_tokens >= ((int64_t)1 << 30) / a->q_heads)  // token and row numbers are ints, with room to round up
         return DSQ_ERR_UNSUPPORTED;
     const bool many = many_rows(d, a) && d->pages > 0;
     const size_t need = many ? kv_prompt_workspace(d->head_dim) : kv_split_workspace();

@@ -464,11 +464,11 @@ typedef struct {
     void *out;      /* device; likewise, same dtype; elements must not overlap one another or q */
     float *lse;     /* device fp32 [q_tokens][q_heads], or NULL: log sum_j exp(score_j) */
     int64_t q_token, q_head, out_token, out_head;  /* strides as in dsq_kv_rows */
-    int64_t q_tokens;   /* rows of q, out and lse */
+    int64_t q_tokens;   /* rows of q, out and lse; times q_heads, below 2^30 */
     int32_t dtype;      /* DSQ_DTYPE_F16 or DSQ_DTYPE_BF16 */
     int32_t q_heads;    /* a multiple of kv_heads */
     int32_t batch;
-    int32_t table_pages; /* columns of page_table */
+    int32_t table_pages; /* columns of page_table; times page_tokens, below 2^30 */
     int32_t causal;     /* 1: a query at position p sees tokens 0 .. p; 0: all tokens of its sequence */
     int32_t window;     /* > 0 (with causal): only the last `window` of those; 0: no limit */
     float scale;        /* score_j = scale * <q, k_j>; finite */
@@ -494,11 +494,15 @@ typedef struct {
  * q_start[batch] are left as they are.  What lies in the cache behind a
  * sequence's tokens, or before or behind what a query sees, never enters its
  * result, NaN included.  A NaN that a query sees makes its lse NaN when it is a
- * key's, and NaN of elements of its out.  Lengths are clamped to [0,
+ * key's (a value's may), and NaN of elements of its out.  Lengths are clamped to [0,
  * table_pages * page_tokens], row numbers to [0, q_tokens]; tokens on a page
  * outside [0, pages) are not seen.
  * Scores, maxima, sums and outputs are accumulated in fp32; the softmax's
- * numerators are rounded to fp16 before they multiply V.
+ * numerators are rounded to fp16 before they multiply V (K and V are exact).
+ * Sequences of up to 16 rows per kv head, on average, take a kernel of
+ * warp-level matrix instructions, ones of more rows a tcgen05 kernel; both
+ * deal the batch's work out evenly, so one call may mix long and short
+ * sequences.  One launch for few and short ones, else two.
  * Asynchronous; allocates nothing; the same inputs give the same bits.
  * Returns DSQ_OK, DSQ_ERR_INVALID_ARG, DSQ_ERR_UNSUPPORTED,
  * DSQ_ERR_BUFFER_TOO_SMALL or DSQ_ERR_CUDA.

@@ -148,8 +148,9 @@ GOOD_Q = dict(q=4096, out=1 << 21, lse=1 << 22, q_token=2048, q_head=128, out_to
     (dict(q_token=2044), BAD), (dict(q_head=1), BAD), (dict(out_token=2052), BAD), (dict(out_head=64), BAD),
     (dict(out_token=0), BAD), (dict(out_token=128), BAD), (dict(q_heads=0), BAD), (dict(q_heads=12), BAD), (dict(batch=-1), BAD),
     (dict(q_tokens=-6), BAD), (dict(q_tokens=7), BAD), (dict(table_pages=-1), BAD), (dict(window=-1), BAD),
-    (dict(window=4, causal=0), BAD), (dict(scale=float("nan")), BAD), (dict(scale=float("inf")), BAD),
-    (dict(dtype=4), BAD), (dict(dtype=2), UNS), (dict(table_pages=1 << 26), UNS), (dict(q_tokens=3 << 28), UNS)])
+    (dict(batch=0), BAD), (dict(window=4, causal=0), BAD), (dict(scale=float("nan")), BAD), (dict(scale=float("inf")), BAD),
+    (dict(dtype=4), BAD), (dict(dtype=2), UNS), (dict(table_pages=1 << 24), UNS), (dict(q_tokens=3 << 28), UNS),
+    (dict(q_tokens=3 << 60), UNS)])
 def test_attend_refusals(change, rc):
     d = dsq.KVDesc(0, 8, 128, 64, 4)
     size = ctypes.c_size_t(1 << 40)
@@ -489,6 +490,101 @@ def test_attend_workspace_contents_do_not_matter_and_bits_repeat(case):
             outs.append(kv.attend(q, table, kv_lens, q_start=start, stream=s, out=torch.zeros_like(q),
                                   workspace=kv.attend_workspace(q.shape[0], q.shape[1], len(lens))))
     torch.cuda.synchronize()
+
+
+def _check_on_gpu(out, lse, q, seqs, lens, start, dtype, window=0):
+    """_check's bounds for long causal sequences, the 64-bit attention on the GPU."""
+    d = q.shape[-1]
+    for b, (k, v) in enumerate(seqs):
+        r0, r1 = int(start[b]), int(start[b + 1])
+        k, v = (torch.from_numpy(x).cuda() for x in (k, v))
+        pos = lens[b] - (r1 - r0) + torch.arange(r1 - r0, device="cuda")[:, None]
+        t = torch.arange(lens[b], device="cuda")
+        seen = (t <= pos) & ((t > pos - window) if window else (t >= 0))
+        share = q.shape[1] // k.shape[1]
+        for h in range(q.shape[1]):
+            x, kh, vh = q[r0:r1, h].double().cuda(), k[:, h // share], v[:, h // share]
+            y = (x @ kh.T * d ** -0.5).masked_fill(~seen, -torch.inf)
+            total = torch.logsumexp(y, -1)
+            p = torch.where(seen, torch.exp(y - total[:, None]), 0.0)
+            want, P = p @ vh, p @ vh.abs()
+            ds = (d + 8) * 2.0 ** -23 * (x.abs() @ kh.abs().T * d ** -0.5).amax(-1)
+            tol = (2 * (ds + 2.0 ** -20) + 2.0 ** -11)[:, None] * P + (lens[b] * 2.0 ** -25 * vh.abs().max()
+                                                                      + EPS[dtype] * want.abs() + 2.0 ** -25)
+            assert bool(((out[r0:r1, h].double() - want).abs() <= tol).all()), (b, h)
+            off = (lse[r0:r1, h].double() - total).abs()
+            assert bool((off <= ds + 2.0 ** -20 + 2.0 ** -22 * total.abs()).all()), (b, h, float(off.max()))
+
+
+LONG = [  # lens, new rows, kv heads, share, dim, page, window
+    ([3000], [1500], 4, 8, 128, 64, 0),                # many jobs a CTA, joined across CTAs
+    ([1400, 900, 33, 2300], [700, 900, 20, 130], 6, 3, 64, 16, 0),
+    ([2500, 2049], [400, 513], 2, 4, 256, 32, 0),
+    ([6000, 130, 4000], [37, 21, 64], 2, 2, 128, 48, 0),   # jobs of one row tile, shared by units
+    ([5000], [1100], 3, 1, 128, 128, 300),
+    ([4000, 5000], [1, 1], 5, 8, 128, 64, 0),
+    ([9000, 17, 3000], [2, 1, 2], 3, 8, 64, 32, 0),
+    ([7000], [1], 1, 16, 256, 16, 0),
+    ([1300] * 40, [1] * 40, 8, 4, 128, 64, 0),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", range(len(LONG)))
+def test_attend_long_and_joined(case):
+    lens, new, h, share, d, page, window = LONG[case]
+    dtype = (F16, BF16)[case % 2]
+    kv, seqs, q, table, kv_lens, start = _problem(700 + case, lens, new, h, share, d, page, dtype)
+    out, lse = kv.attend(q.cuda(), table, kv_lens, q_start=torch.from_numpy(start).cuda(), return_lse=True, window=window)
+    _check_on_gpu(out, lse, q, seqs, lens, start, dtype, window)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [0.0, -0.3])
+@pytest.mark.parametrize("case", [3, 8])
+def test_attend_scales_of_zero_and_below(case, scale):
+    lens, new, h, share, d, page = SHAPES[case]
+    kv, seqs, q, table, kv_lens, start = _problem(case + 800, lens, new, h, share, d, page, F16)
+    out, lse = kv.attend(q.cuda(), table, kv_lens, q_start=torch.from_numpy(start).cuda(), scale=scale, return_lse=True)
+    _check(out, lse, q, seqs, lens, start, F16, scale=scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [4, 100])
+def test_a_query_of_nan_spoils_its_own_row_alone(new):
+    kv, seqs, q, table, kv_lens, start = _problem(850 + new, [600], [new], 2, 2, 128, 64, BF16)
+    clean = kv.attend(q.cuda(), table, kv_lens)
+    q[new // 2, 1, 5] = float("nan")
+    out = kv.attend(q.cuda(), table, kv_lens)
+    assert torch.isnan(out[new // 2, 1]).all()
+    out[new // 2, 1] = clean[new // 2, 1]
+    assert torch.equal(out, clean)
+
+
+@pytest.mark.gpu
+def test_new_tensors_of_a_side_stream_are_made_on_it():
+    """Calls on another stream than the current one, which is kept busy: what they
+    return is zeroed and filled in their own stream's order."""
+    kv, seqs, q, table, kv_lens, start = _problem(870, [300, 40], [1, 1], 2, 4, 64, 16, F16)
+    q, more = q.cuda(), torch.zeros(7, 8, 64, dtype=F16, device="cuda")
+    more[:2] = q
+    qs = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    slots = torch.tensor([int(table[0, 0]) * 16, -1], device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    want = kv.attend(q, table, kv_lens)
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        busy = torch.randn(4096, 4096, device="cuda")
+        for _ in range(20):
+            busy = busy @ busy * 1e-3
+        out, lse = kv.attend(more, table, kv_lens, q_start=qs, return_lse=True, stream=stream)
+        k, v = kv.read(slots, stream=stream)
+        side.synchronize()
+        with torch.cuda.stream(side):
+            assert torch.equal(out[:2], want) and not out[2:].any() and not lse[2:].any()
+            assert not k[1].any() and np.array_equal(k[0].double().cpu().numpy(), seqs[0][0][0])
+        torch.cuda.synchronize()
 
 
 @pytest.mark.gpu
