@@ -478,8 +478,9 @@ class KVCache:
         """Scratch for attend() calls of these sizes that follow one another;
         calls that may overlap need one each."""
         size = ctypes.c_size_t(0)
-        a = KVQueries(q_tokens=int(q_tokens), q_heads=int(q_heads), batch=int(batch))
-        a.q_tokens = a.q_tokens // max(a.batch, 1) * a.batch
+        # the size is asked for with a q_start, which a query of it does not read:
+        # any number of rows may be any number of sequences'
+        a = KVQueries(q_tokens=int(q_tokens), q_heads=int(q_heads), batch=int(batch), q_start=self._data or 256)
         rc = library().dsq_kv_attend(self._d, None, ctypes.byref(a), None, ctypes.byref(size), None)
         if rc != DSQ_ERR_BUFFER_TOO_SMALL:
             _check(rc, "dsq_kv_attend")

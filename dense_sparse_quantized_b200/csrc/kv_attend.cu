@@ -1,4 +1,6 @@
 // kv_attend.cu -- dsq_kv_attend: argument checks and the choice of kernel.
+#include <algorithm>
+
 #include "kv.h"
 
 using namespace dsq;
@@ -14,10 +16,35 @@ int sm_count(int device) {
     return n;
 }
 
-// Rows of a job, on average: query tokens of a sequence times the heads of a
-// group.
+// Which kernel, by the time either takes, in microseconds, for sequences of
+// average rows and of as many tokens as the pages hold.  kv_split.cu works on
+// units of 16 rows (8 at 256 dimensions or for 8 rows in all) x 32 tokens,
+// kv_prompt.cu on units of 256 (128 at 256 dimensions) x 128 tokens and three
+// units' time more for each piece of work; up to 128 rows it takes a unit in
+// three quarters of the time.  Measured, fp16, causal, microseconds
+// (kv_split / kv_prompt), of (sequences x kv heads, rows, tokens):
+//   128 dimensions: (8, 96, 4096) 21 / 51, (64, 24, 4096) 35 / 54,
+//     (64, 96, 4096) 79 / 55, (512, 24, 1024) 63 / 92, (512, 96, 1024) 176 / 93,
+//     (64, 256, 256) 32 / 15
+//   64: (64, 48, 4096) 30 / 38, (64, 96, 4096) 49 / 39, (512, 96, 1024) 91 / 68
+//   256: (64, 16, 4096) 51 / 77, (64, 48, 4096) 118 / 79, (8, 96, 4096) 38 / 77
+double rows_of(const dsq_kv_desc *d, const dsq_kv_queries *a) {
+    return a->batch ? (double)a->q_tokens / a->batch * (a->q_heads / d->kv_heads) : 0.0;
+}
 bool many_rows(const dsq_kv_desc *d, const dsq_kv_queries *a) {
-    return a->batch > 0 && a->q_tokens / a->batch * (a->q_heads / d->kv_heads) > 16;
+    const double each = a->batch ? (double)a->q_tokens / a->batch : 0.0, rows = rows_of(d, a);
+    if (rows <= 8 || d->pages == 0) return false;
+    const double jobs = (double)a->batch * d->kv_heads;
+    double tokens = (double)a->table_pages * d->page_tokens;
+    if (a->window) tokens = fmin(tokens, a->window + each);
+    if (a->causal) tokens = fmax(tokens - each / 2, 1.0);
+    const bool wide = d->head_dim == 256;
+    const double few_unit = d->head_dim == 64 ? 0.8e-3 : d->head_dim == 128 ? 1.36e-3 : 1.95e-3;
+    const double few = 8.0 + few_unit * jobs * ceil(rows / (wide ? 8 : 16)) * ceil(tokens / 32);
+    const double many_unit = (d->head_dim == 64 ? 2.0 : d->head_dim == 128 ? 2.7 : 3.7) * (rows <= 128 && !wide ? 0.75 : 1.0);
+    const double tiles = jobs * ceil(rows / (wide ? 128 : 256)), units = ceil(tokens / 128);
+    const double many = 12.0 + many_unit * fmax(fmin(units + 3, 9.0), tiles * (units + 3) / 148);
+    return many < few;
 }
 
 }  // namespace
@@ -36,8 +63,8 @@ extern "C" int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_
     if ((int64_t)a->table_pages * d->page_tokens >= ((int64_t)1 << 30) ||
         a->q_tokens >= ((int64_t)1 << 30) / a->q_heads)  // token and row numbers are ints, with room to round up
         return DSQ_ERR_UNSUPPORTED;
-    const bool many = many_rows(d, a) && d->pages > 0;
-    const size_t need = many ? kv_prompt_workspace(d->head_dim) : kv_split_workspace();
+    // by the queries' shape alone, so that one workspace does for any lengths
+    const size_t need = rows_of(d, a) <= 8 ? kv_split_workspace() : std::max(kv_split_workspace(), kv_prompt_workspace(d->head_dim));
     if (!workspace || *workspace_bytes < need) {
         *workspace_bytes = need;
         return DSQ_ERR_BUFFER_TOO_SMALL;
@@ -78,6 +105,6 @@ extern "C" int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_
     k.kv_lens = a->kv_lens;
     k.q_start = a->q_start;
     const int sms = sm_count(d->device);
-    return many ? launch_kv_prompt(k, d->head_dim, a->dtype, workspace, sms, (cudaStream_t)stream)
+    return many_rows(d, a) ? launch_kv_prompt(k, d->head_dim, a->dtype, workspace, sms, (cudaStream_t)stream)
                 : launch_kv_split(k, d->head_dim, a->dtype, workspace, sms, (cudaStream_t)stream);
 }

@@ -148,19 +148,24 @@ inline KvCarry *kv_carries(void *workspace) {
     return (KvCarry *)((uint8_t *)workspace + kMaxCtas * 2 * kv_part_floats<D, R>() * 4);
 }
 
-// Joins them, a warp a row and up to four rows a warp, always in the same
-// order.
-template <int R>
-__host__ __device__ constexpr int join_rows() { return R >= 32 ? 32 : 8; }  // of a block
-template <int D, int R, typename T>
+// Joins them, always in the same order.  A warp takes N rows; or, of short
+// tiles, eight warps take one row and share out its parts (37 parts of 8 rows,
+// four heads of 7449 tokens: 22 us for the whole attention with one warp's loop
+// over them, 14 us so).
+template <int D, int R, int N, bool SHARED, typename T>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ KvAttend a, const float *__restrict__ parts,
                                                    const KvCarry *__restrict__ carries) {
     kv_after_previous();
-    constexpr int E = D / 32, N = join_rows<R>() / 8;  // elements of a lane, rows of a warp
+    constexpr int E = D / 32, S = SHARED ? 8 : 1;  // elements of a lane; warps to a row
+    static_assert(!SHARED || N == 1, "");
     const KvCarry c = carries[blockIdx.x];
     if (!c.valid) return;
     const KvSeq s = kv_seq(a, c.b);
-    const int lane = threadIdx.x & 31, row0 = blockIdx.y * join_rows<R>() + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = SHARED ? warp : 0;
+    const int row0 = SHARED ? blockIdx.y : (blockIdx.y * 8 + warp) * N, left = s.rows * a.share - (c.qt * R + row0);
+    if (left <= 0) return;  // the whole block, where it shares
+    const float *const at = parts + row0 * D + lane * E, *const ends = parts + R * D + row0;
+    auto part = [&](int i) { return (2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * kv_part_floats<D, R>(); };
     float top[N], sum[N], x[N][E];
 #pragma unroll
     for (int n = 0; n < N; n++) {
@@ -169,39 +174,52 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ KvAtt
 #pragma unroll
         for (int e = 0; e < E; e++) x[n][e] = 0.0f;
     }
-    auto part_of = [&](int i) { return parts + (2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * kv_part_floats<D, R>() + row0 * D; };
-    const int maxima = (R - row0) * D + row0;  // from there on
-#pragma unroll 4
-    for (int i = 0; i <= c.more; i++)
+#pragma unroll 8
+    for (int i = mine; i <= c.more; i += S)
 #pragma unroll
-        for (int n = 0; n < N; n++) top[n] = fmaxf(top[n], part_of(i)[maxima + 8 * n]);
-#pragma unroll 2
-    for (int i = 0; i <= c.more; i++) {
-        const float *part = part_of(i);
-        float v[N][E], m[N], l[N];
+        for (int n = 0; n < N; n++) top[n] = fmaxf(top[n], ends[part(i) + n]);
+#pragma unroll(N == 1 ? 8 : 2)
+    for (int i = mine; i <= c.more; i += S) {
+        const size_t of = part(i);
 #pragma unroll
         for (int n = 0; n < N; n++) {
-            m[n] = part[maxima + 8 * n];
-            l[n] = part[maxima + R + 8 * n];
+            const float f = ex2(ends[of + n] - top[n]);
+            sum[n] += ends[of + R + n] * f;
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
-                const float2 f = *reinterpret_cast<const float2 *>(part + 8 * n * D + lane * E + e);
-                v[n][e] = f.x;
-                v[n][e + 1] = f.y;
+                const float2 v = *reinterpret_cast<const float2 *>(at + of + n * D + e);
+                x[n][e] += v.x * f;
+                x[n][e + 1] += v.y * f;
             }
         }
+    }
+    if constexpr (SHARED) {
+        __shared__ float found[8][D + 2];
 #pragma unroll
-        for (int n = 0; n < N; n++) {
-            const float f = ex2(m[n] - top[n]);
-            sum[n] += l[n] * f;
+        for (int e = 0; e < E; e++) found[warp][e * 32 + lane] = x[0][e];
+        if (lane == 0) {
+            found[warp][D] = top[0];
+            found[warp][D + 1] = sum[0];
+        }
+        __syncthreads();
+        if (warp) return;
+        top[0] = kNoMax;
+        for (int w = 0; w < 8; w++) top[0] = fmaxf(top[0], found[w][D]);
+        sum[0] = 0.0f;
 #pragma unroll
-            for (int e = 0; e < E; e++) x[n][e] += v[n][e] * f;
+        for (int e = 0; e < E; e++) x[0][e] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; w++) {
+            const float f = ex2(found[w][D] - top[0]);
+            sum[0] += found[w][D + 1] * f;
+#pragma unroll
+            for (int e = 0; e < E; e++) x[0][e] += found[w][e * 32 + lane] * f;
         }
     }
 #pragma unroll
     for (int n = 0; n < N; n++) {
-        const int rho = c.qt * R + row0 + 8 * n;
-        if (rho >= s.rows * a.share) continue;
+        if (n >= left) continue;
+        const int rho = c.qt * R + row0 + n;
         const float inv = sum[n] == 0.0f ? 0.0f : 1.0f / sum[n];
         T *to = (T *)a.out + row_at(a, s, c.head, rho, a.out_token, a.out_head) + lane * E;
 #pragma unroll
@@ -210,9 +228,14 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ KvAtt
     }
 }
 
+// jobs: at most so many.  Fewer than half the CTAs: each spans several, and a
+// warp takes one row and many parts, else four rows and few parts.
 template <int D, int R, typename T>
-int launch_join(const KvAttend &a, const float *parts, const KvCarry *carries, int ctas, cudaStream_t st) {
-    return kv_launch(join_kernel<D, R, T>, dim3(ctas, R / join_rows<R>()), 256, 0, st, a, parts, carries);
+int launch_join(const KvAttend &a, const float *parts, const KvCarry *carries, int ctas, int64_t jobs, cudaStream_t st) {
+    if constexpr (R < 32) return kv_launch(join_kernel<D, R, 1, true, T>, dim3(ctas, R), 256, 0, st, a, parts, carries);
+    else if (2 * jobs <= ctas)
+        return kv_launch(join_kernel<D, R, 1, false, T>, dim3(ctas, R / 8), 256, 0, st, a, parts, carries);
+    else return kv_launch(join_kernel<D, R, 4, false, T>, dim3(ctas, R / 32), 256, 0, st, a, parts, carries);
 }
 
 }  // namespace dsq

@@ -52,7 +52,8 @@ constexpr int kN = 128;          // tokens of a unit
 constexpr int kBlk = 128 * 128;  // bytes of 128 rows x 64 dimensions, swizzled
 constexpr int kThreads = 512;
 constexpr int kFlags = 4;        // units whose flags are kept
-constexpr int kPieceCost = 2;    // units' time that a piece takes besides its units: queries in, outputs out
+constexpr int kPieceCost = 3;    // units' time that a piece takes besides its units: queries in, outputs out
+constexpr int kMinRun = 6;       // least cost of a CTA's run: shorter ones cost more to join than they save
 
 template <int D_>
 struct Shape {
@@ -276,7 +277,7 @@ __device__ __forceinline__ Start find_run(const KvAttend &a, bool one_each, Shar
             for (int b = lane; b < a.batch; b += 32) total += head_cost(b) * a.c.kv_heads;
 #pragma unroll
         for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(kFull, total, m);
-        run = divide(total + gridDim.x - 1, gridDim.x);
+        run = max(divide(total + gridDim.x - 1, gridDim.x), (int64_t)kMinRun);
         u0 = min(total, run * blockIdx.x);
         u1 = min(total, u0 + run);
     }
@@ -1020,7 +1021,7 @@ int launch_prompt(const KvAttend &a, void *workspace, int sms, cudaStream_t st) 
     if (!once.set_smem((const void *)kernel, S::kSmem)) return DSQ_ERR_CUDA;
     const int grid = one_each ? (int)jobs : std::min(sms, kMaxCtas);
     const int rc = kv_launch(kernel, grid, kThreads, S::kSmem, st, p);
-    return rc != DSQ_OK || one_each ? rc : launch_join<D, S::R, T>(a, p.parts, p.carries, grid, st);
+    return rc != DSQ_OK || one_each ? rc : launch_join<D, S::R, T>(a, p.parts, p.carries, grid, jobs, st);
 }
 
 template <typename T>

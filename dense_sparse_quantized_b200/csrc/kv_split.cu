@@ -674,7 +674,7 @@ int launch_split(const KvAttend &a, void *workspace, int sms, cudaStream_t st) {
     if (!once.set_smem((const void *)kernel, S::kSmem)) return DSQ_ERR_CUDA;
     const int grid = one_each ? (int)jobs : std::min(sms, kMaxCtas);
     const int rc = kv_launch(kernel, grid, S::NW * 32, S::kSmem, st, p);
-    return rc != DSQ_OK || one_each ? rc : launch_join<S::D, S::R, T>(a, p.parts, p.carries, grid, st);
+    return rc != DSQ_OK || one_each ? rc : launch_join<S::D, S::R, T>(a, p.parts, p.carries, grid, jobs, st);
 }
 
 template <typename T>
