@@ -16,18 +16,19 @@ int sm_count(int device) {
     return n;
 }
 
-// Which kernel, by the time either takes, in microseconds, for sequences of
-// average rows and of as many tokens as the pages hold.  kv_split.cu works on
-// units of 16 rows (8 at 256 dimensions or for 8 rows in all) x 32 tokens,
-// kv_prompt.cu on units of 256 (128 at 256 dimensions) x 128 tokens and three
-// units' time more for each piece of work; up to 128 rows it takes a unit in
-// three quarters of the time.  Measured, fp16, causal, microseconds
-// (kv_split / kv_prompt), of (sequences x kv heads, rows, tokens):
-//   128 dimensions: (8, 96, 4096) 21 / 51, (64, 24, 4096) 35 / 54,
-//     (64, 96, 4096) 79 / 55, (512, 24, 1024) 63 / 92, (512, 96, 1024) 176 / 93,
-//     (64, 256, 256) 32 / 15
-//   64: (64, 48, 4096) 30 / 38, (64, 96, 4096) 49 / 39, (512, 96, 1024) 91 / 68
-//   256: (64, 16, 4096) 51 / 77, (64, 48, 4096) 118 / 79, (8, 96, 4096) 38 / 77
+// Which kernel, by estimates in microseconds of what either takes, for
+// sequences of average rows and of as many tokens as the pages hold (or their
+// window).  kv_split.cu works on units of 16 rows (8 at 256 dimensions) x 32
+// tokens and takes four units' time more for each tile of rows; kv_prompt.cu on
+// units of 256 rows (128 at 256 dimensions) x 128 tokens and three units' time
+// more for each piece, three quarters of the time for up to 128 rows.
+// Measured, fp16, causal, microseconds (kv_split / kv_prompt), of (sequences x
+// kv heads, rows, tokens):
+//   128 dimensions: (8, 96, 4096) 21 / 26, (8, 96, 16384) 44 / 33,
+//     (64, 24, 4096) 35 / 40, (64, 96, 1024) 33 / 26, (64, 96, 256) 20 / 13,
+//     (512, 24, 256) 33 / 43, (512, 96, 256) 79 / 48
+//   64: (64, 48, 4096) 30 / 38, (64, 96, 256) 16 / 11, (512, 96, 256) 39 / 35
+//   256: (64, 16, 4096) 51 / 77, (64, 48, 1024) 47 / 34, (8, 96, 1024) 16 / 31
 double rows_of(const dsq_kv_desc *d, const dsq_kv_queries *a) {
     return a->batch ? (double)a->q_tokens / a->batch * (a->q_heads / d->kv_heads) : 0.0;
 }
@@ -40,10 +41,13 @@ bool many_rows(const dsq_kv_desc *d, const dsq_kv_queries *a) {
     if (a->causal) tokens = fmax(tokens - each / 2, 1.0);
     const bool wide = d->head_dim == 256;
     const double few_unit = d->head_dim == 64 ? 0.8e-3 : d->head_dim == 128 ? 1.36e-3 : 1.95e-3;
-    const double few = 8.0 + few_unit * jobs * ceil(rows / (wide ? 8 : 16)) * ceil(tokens / 32);
+    const double few_tiles = jobs * ceil(rows / (wide ? 8 : 16));
+    const double few = (few_tiles <= 148 ? 8.0 : 12.0) + few_unit * few_tiles * (ceil(tokens / 32) + 4);
     const double many_unit = (d->head_dim == 64 ? 2.0 : d->head_dim == 128 ? 2.7 : 3.7) * (rows <= 128 && !wide ? 0.75 : 1.0);
-    const double tiles = jobs * ceil(rows / (wide ? 128 : 256)), units = ceil(tokens / 128);
-    const double many = 12.0 + many_unit * fmax(fmin(units + 3, 9.0), tiles * (units + 3) / 148);
+    const double many_tiles = jobs * ceil(rows / (wide ? 128 : 256)), units = ceil(tokens / 128);
+    const double many = many_tiles <= 148 && units <= 4
+                            ? 7.0 + many_unit * (units + 1)
+                            : 12.0 + many_unit * fmax(fmin(units + 3, 7.0), many_tiles * (units + 3) / 148);
     return many < few;
 }
 
