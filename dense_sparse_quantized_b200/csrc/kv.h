@@ -46,7 +46,8 @@ inline int kv_check_desc(const dsq_kv_desc *d) {
     if (!d || d->kv_heads < 1 || d->page_tokens < 1 || d->page_tokens % kKvTile || d->pages < 0 || d->device < 0)
         return DSQ_ERR_INVALID_ARG;
     if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256) return DSQ_ERR_UNSUPPORTED;
-    if ((int64_t)d->pages * d->page_tokens >= ((int64_t)1 << 31)) return DSQ_ERR_UNSUPPORTED;
+    const int64_t slots = (int64_t)d->pages * d->page_tokens;
+    if (slots >= ((int64_t)1 << 31) || slots / kKvTile * d->kv_heads >= ((int64_t)1 << 31)) return DSQ_ERR_UNSUPPORTED;
     return DSQ_OK;
 }
 
@@ -57,7 +58,7 @@ inline KvView kv_view(const dsq_kv_desc *d, const void *cache) {
 
 // Where the tile with token offset `off` of (page, head) starts.
 __device__ __forceinline__ int64_t kv_tile_at(const KvView &c, int D, int page, int head, int off) {
-    return (((int64_t)page * c.kv_heads + head) * c.page_tiles + off / kKvTile) * kv_tile_bytes(D);
+    return (int64_t)((page * c.kv_heads + head) * c.page_tiles + off / kKvTile) * kv_tile_bytes(D);  // fewer than 2^31 tiles
 }
 
 // A group's word: scale (fp16, low four bits zero) and zero point.

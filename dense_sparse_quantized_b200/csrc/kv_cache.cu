@@ -152,14 +152,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
                                                           int64_t tokens) {
     constexpr int kLanes = D / 8;
     kv_after_previous();
-    const int64_t t = (int64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
-    const int dim = (threadIdx.x % kLanes) * 8, head = blockIdx.y;
+    const int64_t t0 = (int64_t)blockIdx.x * (kThreads / kLanes);  // the block's first token
+    const int t = threadIdx.x / kLanes, dim = (threadIdx.x % kLanes) * 8, head = blockIdx.y;
     int64_t slot = -1;
     uint4 k = make_uint4(0, 0, 0, 0), v = k;
-    if (t < tokens) {
-        k = *reinterpret_cast<const uint4 *>((const T *)r.k + t * r.k_token + head * r.k_head + dim);
-        v = *reinterpret_cast<const uint4 *>((const T *)r.v + t * r.v_token + head * r.v_head + dim);
-        slot = slots[t];
+    if (t < tokens - t0) {
+        k = *reinterpret_cast<const uint4 *>((const T *)r.k + t0 * r.k_token + head * r.k_head + t * r.k_token + dim);
+        v = *reinterpret_cast<const uint4 *>((const T *)r.v + t0 * r.v_token + head * r.v_head + t * r.v_token + dim);
+        slot = slots[t0 + t];
     }
     // Even lanes work out the key group's scale and zero, odd ones the value
     // group's, for both.
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         kc = codes_of<T>(k, kg, false);
         vc = codes_of<T>(v, vg, false);
     }
-    if (slot < 0 || slot >= c.slots) return;
+    if ((uint64_t)slot >= (uint64_t)c.slots) return;
     const Place at = place_of<D>(c, (int)slot, head);
     uint8_t *codes = cache + at.tile + at.row * (D / 2) + dim / 2;
     *reinterpret_cast<uint32_t *>(codes + kv_codes(D, 0)) = kc;

@@ -396,7 +396,8 @@ DSQ_API int dsq_decompose(const dsq_desc *d, const float *w, void *codes, void *
 enum { DSQ_DTYPE_F16 = 0, DSQ_DTYPE_BF16 = 1, DSQ_DTYPE_F32 = 2 };
 
 /* One layer's cache.  kv_heads >= 1; head_dim 64, 128 or 256; page_tokens a
- * positive multiple of 16; pages >= 0; pages * page_tokens < 2^31.  The
+ * positive multiple of 16; pages >= 0; pages * page_tokens < 2^31, and
+ * pages * page_tokens / 16 * kv_heads < 2^31.  The
  * kernels run on CUDA device `device`, whichever is current. */
 typedef struct {
     int32_t device;
@@ -419,7 +420,7 @@ typedef struct {
  * dsq_kv_bytes -- the size of the cache's memory, which the caller allocates
  * on the device (128-byte aligned) and owns.  Host-only.  Returns DSQ_OK,
  * DSQ_ERR_INVALID_ARG or DSQ_ERR_UNSUPPORTED (a head_dim other than 64, 128
- * or 256, or 2^31 tokens or more).
+ * or 256, or more tokens or tiles than that).
  */
 DSQ_API int dsq_kv_bytes(const dsq_kv_desc *d, size_t *bytes);
 

@@ -81,7 +81,7 @@ UNS = dsq.DSQ_ERR_UNSUPPORTED
 
 @pytest.mark.parametrize("desc,rc", [
     ((0, 0, 128, 64, 4), BAD), ((0, 8, 128, 0, 4), BAD), ((0, 8, 128, 24, 4), BAD), ((0, 8, 128, 64, -1), BAD),
-    ((-1, 8, 128, 64, 4), BAD), ((0, 8, 96, 64, 4), UNS), ((0, 8, 0, 64, 4), UNS), ((0, 1, 64, 1 << 16, 1 << 15), UNS),
+    ((-1, 8, 128, 64, 4), BAD), ((0, 8, 96, 64, 4), UNS), ((0, 8, 0, 64, 4), UNS), ((0, 1, 64, 1 << 16, 1 << 15), UNS), ((0, 1 << 15, 64, 16, 1 << 16), UNS),
     ((0, 8, 128, 64, 4), dsq.DSQ_OK), ((0, 1, 64, 16, 0), dsq.DSQ_OK)])
 def test_bytes_refusals(desc, rc):
     size = ctypes.c_size_t(0)
