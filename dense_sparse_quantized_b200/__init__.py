@@ -398,7 +398,9 @@ class KVCache:
         self.device = data.device
         self.kv_heads, self.head_dim = int(kv_heads), int(head_dim)
         self.page_tokens, self.pages = int(page_tokens), int(pages)
-        self._lib, self._torch = library(), torch
+        self._lib, self._torch, self._index = library(), torch, self.desc.device
+        self._int32, self._int64 = torch.int32, torch.int64
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
         self._d, self._data = ctypes.byref(self.desc), data.data_ptr()
         self._dtypes = {torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
 
@@ -414,7 +416,7 @@ class KVCache:
         # a decode step makes these calls by the dozen: the raw handle costs a
         # tenth of a torch.cuda.Stream object
         if stream is None:
-            return self._torch._C._cuda_getCurrentRawStream(self.desc.device)
+            return self._raw_stream(self._index)
         return _stream_ptr(stream)
 
     def _new(self, stream, fill, shape, dtype):
@@ -429,7 +431,7 @@ class KVCache:
             return fill(shape, dtype=dtype, device=self.device)
 
     def _rows(self, t, name, tokens, heads):
-        if t.device != self.device or t.shape != (tokens, heads, self.head_dim):
+        if t.get_device() != self._index or t.shape != (tokens, heads, self.head_dim):
             raise ValueError(f"{name} must be [{tokens}, {heads}, {self.head_dim}] on {self.device}")
         strides = t.stride()
         if strides[2] != 1:
@@ -437,7 +439,7 @@ class KVCache:
         return strides
 
     def _kv_rows(self, k, v, slots):
-        if (slots.dtype != self._torch.int64 or slots.device != self.device or slots.dim() != 1
+        if (slots.dtype != self._int64 or slots.get_device() != self._index or slots.dim() != 1
                 or not slots.is_contiguous()):
             raise ValueError(f"slots must be a contiguous 1-D int64 tensor on {self.device}")
         n = slots.shape[0]
@@ -511,7 +513,7 @@ class KVCache:
             raise ValueError("page_table must be [batch, pages] and kv_lens [batch]")
         batch, columns = page_table.shape
         for t in (page_table, kv_lens) if q_start is None else (page_table, kv_lens, q_start):
-            if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+            if t.dtype != self._int32 or t.get_device() != self._index or not t.is_contiguous():
                 raise ValueError(f"page_table, kv_lens and q_start must be contiguous int32 tensors on {device}")
         if q_start is not None and q_start.shape != (batch + 1,):
             raise ValueError("q_start must be [batch + 1]")
@@ -523,17 +525,18 @@ class KVCache:
         if lse is None:
             if return_lse:
                 lse = self._new(stream, torch.zeros, (n, heads), torch.float32)
-        elif lse.dtype != torch.float32 or lse.device != device or lse.shape != (n, heads) or not lse.is_contiguous():
+        elif (lse.dtype != torch.float32 or lse.get_device() != self._index or lse.shape != (n, heads)
+              or not lse.is_contiguous()):
             raise ValueError(f"lse must be a contiguous float32 tensor [{n}, {heads}] on {device}")
         if workspace is None:
             workspace = self.attend_workspace(n, heads, batch, stream)
-        elif workspace.device != device or not workspace.is_contiguous():
+        elif workspace.get_device() != self._index or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {device}")
         a = KVQueries(q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), qs[0], qs[1], os[0], os[1],
                       n, dtype, heads, batch, columns, causal, window,
                       self.head_dim ** -0.5 if scale is None else scale, page_table.data_ptr(), kv_lens.data_ptr(),
                       None if q_start is None else q_start.data_ptr())
-        size = ctypes.c_size_t(workspace.numel() * workspace.element_size())
+        size = ctypes.c_size_t(workspace.nbytes)
         rc = self._lib.dsq_kv_attend(self._d, self._data, ctypes.byref(a), workspace.data_ptr(), ctypes.byref(size),
                                      self._stream(stream))
         if rc:

@@ -7,6 +7,8 @@ using namespace dsq;
 
 namespace {
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 int sm_count(int device) {
     static std::atomic<int> known[64];
     if (device < 64 && known[device].load(std::memory_order_relaxed)) return known[device].load(std::memory_order_relaxed);
@@ -14,6 +16,11 @@ int sm_count(int device) {
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n < 1) n = 1;
     if (device < 64) known[device].store(n, std::memory_order_relaxed);
     return n;
+}
+
+// Rows of a job: query tokens of a sequence, on average, times the heads of a group.
+double rows_of(const dsq_kv_desc *d, const dsq_kv_queries *a) {
+    return a->batch ? (double)a->q_tokens / a->batch * (a->q_heads / d->kv_heads) : 0.0;
 }
 
 // Which kernel, by estimates in microseconds of what either takes, for
@@ -29,9 +36,6 @@ int sm_count(int device) {
 //     (512, 24, 256) 33 / 43, (512, 96, 256) 79 / 48
 //   64: (64, 48, 4096) 30 / 38, (64, 96, 256) 16 / 11, (512, 96, 256) 39 / 35
 //   256: (64, 16, 4096) 51 / 77, (64, 48, 1024) 47 / 34, (8, 96, 1024) 16 / 31
-double rows_of(const dsq_kv_desc *d, const dsq_kv_queries *a) {
-    return a->batch ? (double)a->q_tokens / a->batch * (a->q_heads / d->kv_heads) : 0.0;
-}
 bool many_rows(const dsq_kv_desc *d, const dsq_kv_queries *a) {
     const double each = a->batch ? (double)a->q_tokens / a->batch : 0.0, rows = rows_of(d, a);
     if (rows <= 8 || d->pages == 0) return false;
@@ -59,7 +63,7 @@ extern "C" int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_
     if (rc != DSQ_OK) return rc;
     if (!a || !workspace_bytes) return DSQ_ERR_INVALID_ARG;
     if (a->q_heads < 1 || a->q_heads % d->kv_heads || a->batch < 0 || a->q_tokens < 0 || a->table_pages < 0 ||
-        a->window < 0 || (a->window > 0 && !a->causal) || !isfinite(a->scale))
+        a->window < 0 || (a->window > 0 && !a->causal) || !isfinite(a->scale * kLog2e))
         return DSQ_ERR_INVALID_ARG;
     if (a->dtype != DSQ_DTYPE_F16 && a->dtype != DSQ_DTYPE_BF16)
         return a->dtype == DSQ_DTYPE_F32 ? DSQ_ERR_UNSUPPORTED : DSQ_ERR_INVALID_ARG;
@@ -103,12 +107,12 @@ extern "C" int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_
     k.batch = a->batch;
     k.table_pages = a->table_pages;
     k.causal = a->causal;
-    k.window = a->window;
-    k.scale_log2 = a->scale * 1.4426950408889634f;
+    k.window = std::min(a->window, 1 << 30);  // more than any position; token numbers less it stay ints
+    k.scale_log2 = a->scale * kLog2e;
     k.page_table = a->page_table;
     k.kv_lens = a->kv_lens;
     k.q_start = a->q_start;
     const int sms = sm_count(d->device);
     return many_rows(d, a) ? launch_kv_prompt(k, d->head_dim, a->dtype, workspace, sms, (cudaStream_t)stream)
-                : launch_kv_split(k, d->head_dim, a->dtype, workspace, sms, (cudaStream_t)stream);
+                           : launch_kv_split(k, d->head_dim, a->dtype, workspace, sms, (cudaStream_t)stream);
 }

@@ -151,7 +151,7 @@ inline KvCarry *kv_carries(void *workspace) {
 // Joins them, always in the same order.  A warp takes N rows; or, of short
 // tiles, eight warps take one row and share out its parts (37 parts of 8 rows,
 // four heads of 7449 tokens: 22 us for the whole attention with one warp's loop
-// over them, 14 us so).
+// over them, 12 us so).
 template <int D, int R, int N, bool SHARED, typename T>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ KvAttend a, const float *__restrict__ parts,
                                                    const KvCarry *__restrict__ carries) {

@@ -472,7 +472,7 @@ typedef struct {
     int32_t table_pages; /* columns of page_table; times page_tokens, below 2^30 */
     int32_t causal;     /* 1: a query at position p sees tokens 0 .. p; 0: all tokens of its sequence */
     int32_t window;     /* > 0 (with causal): only the last `window` of those; 0: no limit */
-    float scale;        /* score_j = scale * <q, k_j>; finite */
+    float scale;        /* score_j = scale * <q, k_j>; finite, also times log2(e) */
     const int32_t *page_table; /* device [batch][table_pages] */
     const int32_t *kv_lens;    /* device [batch] */
     const int32_t *q_start;    /* device [batch + 1], nondecreasing from 0; or NULL */

@@ -148,7 +148,7 @@ GOOD_Q = dict(q=4096, out=1 << 21, lse=1 << 22, q_token=2048, q_head=128, out_to
     (dict(q_token=2044), BAD), (dict(q_head=1), BAD), (dict(out_token=2052), BAD), (dict(out_head=64), BAD),
     (dict(out_token=0), BAD), (dict(out_token=128), BAD), (dict(q_heads=0), BAD), (dict(q_heads=12), BAD), (dict(batch=-1), BAD),
     (dict(q_tokens=-6), BAD), (dict(q_tokens=7), BAD), (dict(table_pages=-1), BAD), (dict(window=-1), BAD),
-    (dict(batch=0), BAD), (dict(window=4, causal=0), BAD), (dict(scale=float("nan")), BAD), (dict(scale=float("inf")), BAD),
+    (dict(batch=0), BAD), (dict(window=4, causal=0), BAD), (dict(scale=float("nan")), BAD), (dict(scale=float("inf")), BAD), (dict(scale=3e38), BAD),
     (dict(dtype=4), BAD), (dict(dtype=2), UNS), (dict(table_pages=1 << 24), UNS), (dict(q_tokens=3 << 28), UNS),
     (dict(q_tokens=3 << 60), UNS)])
 def test_attend_refusals(change, rc):
@@ -537,6 +537,17 @@ def test_attend_long_and_joined(case):
     kv, seqs, q, table, kv_lens, start = _problem(700 + case, lens, new, h, share, d, page, dtype)
     out, lse = kv.attend(q.cuda(), table, kv_lens, q_start=torch.from_numpy(start).cuda(), return_lse=True, window=window)
     _check_on_gpu(out, lse, q, seqs, lens, start, dtype, window)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [1, 7, 300])
+def test_attend_window_of_any_size(new):
+    """A window past every position, the largest number among them, is none."""
+    kv, seqs, q, table, kv_lens, start = _problem(860 + new, [new // 2, 400], [new, new], 1, 3, 64, 16, F16)
+    q = q.cuda()
+    want = kv.attend(q, table, kv_lens)
+    for window in (401, 1 << 30, (1 << 31) - 1):
+        assert torch.equal(kv.attend(q, table, kv_lens, window=window), want)
 
 
 @pytest.mark.gpu
