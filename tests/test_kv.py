@@ -277,9 +277,10 @@ def test_read_of_keys_alone_and_of_repeated_slots():
         assert np.array_equal(out.cpu().double().numpy(), _held(x[slots]))
 
 
-def _problem(seed, lens, new, h, share, d, page, dtype, fill=0xFF, extra=2):
+def _problem(seed, lens, new, h, share, d, page, dtype, fill=0xFF, extra=2, sizes=None):
     """A cache with the sequences' tokens on shuffled pages; all other bytes are
-    `fill` (0xFF: NaN scales)."""
+    `fill` (0xFF: NaN scales).  sizes: what each token's values are multiplied by,
+    over and over."""
     rng = np.random.default_rng(seed)
     need = [-(-n // page) for n in lens]
     pages, cols = sum(need) + extra, max(need + [1])
@@ -291,7 +292,11 @@ def _problem(seed, lens, new, h, share, d, page, dtype, fill=0xFF, extra=2):
     for b, n in enumerate(lens):
         table[b, :need[b]] = order[at:at + need[b]]
         at += need[b]
-        k, v = _rows(rng, n, h, d).to(dtype), _rows(rng, n, h, d).to(dtype)
+        k, v = _rows(rng, n, h, d), _rows(rng, n, h, d)
+        if sizes is not None and n:
+            by = torch.tensor(sizes * n)[:n, None, None]
+            k, v = k * by, v * by.flip(0)
+        k, v = k.to(dtype), v.to(dtype)
         t = np.arange(n)
         if n:
             kv.append(k.cuda(), v.cuda(), torch.from_numpy(table[b, t // page].astype(np.int64) * page + t % page).cuda())
@@ -548,6 +553,18 @@ def test_attend_window_of_any_size(new):
     want = kv.attend(q, table, kv_lens)
     for window in (401, 1 << 30, (1 << 31) - 1):
         assert torch.equal(kv.attend(q, table, kv_lens, window=window), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sizes", [[0.004], [300.0], [1.0] * 64 + [0.003] * 40 + [50.0] * 7 + [2e-6], [1.0, 1.0, 9.0], [1e4]])
+@pytest.mark.parametrize("case", [3, 4, 5, 6, 8])
+def test_attend_small_and_large_values(case, sizes):
+    """Scales from the smallest to the largest, in one run of tokens and side by side."""
+    lens, new, h, share, d, page = SHAPES[case]
+    kv, seqs, q, table, kv_lens, start = _problem(case + 900, lens, new, h, share, d, page, F16, sizes=sizes)
+    scale = float(d ** -0.5 / max(sizes))
+    out, lse = kv.attend(q.cuda(), table, kv_lens, q_start=torch.from_numpy(start).cuda(), scale=scale, return_lse=True)
+    _check(out, lse, q, seqs, lens, start, F16, scale=scale)
 
 
 @pytest.mark.gpu
