@@ -61,9 +61,6 @@ __device__ __forceinline__ int64_t kv_tile_at(const KvView &c, int D, int page, 
     return (int64_t)((page * c.kv_heads + head) * c.page_tiles + off / kKvTile) * kv_tile_bytes(D);  // fewer than 2^31 tiles
 }
 
-// A group's word: scale (fp16, low four bits zero) and zero point.
-__device__ __forceinline__ float kv_scale(uint32_t word) { return __half2float(__ushort_as_half((uint16_t)(word & 0xfff0u))); }
-
 struct KvAttend {
     KvView c;
     KvDivisor share_by, tiles_by;  // by heads of a group, by tiles of a page

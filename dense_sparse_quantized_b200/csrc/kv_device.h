@@ -83,14 +83,6 @@ __device__ __forceinline__ int up_of(uint32_t top) {
     const int e = (int)(top >> 7);  // biased; 0 for zero, 255 for an infinity or a NaN
     return e == 0 || e == 255 ? 0 : min(127 + 14 - e, 120);
 }
-template <typename T, int D>
-__device__ __forceinline__ int query_exponent(const T *row) {
-    if constexpr (std::is_same<T, __half>::value) return 0;
-    uint32_t top = 0;
-#pragma unroll 4
-    for (int i = 0; i < D / 8; i++) top = top_bits(reinterpret_cast<const uint4 *>(row)[i], top);
-    return up_of(top);
-}
 // N x 8 elements of a row in the order in which codes unpack: (0, 4), (1, 5),
 // (2, 6), (3, 7) of every eight.
 template <typename T, int N>

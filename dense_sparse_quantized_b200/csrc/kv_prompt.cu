@@ -48,7 +48,8 @@
 // pair and numerators handed over by halves, 621 -> 527; pieces' own cost dealt
 // too, 527 -> 468; no 64-bit division, 474 -> 427; turns at the exponentials,
 // 444 -> 402 (in step, both pairs wait for the same pipe); pieces worked out by
-// a warp of its own, 402 -> 387.
+// a warp of its own, 402 -> 387; the first half's numerators handed over while the
+// second's are worked out, 387 -> 382; parts joined a row a warp, 382 -> 355.
 //
 // Every mbarrier wait is bounded (ptx.h); one that runs out ends its role, the
 // others' waits run out in turn, and the CTA frees its tensor memory and

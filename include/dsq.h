@@ -500,8 +500,9 @@ typedef struct {
  * outside [0, pages) are not seen.
  * Scores, maxima, sums and outputs are accumulated in fp32; the softmax's
  * numerators are rounded to fp16 before they multiply V (K and V are exact).
- * Sequences of up to 16 rows per kv head, on average, take a kernel of
- * warp-level matrix instructions, ones of more rows a tcgen05 kernel; both
+ * Two kernels, one of warp-level matrix instructions for few rows per kv head
+ * and a tcgen05 one for many; a call takes the one that is estimated to be
+ * faster, from its rows, its heads and the lengths that its pages allow.  Both
  * deal the batch's work out evenly, so one call may mix long and short
  * sequences.  One launch for few and short ones, else two.
  * Asynchronous; allocates nothing; the same inputs give the same bits.
