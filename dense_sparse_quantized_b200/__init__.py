@@ -497,7 +497,7 @@ class KVCache:
         of each sequence in the cache, those of its queries among them;
         q_start: int32 [batch + 1], the first row of each sequence (default:
         q_tokens / batch rows each); scale: default head_dim ** -0.5; window:
-        see only the last that many tokens.  Returns out (like q), and with
+        see only the last that many tokens; out: not q's memory.  Returns out (like q), and with
         ``return_lse`` or ``lse`` also the fp32 log-sum-exp [q_tokens,
         q_heads].  Rows of no sequence stay as they are in a given out and
         lse, and hold 0 in new ones."""

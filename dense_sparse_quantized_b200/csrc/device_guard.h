@@ -4,13 +4,15 @@
 
 namespace dsq {
 
-// Makes `device` current for the scope and restores the caller's device.
+// Makes `device` current for the scope and restores the caller's device.  A
+// failure is the entry point's to return: the runtime's last error is cleared,
+// or the caller's next launch check would report it.
 struct DeviceGuard {
     int prev = -1;
     bool ok = false;
     explicit DeviceGuard(int device) {
-        if (cudaGetDevice(&prev) != cudaSuccess) return;
-        ok = prev == device || cudaSetDevice(device) == cudaSuccess;
+        ok = cudaGetDevice(&prev) == cudaSuccess && (prev == device || cudaSetDevice(device) == cudaSuccess);
+        if (!ok) cudaGetLastError();
     }
     ~DeviceGuard() {
         int cur = -1;

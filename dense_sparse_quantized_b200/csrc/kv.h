@@ -123,7 +123,9 @@ int kv_launch(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t sme
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? DSQ_OK : DSQ_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return DSQ_OK;
+    cudaGetLastError();  // returned here, not left for the caller's next check
+    return DSQ_ERR_CUDA;
 }
 
 // Sets a kernel's shared-memory limit once per device (a call per launch
@@ -135,7 +137,10 @@ struct KvOnce {
         if (cudaGetDevice(&dev) != cudaSuccess) return false;
         const uint64_t bit = 1ull << (dev & 63);
         if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return true;
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
         if (dev < 64) done.fetch_or(bit, std::memory_order_release);
         return true;
     }

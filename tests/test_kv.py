@@ -735,3 +735,22 @@ def test_binding_refusals():
         with pytest.raises(dsq.DSQError) as e:
             call()
         assert e.value.status == rc
+
+
+@pytest.mark.gpu
+def test_a_failed_call_is_its_own_failure():
+    """An unknown device fails that call, not the library's next one."""
+    kv = dsq.KVCache(2, 64, 2, 16)
+    k = torch.zeros(3, 2, 64, dtype=F16, device="cuda")
+    s = torch.arange(3, device="cuda")
+    t, n = torch.zeros(3, 1, dtype=torch.int32, device="cuda"), torch.ones(3, dtype=torch.int32, device="cuda")
+    work = kv.attend_workspace(3, 2, 3)
+    w = torch.arange(16 * 64, dtype=F32, device="cuda").view(16, 64)
+    for call in (lambda: kv.append(k, k, s), lambda: kv.read(s), lambda: kv.attend(k, t, n, workspace=work)):
+        kv.desc.device = 99
+        with pytest.raises(dsq.DSQError) as e:
+            call()
+        assert e.value.status == dsq.DSQ_ERR_CUDA
+        kv.desc.device = 0
+        dsq.decompose(w, 4, "affine", 8)
+        call()
