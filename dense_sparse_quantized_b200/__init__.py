@@ -39,7 +39,8 @@ DTYPE_F32 = 2
 EXPORTS = ("dsq_pack", "dsq_pack_two_axis", "dsq_pack_intgrid", "dsq_blob_desc", "dsq_create", "dsq_gemv", "dsq_gemv_launches", "dsq_decode",
            "dsq_handle_desc", "dsq_device_bytes", "dsq_check", "dsq_destroy", "dsq_status_string",
            "dsq_gemv_noalloc", "dsq_selftest_wait_timeout", "dsq_decompose",
-           "dsq_kv_bytes", "dsq_kv_append", "dsq_kv_read", "dsq_kv_attend")
+           "dsq_kv_bytes", "dsq_kv_append", "dsq_kv_read", "dsq_kv_attend",
+           "dsq_kv_check", "dsq_kv_selftest_wait_timeout")
 
 
 class DSQError(RuntimeError):
@@ -107,6 +108,8 @@ def library() -> ctypes.CDLL:
         lib.dsq_kv_read.argtypes = [ctypes.POINTER(KVDesc), P, ctypes.POINTER(KVRows), P, ctypes.c_int64, P]
         lib.dsq_kv_attend.argtypes = [ctypes.POINTER(KVDesc), P, ctypes.POINTER(KVQueries), P,
                                       ctypes.POINTER(SZ), P]
+        lib.dsq_kv_check.argtypes = [ctypes.POINTER(KVDesc)]
+        lib.dsq_kv_selftest_wait_timeout.argtypes = [ctypes.POINTER(KVDesc), P]
         lib.dsq_status_string.argtypes = [I]
         lib.dsq_status_string.restype = ctypes.c_char_p
         for name in EXPORTS:
@@ -542,3 +545,13 @@ class KVCache:
         if rc:
             _check(rc, "dsq_kv_attend")
         return out if lse is None else (out, lse)
+
+    def check(self):
+        """Synchronise the device; raise if a kernel of an attend() on it, of any
+        cache, gave up a bounded wait since the last check."""
+        _check(self._lib.dsq_kv_check(self._d), "dsq_kv_check")
+
+    def selftest_wait_timeout(self, stream=None):
+        """Test hook: launch a kernel whose bounded wait runs out (about 2 s);
+        the next check() raises DSQ_ERR_DEVICE."""
+        _check(self._lib.dsq_kv_selftest_wait_timeout(self._d, self._stream(stream)), "dsq_kv_selftest_wait_timeout")

@@ -153,5 +153,7 @@ int launch_kv_split(const KvAttend &a, int head_dim, int dtype, void *workspace,
 // Many query rows per sequence (kv_prompt.cu).
 size_t kv_prompt_workspace(int head_dim);
 int launch_kv_prompt(const KvAttend &a, int head_dim, int dtype, void *workspace, int sms, cudaStream_t stream);
+int launch_kv_wait_timeout(cudaStream_t stream);  // a kernel whose wait runs out
+int kv_take_status(int *word);                    // the current device's status word, cleared; waits for the device
 
 }  // namespace dsq

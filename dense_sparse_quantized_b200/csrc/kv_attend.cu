@@ -1,4 +1,5 @@
-// kv_attend.cu -- dsq_kv_attend: argument checks and the choice of kernel.
+// kv_attend.cu -- dsq_kv_attend: argument checks and the choice of kernel; the
+// report of waits that ran out.
 #include <algorithm>
 
 #include "kv.h"
@@ -115,4 +116,22 @@ extern "C" int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_
     const int sms = sm_count(d->device);
     return many_rows(d, a) ? launch_kv_prompt(k, d->head_dim, a->dtype, workspace, sms, (cudaStream_t)stream)
                            : launch_kv_split(k, d->head_dim, a->dtype, workspace, sms, (cudaStream_t)stream);
+}
+
+extern "C" int dsq_kv_check(const dsq_kv_desc *d) {
+    int rc = kv_check_desc(d);
+    if (rc != DSQ_OK) return rc;
+    DeviceGuard guard(d->device);
+    if (!guard.ok) return DSQ_ERR_CUDA;
+    int word = 0;
+    if ((rc = kv_take_status(&word)) != DSQ_OK) return rc;
+    return word == 0 ? DSQ_OK : DSQ_ERR_DEVICE;
+}
+
+extern "C" int dsq_kv_selftest_wait_timeout(const dsq_kv_desc *d, void *stream) {
+    const int rc = kv_check_desc(d);
+    if (rc != DSQ_OK) return rc;
+    DeviceGuard guard(d->device);
+    if (!guard.ok) return DSQ_ERR_CUDA;
+    return launch_kv_wait_timeout((cudaStream_t)stream);
 }

@@ -51,9 +51,10 @@
 // a warp of its own, 402 -> 387; the first half's numerators handed over while the
 // second's are worked out, 387 -> 382; parts joined a row a warp, 382 -> 355.
 //
-// Every mbarrier wait is bounded (ptx.h); one that runs out ends its role, the
-// others' waits run out in turn, and the CTA frees its tensor memory and
-// returns.
+// Every mbarrier wait is bounded (ptx.h).  One that runs out sets the device's
+// status word, which dsq_kv_check reports, and ends its role; the others' waits
+// run out in turn; what the product warps have issued is waited for (again with
+// a limit), and the CTA frees its tensor memory and returns.
 #include <algorithm>
 
 #include "kv_device.h"
@@ -116,6 +117,7 @@ constexpr int kPieces = 4;  // worked out ahead
 struct Shared {
     uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2][2], qfull[2], ofull[2], turn[2], other, joined;
     uint64_t piece_full[kPieces], piece_empty[kPieces];
+    uint64_t drained[2];                // products issued by a warp that gave up a wait
     Piece piece[kPieces];
     uint4 nans[kFlags], holes[kFlags];  // by loading warp: NaN tokens; sub-tiles without a page
     float other_m[128], other_l[128];   // of a shared job, the second pair's maxima and sums
@@ -185,6 +187,9 @@ constexpr uint32_t kOperandHigh = 64u | 1u << 14 | 2u << 29;
 constexpr uint32_t instruction(int n, bool b_mn_major) {
     return (1u << 4) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
+
+// Set when a wait ran out, until dsq_kv_check reads it; one on each device.
+__device__ int g_status;
 
 // A warp's wait, all lanes testing; the same answer for all.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
@@ -342,8 +347,9 @@ __device__ __forceinline__ Start find_run(const KvAttend &a, bool one_each, Shar
 }
 
 // Finds the run and works its pieces out, ahead of the warps that use them.
+// This role and the others: false if a wait ran out.
 template <int D, typename T>
-__device__ __forceinline__ void piece_role(const KvAttend &a, bool one_each, Shared &sh) {
+__device__ __forceinline__ bool piece_role(const KvAttend &a, bool one_each, Shared &sh) {
     using S = Shape<D>;
     constexpr int R = S::R;
     const int lane = threadIdx.x & 31;
@@ -387,13 +393,13 @@ __device__ __forceinline__ void piece_role(const KvAttend &a, bool one_each, Sha
             p.share[0] = share_of<R>(a, p, 0);
             p.share[1] = share_of<R>(a, p, 1);
         }
-        if (!warp_wait(&sh.piece_empty[n % kPieces], (n / kPieces & 1) ^ 1)) return;
+        if (!warp_wait(&sh.piece_empty[n % kPieces], (n / kPieces & 1) ^ 1)) return false;
         if (lane == 0) {
             sh.piece[n % kPieces] = p;
             mbar_arrive(&sh.piece_full[n % kPieces]);
         }
         __syncwarp();
-        if (!p.valid) return;
+        if (!p.valid) return true;
         for (int rho = p.qt * R + lane; rho <= last; rho += 32) {  // its queries come to L2 meanwhile
             const T *q = (const T *)a.q + row_at(a, p.s, p.head, rho, a.q_token, a.q_head);
 #pragma unroll
@@ -405,10 +411,11 @@ __device__ __forceinline__ void piece_role(const KvAttend &a, bool one_each, Sha
 // The pieces, for a warp of the other roles.
 struct Pieces {
     uint32_t n = 0;
+    bool ok = true;      // no wait for one ran out
     Share mine, theirs;  // the r-th pair's, and the other's
     __device__ __forceinline__ bool next(Shared &sh, Piece &p, int r) {
         const uint32_t at = n % kPieces;
-        if (!warp_wait(&sh.piece_full[at], n / kPieces & 1)) return false;
+        if (!warp_wait(&sh.piece_full[at], n / kPieces & 1)) return ok = false;
         p = sh.piece[at];
         mine = sh.piece[at].share[r];
         theirs = sh.piece[at].share[r ^ 1];
@@ -551,7 +558,7 @@ struct Loader {
 };
 
 template <int D>
-__device__ __forceinline__ void load_role(const KvAttend &a, Shared &sh, uint32_t kbuf, uint32_t vbuf, uint32_t raw0) {
+__device__ __forceinline__ bool load_role(const KvAttend &a, Shared &sh, uint32_t kbuf, uint32_t vbuf, uint32_t raw0) {
     using S = Shape<D>;
     using L = Loader<D>;
     L ld(a, sh);
@@ -567,7 +574,7 @@ __device__ __forceinline__ void load_role(const KvAttend &a, Shared &sh, uint32_
         for (int which = 0; which < 2; which++) {
             if (!warp_wait(which ? &sh.vempty[stage] : &sh.kempty[stage], phase ^ 1)) {
                 cp_async_wait<0>();
-                return;
+                return false;
             }
             cp_async_wait<S::kTurns ? 0 : 1>();  // all copies but the other half's, the last started
             __syncwarp();
@@ -598,28 +605,28 @@ __device__ __forceinline__ void load_role(const KvAttend &a, Shared &sh, uint32_
         u1 = u2;
     }
     cp_async_wait<0>();
+    return ld.pieces.ok;
 }
 
 // ----------------------------------------------------------- warps 12, 13
 // One for each row tile, so that neither waits for the other's softmax.  All
-// lanes walk, one issues.
+// lanes walk, one issues.  `it`: units worked on.
 template <int D>
-__device__ __forceinline__ void product_role(Shared &sh, uint32_t qbuf, uint32_t kbuf, uint32_t vbuf, int r) {
+__device__ __forceinline__ bool issue_products(Shared &sh, uint32_t qbuf, uint32_t kbuf, uint32_t vbuf, int r, bool lead, uint32_t &it) {
     using S = Shape<D>;
     constexpr uint32_t kScores = instruction(kN, false), kOut = instruction(D, true);
     const uint32_t st = sh.tmem + 128 * r, ot = sh.tmem + S::kO + D * r;
     const uint32_t q0 = operand(qbuf + r * S::kTile, 16), k0 = operand(kbuf, 16), v0 = operand(vbuf, kBlk);
-    const bool lead = elect_one();  // one thread throughout: a commit speaks for its own thread's products
     Pieces pieces;
     Piece p;
-    uint32_t it = 0, done = 0, queries = 0;
+    uint32_t done = 0, queries = 0;
     while (pieces.next(sh, p, r)) {
         const Share &mine = pieces.mine;
         for (int t = p.t0; t < p.t1; t++, it++) {
             const uint32_t stage = it % S::kStages, phase = it / S::kStages & 1;
             const bool on = t >= mine.x && t < mine.y && !((t - mine.x) & (mine.step - 1));
-            if (!warp_wait(&sh.kfull[stage], phase)) return;
-            if (t == mine.x && on && !warp_wait(&sh.qfull[r], queries++ & 1)) return;
+            if (!warp_wait(&sh.kfull[stage], phase)) return false;
+            if (t == mine.x && on && !warp_wait(&sh.qfull[r], queries++ & 1)) return false;
             fence_after();
             if (lead) {
                 if (on) {
@@ -634,10 +641,10 @@ __device__ __forceinline__ void product_role(Shared &sh, uint32_t qbuf, uint32_t
                 commit(&sh.kempty[stage]);
             }
             __syncwarp();
-            if (!warp_wait(&sh.vfull[stage], phase)) return;
+            if (!warp_wait(&sh.vfull[stage], phase)) return false;
 #pragma unroll
             for (int half = 0; half < 2; half++) {
-                if (on && !warp_wait(&sh.pfull[r][half], done & 1)) return;
+                if (on && !warp_wait(&sh.pfull[r][half], done & 1)) return false;
                 fence_after();
                 if (lead) {
                     if (on) {
@@ -653,6 +660,25 @@ __device__ __forceinline__ void product_role(Shared &sh, uint32_t qbuf, uint32_t
             done += on;
         }
     }
+    return pieces.ok;
+}
+
+template <int D>
+__device__ __forceinline__ bool product_role(Shared &sh, uint32_t qbuf, uint32_t kbuf, uint32_t vbuf, int r) {
+    constexpr uint32_t kStages = Shape<D>::kStages;
+    const bool lead = elect_one();  // one thread throughout: a commit speaks for its own thread's products
+    uint32_t it = 0;
+    if (!issue_products<D>(sh, qbuf, kbuf, vbuf, r, lead, it)) {
+        if (lead) commit(&sh.drained[r]);
+        __syncwarp();
+        warp_wait(&sh.drained[r], 0);
+        return false;
+    }
+    // The last releases of the ring, which nobody else waits for: none is to
+    // arrive when the CTA's shared memory is another's.
+    for (uint32_t i = it > kStages ? it - kStages : 0; i < it; i++)
+        if (!warp_wait(&sh.kempty[i % kStages], i / kStages & 1) || !warp_wait(&sh.vempty[i % kStages], i / kStages & 1)) return false;
+    return true;
 }
 
 // ------------------------------------------------------------- warps 0-7
@@ -735,7 +761,7 @@ __device__ __forceinline__ float load_queries(const KvAttend &a, const Piece &p,
 }
 
 template <int D, typename T>
-__device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh, uint32_t qbuf, int r) {
+__device__ __forceinline__ bool softmax_role(const PromptParams &pp, Shared &sh, uint32_t qbuf, int r) {
     using S = Shape<D>;
     const KvAttend &a = pp.a;
     const int row = threadIdx.x & 127, row0 = row & 96;
@@ -765,12 +791,12 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
             __syncwarp();
             if (lead) mbar_arrive(&sh.qfull[r]);
             for (int t = mine.x; t < mine.y; t += mine.step) {
-                if (!warp_wait(&sh.sfull[r], sn++ & 1)) return;
+                if (!warp_wait(&sh.sfull[r], sn++ & 1)) return false;
                 fence_after();
                 const bool in_turn = t >= both.x && t < both.y;
                 if (idle) {
                     if (in_turn) {
-                        if (!warp_wait(&sh.turn[r], (turns ^ r ^ 1) & 1)) return;
+                        if (!warp_wait(&sh.turn[r], (turns ^ r ^ 1) & 1)) return false;
                         turns++;
                     }
                     if (lead) {
@@ -832,7 +858,7 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
                 }
                 // The first pair's first turn is there from the start.
                 if (in_turn) {
-                    if (!warp_wait(&sh.turn[r], (turns ^ r ^ 1) & 1)) return;
+                    if (!warp_wait(&sh.turn[r], (turns ^ r ^ 1) & 1)) return false;
                     turns++;
                 }
                 float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
@@ -861,7 +887,7 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
             }
-            if (!warp_wait(&sh.ofull[r], on++ & 1)) return;
+            if (!warp_wait(&sh.ofull[r], on++ & 1)) return false;
             fence_after();
         }
         it0 += p.t1 - p.t0;
@@ -876,10 +902,10 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
                 fence_before();
                 __syncwarp();
                 if (lead) mbar_arrive(&sh.other);
-                if (!warp_wait(&sh.joined, joins++ & 1)) return;
+                if (!warp_wait(&sh.joined, joins++ & 1)) return false;
                 continue;
             }
-            if (!warp_wait(&sh.other, joins++ & 1)) return;
+            if (!warp_wait(&sh.other, joins++ & 1)) return false;
             fence_after();
             const Share &theirs = pieces.theirs;
             two = theirs.x < theirs.y;
@@ -959,6 +985,7 @@ __device__ __forceinline__ void softmax_role(const PromptParams &pp, Shared &sh,
             if (lead) mbar_arrive(&sh.joined);
         }
     }
+    return pieces.ok;
 }
 
 template <int D, typename T>
@@ -981,6 +1008,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             mbar_init(&sh.pfull[i][1], 4);
             mbar_init(&sh.qfull[i], 4);
             mbar_init(&sh.turn[i], 4);
+            mbar_init(&sh.drained[i], 1);
         }
         for (int i = 0; i < kPieces; i++) {
             mbar_init(&sh.piece_full[i], 1);
@@ -1001,17 +1029,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     fence_after();
 
     // 512 threads x 128 registers: 2 x 184 + 88 + 56 for the four warpgroups.
+    bool ok = true;
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-        if (warp < 4 * S::A) softmax_role<D, T>(pp, sh, qbuf, warp >> 2);
+        if (warp < 4 * S::A) ok = softmax_role<D, T>(pp, sh, qbuf, warp >> 2);
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        load_role<D>(pp.a, sh, kbuf, vbuf, vbuf + S::kStages * S::kTile);
+        ok = load_role<D>(pp.a, sh, kbuf, vbuf, vbuf + S::kStages * S::kTile);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (warp == 14) piece_role<D, T>(pp.a, pp.one_each, sh);
-        else if (warp < 12 + S::A) product_role<D>(sh, qbuf, kbuf, vbuf, warp - 12);
+        if (warp == 14) ok = piece_role<D, T>(pp.a, pp.one_each, sh);
+        else if (warp < 12 + S::A) ok = product_role<D>(sh, qbuf, kbuf, vbuf, warp - 12);
     }
+    if (!ok && (threadIdx.x & 31) == 0) report(&g_status, kStatusTimeout);
     fence_before();
     __syncthreads();
     if (warp == 12) {
@@ -1039,6 +1069,17 @@ int launch_prompt(const KvAttend &a, void *workspace, int sms, cudaStream_t st) 
     return rc != DSQ_OK || one_each ? rc : launch_join<D, S::R, T>(a, p.parts, p.carries, grid, jobs, st);
 }
 
+// A wait that nothing ends, through the wait of the roles above.
+__global__ void __launch_bounds__(32) wait_timeout_kernel() {
+    __shared__ uint64_t bar;
+    if (threadIdx.x == 0) {
+        mbar_init(&bar, 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    if (!warp_wait(&bar, 0) && threadIdx.x == 0) report(&g_status, kStatusTimeout);
+}
+
 template <typename T>
 int launch_of(const KvAttend &a, int head_dim, void *workspace, int sms, cudaStream_t st) {
     if (head_dim == 64) return launch_prompt<64, T>(a, workspace, sms, st);
@@ -1056,6 +1097,21 @@ size_t kv_prompt_workspace(int head_dim) {
 int launch_kv_prompt(const KvAttend &a, int head_dim, int dtype, void *workspace, int sms, cudaStream_t st) {
     if (dtype == DSQ_DTYPE_F16) return launch_of<__half>(a, head_dim, workspace, sms, st);
     return launch_of<__nv_bfloat16>(a, head_dim, workspace, sms, st);
+}
+
+int launch_kv_wait_timeout(cudaStream_t st) {
+    wait_timeout_kernel<<<1, 32, 0, st>>>();
+    return cudaGetLastError() == cudaSuccess ? DSQ_OK : DSQ_ERR_CUDA;
+}
+
+int kv_take_status(int *word) {
+    *word = 0;
+    const int zero = 0;
+    if (cudaDeviceSynchronize() == cudaSuccess && cudaMemcpyFromSymbol(word, g_status, sizeof(int)) == cudaSuccess &&
+        (*word == 0 || cudaMemcpyToSymbol(g_status, &zero, sizeof(int)) == cudaSuccess))
+        return DSQ_OK;
+    cudaGetLastError();
+    return DSQ_ERR_CUDA;
 }
 
 }  // namespace dsq

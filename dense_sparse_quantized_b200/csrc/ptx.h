@@ -3,7 +3,8 @@
 //
 // No wait here can spin forever: mbar_wait gives up after kWaitNs of wall
 // time (read from %globaltimer) and returns false, and every caller then
-// records the failure in the handle's status word (dsq_check reports it) and
+// records the failure in the handle's status word (dsq_check reports it; the
+// cache's attention has a word on each device, which dsq_kv_check reports) and
 // abandons the call.
 #pragma once
 #include <stdint.h>

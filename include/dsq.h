@@ -505,12 +505,34 @@ typedef struct {
  * faster, from its rows, its heads and the lengths that its pages allow.  Both
  * deal the batch's work out evenly, so one call may mix long and short
  * sequences.  One launch for few and short ones, else two.
- * Asynchronous; allocates nothing; the same inputs give the same bits.
+ * Asynchronous; allocates nothing; the same inputs give the same bits.  A wait
+ * that runs out inside the kernels is reported by dsq_kv_check.
  * Returns DSQ_OK, DSQ_ERR_INVALID_ARG, DSQ_ERR_UNSUPPORTED,
  * DSQ_ERR_BUFFER_TOO_SMALL or DSQ_ERR_CUDA.
  */
 DSQ_API int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_kv_queries *a, void *workspace,
                           size_t *workspace_bytes, void *stream);
+
+/*
+ * dsq_kv_check -- synchronise CUDA device d->device and report whether a
+ * dsq_kv_attend kernel on it, whichever cache it read, gave up a bounded wait
+ * since the last check (a broken device, never a normal call: a wait that
+ * makes no progress for about 2 s abandons the call and sets a status word).
+ * Returns DSQ_OK, DSQ_ERR_DEVICE (the word was set; it is cleared, and the
+ * outputs of the affected calls are undefined), DSQ_ERR_INVALID_ARG,
+ * DSQ_ERR_UNSUPPORTED or DSQ_ERR_CUDA.  Host-side; blocks until the device is
+ * idle.
+ */
+DSQ_API int dsq_kv_check(const dsq_kv_desc *d);
+
+/*
+ * dsq_kv_selftest_wait_timeout -- test hook for that failure path, as
+ * dsq_selftest_wait_timeout is for the products': launches on `stream` one
+ * small kernel whose wait nothing ends; about 2 s later it gives up, sets the
+ * device's status word and returns, leaving the context usable.  Returns
+ * DSQ_OK (launched), DSQ_ERR_INVALID_ARG, DSQ_ERR_UNSUPPORTED or DSQ_ERR_CUDA.
+ */
+DSQ_API int dsq_kv_selftest_wait_timeout(const dsq_kv_desc *d, void *stream);
 
 /* Static, never-NULL text for a status code. */
 DSQ_API const char *dsq_status_string(int status);

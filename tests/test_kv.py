@@ -754,3 +754,33 @@ def test_a_failed_call_is_its_own_failure():
         kv.desc.device = 0
         dsq.decompose(w, 4, "affine", 8)
         call()
+
+
+def test_check_refusals():
+    for desc, rc in (((0, 0, 128, 64, 4), BAD), ((-1, 8, 128, 64, 4), BAD), ((0, 8, 96, 64, 4), UNS)):
+        d = dsq.KVDesc(*desc)
+        assert _status("dsq_kv_check", ctypes.byref(d)) == rc
+        assert _status("dsq_kv_selftest_wait_timeout", ctypes.byref(d), None) == rc
+    assert _status("dsq_kv_check", None) == BAD and _status("dsq_kv_selftest_wait_timeout", None, None) == BAD
+
+
+@pytest.mark.gpu
+def test_a_wait_that_runs_out_is_reported_once():
+    """The attention kernels' bounded wait gives up and returns; check() reports it
+    once and clears it, on every cache of the device, and the next call works."""
+    kv, seqs, q, table, kv_lens, start = _problem(940, [700], [260], 1, 8, 64, 16, F16)
+    other = dsq.KVCache(1, 128, 1, 16)
+    kv.attend(q.cuda(), table, kv_lens)
+    kv.check()
+    kv.selftest_wait_timeout()
+    with pytest.raises(dsq.DSQError) as e:
+        other.check()
+    assert e.value.status == dsq.DSQ_ERR_DEVICE
+    kv.check()
+    side = torch.cuda.Stream()
+    kv.selftest_wait_timeout(stream=side)
+    out, lse = kv.attend(q.cuda(), table, kv_lens, return_lse=True)
+    with pytest.raises(dsq.DSQError):
+        kv.check()
+    _check(out, lse, q, seqs, [700], start, F16)
+    kv.check()
