@@ -6,7 +6,14 @@
 namespace dsq {
 
 constexpr float kNoMax = -3.0e38f;  // a maximum of no scores: finite, so that -inf minus it stays -inf
-constexpr float kLazy = 8.0f;       // log2 of how far numerators may pass 1
+// Numerators are rounded to fp16, which has them down to 2^-25: a running
+// maximum is held kLift below the largest score, so that numerators are 2^7 at
+// it and small ones that far from the end of the range (2^-32 of the largest;
+// 2^20 tokens at 2^-25.2 beside one that attracts a row lost 2.6 % of its
+// output without).  kLazy: log2 of how far they may pass 2^7; 2^15 is fp16's
+// last power.
+constexpr float kLift = 7.0f;
+constexpr float kLazy = 8.0f;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kMaxCtas = 160;  // workspace slots; the kernels run one CTA per SM, at most this many
 

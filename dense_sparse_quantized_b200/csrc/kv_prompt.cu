@@ -840,8 +840,8 @@ __device__ __forceinline__ bool softmax_role(const PromptParams &pp, Shared &sh,
 #pragma unroll
                     for (int k = 0; k < 4; k++) top[k] = max3(top[k], s[32 * k + i], s[32 * k + i + 1]);
                 const float x = max3(max3(top[0], top[1], top[2]), max3(top[3], s[31], s[63]), fmaxf(s[95], s[127])) * f;
-                if (__any_sync(kFull, x > m + kLazy)) {
-                    const float next = fmaxf(m, x), keep = ex2(m - next);
+                if (__any_sync(kFull, x > m + (kLift + kLazy))) {
+                    const float next = fmaxf(m, x - kLift), keep = ex2(m - next);
                     m = next;
                     l *= keep;
                     if (t > mine.x) {

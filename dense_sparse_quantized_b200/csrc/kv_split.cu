@@ -31,8 +31,8 @@
 // movmatrix, is the B operand of the second product, out^T = V^T P^T.
 //
 // The running maximum is raised only when some score exceeds it by more than
-// 2^8 in the numerator (one vote a unit); until then numerators up to 256 are
-// as exact as ones up to 1.
+// 2^8 in the numerator (one vote a unit); until then numerators up to 2^15 are
+// as exact as ones up to 2^7, which they are at the maximum (kLift).
 //
 // Measured on one B200: four sequences of 100000 to 131072 tokens, 64 query
 // heads on 8 kv heads of 128, 558 MB of cache, take 129 us, 4.3 TB/s (0.66 of a
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
 #pragma unroll
                 for (int c = 0; c < 2; c++) {
                     top[n][c] = scale[n][c] * fmaxf(fmaxf(s[0][n][c], s[0][n][2 + c]), fmaxf(s[1][n][c], s[1][n][2 + c]));
-                    raise |= top[n][c] > m[n][c] + kLazy;
+                    raise |= top[n][c] > m[n][c] + (kLift + kLazy);
                 }
             if (__any_sync(kFull, raise)) {
 #pragma unroll
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
                         x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-                        x = fmaxf(x, m[n][c]);
+                        x = fmaxf(x - kLift, m[n][c]);
                         const float keep = ex2(m[n][c] - x);
                         m[n][c] = x;
                         l[n][c] *= keep;

@@ -499,7 +499,9 @@ typedef struct {
  * table_pages * page_tokens], row numbers to [0, q_tokens]; tokens on a page
  * outside [0, pages) are not seen.
  * Scores, maxima, sums and outputs are accumulated in fp32; the softmax's
- * numerators are rounded to fp16 before they multiply V (K and V are exact).
+ * numerators are rounded to fp16 before they multiply V (K and V are exact): by
+ * half a step, 2^-11 of themselves, or 2^-32 of the largest so far where that
+ * is more.
  * Two kernels, one of warp-level matrix instructions for few rows per kv head
  * and a tcgen05 one for many; a call takes the one that is estimated to be
  * faster, from its rows, its heads and the lengths that its pages allow.  Both

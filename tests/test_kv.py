@@ -784,3 +784,36 @@ def test_a_wait_that_runs_out_is_reported_once():
         kv.check()
     _check(out, lse, q, seqs, [700], start, F16)
     kv.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d,new,share,n", [(64, 1, 1, 333), (128, 1, 8, 333), (256, 1, 2, 500), (128, 5, 4, 333), (64, 5, 5, 40),
+                                           (64, 300, 4, 300), (128, 300, 4, 301), (256, 400, 2, 400), (128, 900, 8, 3000)])
+def test_attend_tokens_far_below_the_largest(d, new, share, n, dtype):
+    """Every 16th token attracts the row and has the value 0; the others, at 2^-25.3
+    of it, are the whole output.  Numerators in fp16 are within 2^-11 of
+    themselves or 2^-32 of the largest."""
+    h, page = 2, 64
+    q0 = torch.tensor(25.3 * np.log(2) / 15 * 8).to(dtype)
+    attracts = (torch.arange(n) % 16 == 0)[:, None, None]
+    k, v = torch.zeros(n, h, d), torch.where(attracts, 0.0, 30720.0).expand(n, h, d)
+    k[..., 0] = torch.where(attracts[..., 0], 15.0, 0.0)
+    pages = -(-n // page)
+    kv = dsq.KVCache(h, d, pages, page)
+    kv.append(k.half().cuda(), v.half().contiguous().cuda(), torch.arange(n, device="cuda"))
+    q = torch.zeros(new, h * share, d, dtype=dtype)
+    q[..., 0] = q0
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    out, lse = kv.attend(q.cuda(), table, torch.tensor([n], dtype=torch.int32, device="cuda"), scale=0.125, return_lse=True)
+    pos = n - new + np.arange(new)
+    few = n if new == 1 else 64  # rows are alike: some of them
+    rows = np.unique(np.linspace(0, new - 1, few).astype(int))
+    want, want_lse, P = okv.attend(q[rows].double().numpy(), k.double().numpy(), v.double().numpy(), 0.125, pos[rows])
+    ds = (d + 8) * 2.0 ** -23 * 0.125 * float(q0) * 15
+    each = (pos[rows] + 1) / (pos[rows] // 16 + 1)  # tokens seen to one that attracts: their errors' sum over the numerators'
+    tol = (2 * (ds + 2.0 ** -20) + 2.0 ** -11) * P + (each * 2.0 ** -32 * 30720)[:, None, None] + EPS[dtype] * np.abs(want) + 2.0 ** -25
+    err = np.abs(out.double().cpu().numpy()[rows] - want)
+    assert np.all(err <= tol), (float((err / tol).max()), float((err / np.maximum(np.abs(want), 1e-30)).max()))
+    off = np.abs(lse.double().cpu().numpy()[rows] - want_lse)
+    assert np.all(off <= ds + 2.0 ** -20 + 2.0 ** -22 * np.abs(want_lse))
