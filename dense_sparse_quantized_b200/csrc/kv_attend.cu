@@ -70,7 +70,8 @@ extern "C" int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_
         return a->dtype == DSQ_DTYPE_F32 ? DSQ_ERR_UNSUPPORTED : DSQ_ERR_INVALID_ARG;
     if (!a->q_start && (a->batch == 0 ? a->q_tokens > 0 : a->q_tokens % a->batch != 0)) return DSQ_ERR_INVALID_ARG;
     if ((int64_t)a->table_pages * d->page_tokens >= ((int64_t)1 << 30) ||
-        a->q_tokens >= ((int64_t)1 << 30) / a->q_heads)  // token and row numbers are ints, with room to round up
+        a->q_tokens >= ((int64_t)1 << 30) / a->q_heads ||  // token and row numbers are ints, with room to round up
+        (int64_t)a->batch * d->kv_heads >= ((int64_t)1 << 29))  // and so are job numbers (launch_split's shift)
         return DSQ_ERR_UNSUPPORTED;
     // by the queries' shape alone, so that one workspace does for any lengths
     const size_t need = rows_of(d, a) <= 8 ? kv_split_workspace() : std::max(kv_split_workspace(), kv_prompt_workspace(d->head_dim));

@@ -675,7 +675,7 @@ int launch_split(const KvAttend &a, void *workspace, int sms, cudaStream_t st) {
     int64_t tokens = (int64_t)a.table_pages * a.c.page_tokens;
     if (a.window) tokens = std::min(tokens, a.window + most_rows);
     const bool one_each = jobs <= sms && tokens / 32 + 2 <= 6 * S::NW;
-    int shift = 0;
+    int shift = 0;  // 25 at most: fewer than 2^30 tokens, and jobs
     while ((double)a.c.kv_heads * (a.batch + (double)a.q_tokens * a.share / S::R) * ((a.most_tokens >> (5 + shift)) + 2) >= 2147483648.0)
         shift++;
     const SplitParams p = {a, (float *)workspace, kv_carries<S::D, S::R>(workspace), one_each ? 0 : 4, shift};

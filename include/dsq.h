@@ -468,7 +468,7 @@ typedef struct {
     int64_t q_tokens;   /* rows of q, out and lse; times q_heads, below 2^30 */
     int32_t dtype;      /* DSQ_DTYPE_F16 or DSQ_DTYPE_BF16 */
     int32_t q_heads;    /* a multiple of kv_heads */
-    int32_t batch;
+    int32_t batch;      /* times kv_heads, below 2^29 */
     int32_t table_pages; /* columns of page_table; times page_tokens, below 2^30 */
     int32_t causal;     /* 1: a query at position p sees tokens 0 .. p; 0: all tokens of its sequence */
     int32_t window;     /* > 0 (with causal): only the last `window` of those; 0: no limit */

@@ -817,3 +817,14 @@ def test_attend_tokens_far_below_the_largest(d, new, share, n, dtype):
     assert np.all(err <= tol), (float((err / tol).max()), float((err / np.maximum(np.abs(want), 1e-30)).max()))
     off = np.abs(lse.double().cpu().numpy()[rows] - want_lse)
     assert np.all(off <= ds + 2.0 ** -20 + 2.0 ** -22 * np.abs(want_lse))
+
+
+@pytest.mark.parametrize("change,rc", [
+    (dict(batch=1 << 30), UNS), (dict(batch=1 << 26), UNS), (dict(batch=(1 << 31) - 1, q_heads=8), UNS),
+    (dict(batch=(1 << 26) - 1, out=None), BAD)])   # the last is refused for its outputs alone
+def test_attend_refuses_more_jobs_than_it_can_number(change, rc):
+    """Sequences times kv heads from 2^29 on: the choice of the units' size had no end."""
+    d = dsq.KVDesc(0, 8, 128, 64, 4)
+    size = ctypes.c_size_t(1 << 40)
+    a = dsq.KVQueries(**{**GOOD_Q, "q_start": 1 << 18, **change})
+    assert _status("dsq_kv_attend", ctypes.byref(d), 1 << 20, ctypes.byref(a), 1 << 24, ctypes.byref(size), None) == rc
