@@ -189,6 +189,9 @@ __device__ __forceinline__ void find_run(const SplitParams &p, Run &run) {
             const int l = __ffs(past) - 1;
             b = b0 + l;
             before += __shfl_sync(kFull, sum - w, l);
+            // A q_start out of order can have more units than 31 bits count:
+            // no place in the sequence is taken that is not in it.
+            if (a.q_start && (uint32_t)first - (uint32_t)before >= (uint32_t)__shfl_sync(kFull, w, l)) b = a.batch;
             break;
         }
         before += __shfl_sync(kFull, sum, 31);
@@ -248,8 +251,8 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
     const int u_end = u + min(mine, run.size - skip);
     while (u < u_end && b < a.batch) {
         const Jobs j = jobs_of<R>(a, b, p.shift);
-        if (u >= before + j.weight) {
-            before += j.weight;
+        if ((uint32_t)u - (uint32_t)before >= (uint32_t)j.weight) {
+            before = (int)((uint32_t)before + (uint32_t)j.weight);
             b++;
             continue;
         }
@@ -620,7 +623,8 @@ __global__ void __launch_bounds__(S::NW * 32, 1) split_kernel(const __grid_const
             head = job_id[w][1];
             rho0 = job_id[w][2] * R;
         } else if (w >= 0 && warp % group == 0 && lane == 0) {
-            const KvCarry mt = {1, (int)((uint32_t)(job_end[w] - 1) / (uint32_t)run.of) - (int)blockIdx.x, job_id[w][0], job_id[w][1], job_id[w][2], {}};
+            const uint32_t last = min((uint32_t)(job_end[w] - 1) / (uint32_t)run.of, gridDim.x - 1);  // of a q_start out of order it may be anything
+            const KvCarry mt = {1, (int)last - (int)blockIdx.x, job_id[w][0], job_id[w][1], job_id[w][2], {}};
             p.carries[blockIdx.x] = mt;
         }
         // Accumulators 4 i0 .. 4 i0 + 3 of row group nc at a time: they share

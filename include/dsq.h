@@ -497,7 +497,8 @@ typedef struct {
  * result, NaN included.  A NaN that a query sees makes its lse NaN when it is a
  * key's (a value's may), and NaN of elements of its out.  Lengths are clamped to [0,
  * table_pages * page_tokens], row numbers to [0, q_tokens]; tokens on a page
- * outside [0, pages) are not seen.
+ * outside [0, pages) are not seen.  With a q_start out of order the outputs are
+ * undefined; no other memory is touched.
  * Scores, maxima, sums and outputs are accumulated in fp32; the softmax's
  * numerators are rounded to fp16 before they multiply V (K and V are exact): by
  * half a step, 2^-11 of themselves, or 2^-32 of the largest so far where that

@@ -828,3 +828,31 @@ def test_attend_refuses_more_jobs_than_it_can_number(change, rc):
     size = ctypes.c_size_t(1 << 40)
     a = dsq.KVQueries(**{**GOOD_Q, "q_start": 1 << 18, **change})
     assert _status("dsq_kv_attend", ctypes.byref(d), 1 << 20, ctypes.byref(a), 1 << 24, ctypes.byref(size), None) == rc
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch,new,n,window", [
+    (6, 40, 200, 0), (6, 300, 400, 0),
+    (2896, 8, 23168, 1)])   # 1448 sequences of 23168 rows: 3e9 units of work, more than 31 bits count
+def test_attend_row_numbers_out_of_order_touch_nothing_else(batch, new, n, window):
+    """q_start 0, N, 0, N, ...: every other sequence has all rows.  What lies around
+    the outputs stays as it is, and the next call is right."""
+    d, page, rows = 64, 64, batch * new
+    rng = np.random.default_rng(batch)
+    pages = -(-n // page)
+    kv = dsq.KVCache(1, d, pages, page)
+    k, v = _rows(rng, n, 1, d).half().cuda(), _rows(rng, n, 1, d).half().cuda()
+    kv.append(k, v, torch.arange(n, device="cuda"))
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(batch, pages).contiguous()
+    lens = torch.full((batch,), n, dtype=torch.int32, device="cuda")
+    start = torch.tensor([0, rows] * (batch // 2) + [0], dtype=torch.int32, device="cuda")
+    q = torch.from_numpy(rng.standard_normal((rows, 1, d))).half().cuda()
+    around, lse = torch.full((rows + 2048, 1, d), 3.0, dtype=F16, device="cuda"), torch.full((rows + 2048, 1), 5.0, device="cuda")
+    work = torch.full((kv.attend_workspace(rows, 1, batch).numel() + 8192,), 0xAB, dtype=torch.uint8, device="cuda")
+    kv.attend(q, table, lens, q_start=start, window=window, out=around[1024:-1024], lse=lse[1024:-1024], workspace=work[:-8192])
+    for t, fill in ((around, 3.0), (lse, 5.0)):
+        assert (t[:1024] == fill).all() and (t[-1024:] == fill).all()
+    assert (work[-8192:] == 0xAB).all()
+    few = min(rows, 300)
+    out, lse = kv.attend(q[:few], table[:1], lens[:1], window=window, return_lse=True)
+    _check(out, lse, q[:few].cpu(), [(_held(k), _held(v))], [n], [0, few], F16, window=window)
