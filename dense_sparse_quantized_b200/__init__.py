@@ -59,6 +59,14 @@ class KVDesc(ctypes.Structure):
                 ("page_tokens", ctypes.c_int32), ("pages", ctypes.c_int32)]
 
 
+def _kv_desc(*values) -> KVDesc:
+    # ctypes takes a number's low 32 bits
+    values = tuple(int(v) for v in values)
+    if not all(-1 << 31 <= v < 1 << 31 for v in values):
+        raise ValueError(f"device, kv_heads, head_dim, page_tokens and pages must fit 32 bits: {values}")
+    return KVDesc(*values)
+
+
 class KVRows(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_token", ctypes.c_int64),
                 ("k_head", ctypes.c_int64), ("v_token", ctypes.c_int64), ("v_head", ctypes.c_int64),
@@ -391,7 +399,7 @@ class KVCache:
             if data.dtype != torch.uint8 or not data.is_cuda or not data.is_contiguous():
                 raise ValueError("data must be a contiguous cuda uint8 tensor")
             device = data.device.index
-        self.desc = KVDesc(int(device), int(kv_heads), int(head_dim), int(page_tokens), int(pages))
+        self.desc = _kv_desc(device, kv_heads, head_dim, page_tokens, pages)
         size = self.bytes_for(kv_heads, head_dim, pages, page_tokens)
         if data is None:
             data = torch.zeros(size, dtype=torch.uint8, device=f"cuda:{int(device)}")
@@ -411,7 +419,7 @@ class KVCache:
     def bytes_for(kv_heads: int, head_dim: int, pages: int, page_tokens: int = 64) -> int:
         """Bytes of a cache of that shape (dsq_kv_bytes)."""
         size = ctypes.c_size_t(0)
-        d = KVDesc(0, int(kv_heads), int(head_dim), int(page_tokens), int(pages))
+        d = _kv_desc(0, kv_heads, head_dim, page_tokens, pages)
         _check(library().dsq_kv_bytes(ctypes.byref(d), ctypes.byref(size)), "dsq_kv_bytes")
         return size.value
 
@@ -483,6 +491,8 @@ class KVCache:
         """Scratch for attend() calls of these sizes that follow one another;
         calls that may overlap need one each."""
         size = ctypes.c_size_t(0)
+        if not (-1 << 31 <= q_heads < 1 << 31 and -1 << 31 <= batch < 1 << 31 and -1 << 63 <= q_tokens < 1 << 63):
+            raise ValueError("q_heads and batch must fit 32 bits, q_tokens 64")
         # the size is asked for with a q_start, which a query of it does not read:
         # any number of rows may be any number of sequences'
         a = KVQueries(q_tokens=int(q_tokens), q_heads=int(q_heads), batch=int(batch), q_start=self._data or 256)
@@ -535,6 +545,8 @@ class KVCache:
             workspace = self.attend_workspace(n, heads, batch, stream)
         elif workspace.get_device() != self._index or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        if not 0 <= window < 1 << 31:  # ctypes would take its low 32 bits; one past every position is none
+            window = -1 if window < 0 else (1 << 31) - 1
         a = KVQueries(q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), qs[0], qs[1], os[0], os[1],
                       n, dtype, heads, batch, columns, causal, window,
                       self.head_dim ** -0.5 if scale is None else scale, page_table.data_ptr(), kv_lens.data_ptr(),

@@ -856,3 +856,30 @@ def test_attend_row_numbers_out_of_order_touch_nothing_else(batch, new, n, windo
     few = min(rows, 300)
     out, lse = kv.attend(q[:few], table[:1], lens[:1], window=window, return_lse=True)
     _check(out, lse, q[:few].cpu(), [(_held(k), _held(v))], [n], [0, few], F16, window=window)
+
+
+@pytest.mark.parametrize("shape", [((1 << 32) + 1, 64, 4, 16), (1, (1 << 32) + 64, 4, 16), (1, 64, 1 << 32, 16),
+                                   (1, 64, 4, (1 << 32) + 16), (1, 64, -(1 << 33), 16)])
+def test_binding_refuses_sizes_past_32_bits(shape):
+    """The bytes of the sizes' low 32 bits were returned."""
+    with pytest.raises(ValueError):
+        dsq.KVCache.bytes_for(*shape)
+    with pytest.raises(ValueError):
+        dsq.KVCache(*shape)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [1, 300])
+def test_binding_takes_windows_past_32_bits_as_none(new):
+    kv, seqs, q, table, kv_lens, start = _problem(960 + new, [600], [new], 1, 3, 64, 16, F16)
+    q = q.cuda()
+    want = kv.attend(q, table, kv_lens)
+    for window in (1 << 31, (1 << 32) + 1, 1 << 32, (1 << 64) + 5):
+        assert torch.equal(kv.attend(q, table, kv_lens, window=window), want)
+    for window in (-1, -(1 << 32), 3 - (1 << 32)):
+        with pytest.raises(dsq.DSQError) as e:
+            kv.attend(q, table, kv_lens, window=window)
+        assert e.value.status == BAD
+    for sizes in ((q.shape[0], 3, 1 << 32), (q.shape[0], (1 << 32) + 3, 1), (1 << 64, 3, 1)):
+        with pytest.raises(ValueError):
+            kv.attend_workspace(*sizes)
