@@ -39,7 +39,7 @@ DTYPE_F32 = 2
 EXPORTS = ("dsq_pack", "dsq_pack_two_axis", "dsq_pack_intgrid", "dsq_blob_desc", "dsq_create", "dsq_gemv", "dsq_gemv_launches", "dsq_decode",
            "dsq_handle_desc", "dsq_device_bytes", "dsq_check", "dsq_destroy", "dsq_status_string",
            "dsq_gemv_noalloc", "dsq_selftest_wait_timeout", "dsq_decompose",
-           "dsq_kv_bytes", "dsq_kv_append", "dsq_kv_read", "dsq_kv_attend",
+           "dsq_kv_bytes", "dsq_kv_append", "dsq_kv_read", "dsq_kv_attend", "dsq_kv_attend_kernel",
            "dsq_kv_check", "dsq_kv_selftest_wait_timeout")
 
 
@@ -116,6 +116,7 @@ def library() -> ctypes.CDLL:
         lib.dsq_kv_read.argtypes = [ctypes.POINTER(KVDesc), P, ctypes.POINTER(KVRows), P, ctypes.c_int64, P]
         lib.dsq_kv_attend.argtypes = [ctypes.POINTER(KVDesc), P, ctypes.POINTER(KVQueries), P,
                                       ctypes.POINTER(SZ), P]
+        lib.dsq_kv_attend_kernel.argtypes = [ctypes.POINTER(KVDesc), ctypes.POINTER(KVQueries)]
         lib.dsq_kv_check.argtypes = [ctypes.POINTER(KVDesc)]
         lib.dsq_kv_selftest_wait_timeout.argtypes = [ctypes.POINTER(KVDesc), P]
         lib.dsq_status_string.argtypes = [I]
@@ -557,6 +558,17 @@ class KVCache:
         if rc:
             _check(rc, "dsq_kv_attend")
         return out if lse is None else (out, lse)
+
+    def attend_kernel(self, q_tokens: int, q_heads: int, batch: int, table_pages: int, ragged=False, causal=True,
+                      window=0) -> str:
+        """The kernel that attend() calls of these sizes take, "few_rows" or
+        "many_rows" (dsq_kv_attend_kernel).  ragged: with a q_start."""
+        a = KVQueries(q_tokens=q_tokens, q_heads=q_heads, batch=batch, table_pages=table_pages, causal=causal,
+                      window=window, q_start=256 if ragged else None)
+        which = self._lib.dsq_kv_attend_kernel(self._d, ctypes.byref(a))
+        if which < 0:
+            _check(which, "dsq_kv_attend_kernel")
+        return ("few_rows", "many_rows")[which]
 
     def check(self):
         """Synchronise the device; raise if a kernel of an attend() on it, of any

@@ -56,13 +56,11 @@ bool many_rows(const dsq_kv_desc *d, const dsq_kv_queries *a) {
     return many < few;
 }
 
-}  // namespace
-
-extern "C" int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_kv_queries *a, void *workspace,
-                             size_t *workspace_bytes, void *stream) {
-    int rc = kv_check_desc(d);
+// Whether the shape of a call is one there is: what does not need its pointers.
+int check_shape(const dsq_kv_desc *d, const dsq_kv_queries *a) {
+    const int rc = kv_check_desc(d);
     if (rc != DSQ_OK) return rc;
-    if (!a || !workspace_bytes) return DSQ_ERR_INVALID_ARG;
+    if (!a) return DSQ_ERR_INVALID_ARG;
     if (a->q_heads < 1 || a->q_heads % d->kv_heads || a->batch < 0 || a->q_tokens < 0 || a->table_pages < 0 ||
         a->window < 0 || (a->window > 0 && !a->causal) || !isfinite(a->scale * kLog2e))
         return DSQ_ERR_INVALID_ARG;
@@ -73,6 +71,21 @@ extern "C" int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_
         a->q_tokens >= ((int64_t)1 << 30) / a->q_heads ||  // token and row numbers are ints, with room to round up
         (int64_t)a->batch * d->kv_heads >= ((int64_t)1 << 29))  // and so are job numbers (launch_split's shift)
         return DSQ_ERR_UNSUPPORTED;
+    return DSQ_OK;
+}
+
+}  // namespace
+
+extern "C" int dsq_kv_attend_kernel(const dsq_kv_desc *d, const dsq_kv_queries *a) {
+    const int rc = check_shape(d, a);
+    return rc != DSQ_OK ? rc : many_rows(d, a) ? 1 : 0;
+}
+
+extern "C" int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_kv_queries *a, void *workspace,
+                             size_t *workspace_bytes, void *stream) {
+    const int rc = check_shape(d, a);
+    if (rc != DSQ_OK) return rc;
+    if (!workspace_bytes) return DSQ_ERR_INVALID_ARG;
     // by the queries' shape alone, so that one workspace does for any lengths
     const size_t need = rows_of(d, a) <= 8 ? kv_split_workspace() : std::max(kv_split_workspace(), kv_prompt_workspace(d->head_dim));
     if (!workspace || *workspace_bytes < need) {

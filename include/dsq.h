@@ -517,6 +517,14 @@ DSQ_API int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_kv_
                           size_t *workspace_bytes, void *stream);
 
 /*
+ * dsq_kv_attend_kernel -- which kernel such a call takes: 0, the one for few
+ * rows; 1, the one for many.  Host-only; of `a` it reads the numbers and
+ * whether q_start is NULL.  Returns that, or DSQ_ERR_INVALID_ARG or
+ * DSQ_ERR_UNSUPPORTED as dsq_kv_attend would.
+ */
+DSQ_API int dsq_kv_attend_kernel(const dsq_kv_desc *d, const dsq_kv_queries *a);
+
+/*
  * dsq_kv_check -- synchronise CUDA device d->device and report whether a
  * dsq_kv_attend kernel on it, whichever cache it read, gave up a bounded wait
  * since the last check (a broken device, never a normal call: a wait that

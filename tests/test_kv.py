@@ -883,3 +883,288 @@ def test_binding_takes_windows_past_32_bits_as_none(new):
     for sizes in ((q.shape[0], 3, 1 << 32), (q.shape[0], (1 << 32) + 3, 1), (1 << 64, 3, 1)):
         with pytest.raises(ValueError):
             kv.attend_workspace(*sizes)
+
+
+# ------------------------------------------------- each kernel by its own shapes
+#
+# Which kernel a shape takes follows from estimates of times; the tests below
+# state the one that they are for, so that no change of those moves them.
+
+def test_kernel_query_refuses_what_attend_refuses():
+    d = dsq.KVDesc(0, 8, 128, 64, 4)
+    ask = lambda d, a: _status("dsq_kv_attend_kernel", d and ctypes.byref(d), a and ctypes.byref(a))  # noqa: E731
+    assert ask(d, dsq.KVQueries(**GOOD_Q)) in (0, 1)
+    for change, rc in ((dict(q_heads=12), BAD), (dict(batch=-1), BAD), (dict(q_tokens=7), BAD), (dict(dtype=2), UNS),
+                       (dict(window=4, causal=0), BAD), (dict(table_pages=1 << 24), UNS), (dict(q_tokens=3 << 28), UNS)):
+        assert ask(d, dsq.KVQueries(**{**GOOD_Q, **change})) == rc
+    assert ask(None, dsq.KVQueries(**GOOD_Q)) == BAD and ask(d, None) == BAD
+    assert ask(dsq.KVDesc(0, 8, 96, 64, 4), dsq.KVQueries(**GOOD_Q)) == UNS
+
+
+def _takes(kv, q, table, ragged=True, **how):
+    return kv.attend_kernel(q.shape[0], q.shape[1], table.shape[0], table.shape[1], ragged, **how)
+
+
+def _check_each(out, lse, q, seqs, lens, start, dtype, causal=True, window=0, scale=None, keep=None):
+    """Against attention in 64 bits, worked out on the GPU; the bounds of this file
+    with the numerators' 2^-32.  keep: by sequence, the tokens that are there."""
+    d = q.shape[-1]
+    scale = d ** -0.5 if scale is None else scale
+    for b, (k, v) in enumerate(seqs):
+        r0, r1, n = int(start[b]), int(start[b + 1]), int(lens[b])
+        if r1 == r0:
+            continue
+        if n == 0:
+            assert not out[r0:r1].any() and (lse is None or torch.isneginf(lse[r0:r1]).all())
+            continue
+        k, v = (torch.from_numpy(np.ascontiguousarray(x)).cuda() for x in (k, v))
+        t = torch.arange(n, device="cuda")
+        pos = n - (r1 - r0) + torch.arange(r1 - r0, device="cuda")[:, None]
+        seen = (t <= pos) if causal else (t >= 0).expand(r1 - r0, n)
+        if window:
+            seen = seen & (t > pos - window)
+        if keep is not None and keep[b] is not None:
+            seen = seen & torch.from_numpy(keep[b]).cuda()
+        none = ~seen.any(-1)
+        share = q.shape[1] // k.shape[1]
+        for h in range(q.shape[1]):
+            x, kh, vh = q[r0:r1, h].double().cuda(), k[:, h // share], v[:, h // share]
+            y = (x @ kh.T * scale).masked_fill(~seen, -torch.inf)
+            total = torch.logsumexp(y, -1)
+            p = torch.where(seen, torch.exp(y - total[:, None]), 0.0)
+            want, P = p @ vh, p @ vh.abs()
+            ds = (d + 8) * 2.0 ** -23 * (x.abs() @ kh.abs().T * abs(scale)).amax(-1)
+            tol = (2 * (ds + 2.0 ** -20) + 2.0 ** -11)[:, None] * P + (n * 2.0 ** -32 * vh.abs().max()
+                                                                      + EPS[dtype] * want.abs() + 2.0 ** -25)
+            err = (out[r0:r1, h].double() - want).abs()
+            assert bool((err <= tol).all()), (b, h, float((err / tol).max()))
+            assert not out[r0:r1, h][none].any()
+            if lse is not None:
+                got = lse[r0:r1, h].double()
+                assert torch.equal(torch.isneginf(got), none), (b, h)
+                off = (got - total)[~none].abs()
+                assert bool((off <= (ds + 2.0 ** -20 + 2.0 ** -22 * total.abs())[~none]).all()), (b, h, float(off.max()))
+
+
+MANY = {  # lens, new rows, kv heads, share, page; for kv_prompt.cu at every head_dim
+    "short": ([500, 130, 0, 77, 340], [500, 130, 0, 90, 340], 2, 8, 16),      # a job a CTA; rows that see nothing
+    "dealt": ([1900, 700, 0, 1300], [1000, 300, 0, 1300], 3, 4, 64),          # dealt out, joined
+    "nine": ([150 * i for i in range(9)], [130 * i for i in range(9)], 2, 4, 32),   # eight sequences and more
+    "forty": ([37 * i % 900 for i in range(40)], [min(37 * i % 900, 53 * i % 400) for i in range(40)], 2, 8, 16),
+    "halves": ([600, 500, 129, 590, 124, 60, 431, 600], [100, 120, 128, 1, 77, 60, 100, 100], 16, 1, 16),  # up to 128 rows a job
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("name", MANY)
+def test_many_rows_causal_all_tokens_and_windows(name, d, dtype):
+    lens, new, h, share, page = MANY[name]
+    kv, seqs, q, table, kv_lens, start = _problem(1000 + d, lens, new, h, share, d, page, dtype)
+    x, qs = q.cuda(), torch.from_numpy(start).cuda()
+    for how in (dict(), dict(causal=False), dict(window=1), dict(window=100), dict(window=450)):
+        assert _takes(kv, q, table, **how) == "many_rows"
+        out, lse = kv.attend(x, table, kv_lens, q_start=qs, return_lse=True, **how)
+        _check_each(out, lse, q, seqs, lens, start, dtype, **how)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("name", ["short", "dealt", "halves"])
+def test_many_rows_scales_and_values(name, d):
+    """Scales of zero and below, tokens of very different sizes, rows that pick out
+    one token, bf16 rows that fp16 could not hold."""
+    lens, new, h, share, page = MANY[name]
+    sizes = [1.0] * 64 + [0.003] * 40 + [50.0] * 7 + [2e-6]
+    kv, seqs, q, table, kv_lens, start = _problem(1100 + d, lens, new, h, share, d, page, F16, sizes=sizes)
+    qs = torch.from_numpy(start).cuda()
+    assert _takes(kv, q, table) == "many_rows"
+    for scale in (0.0, -0.3, 0.01):
+        out, lse = kv.attend(q.cuda(), table, kv_lens, q_start=qs, scale=scale, return_lse=True)
+        _check_each(out, lse, q, seqs, lens, start, F16, scale=scale)
+    kv, seqs, q, table, kv_lens, start = _problem(1110 + d, lens, new, h, share, d, page, F16)
+    x = q.clone()
+    x[::2] *= 40
+    x[1::2] *= 1e-4
+    out, lse = kv.attend(x.cuda(), table, kv_lens, q_start=qs, return_lse=True)
+    _check_each(out, lse, x, seqs, lens, start, F16)
+    for factor in (1e-12, 1e10):
+        x, scale = (q.double() * factor).to(BF16), float(d ** -0.5 / factor)
+        out, lse = kv.attend(x.cuda(), table, kv_lens, q_start=qs, scale=scale, return_lse=True)
+        _check_each(out, lse, x, seqs, lens, start, BF16, scale=scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("name", ["short", "dealt", "halves"])
+def test_many_rows_pages_that_are_not_there(name, d):
+    """Page numbers outside the cache, in the middle of sequences; rows behind the last one."""
+    lens, new, h, share, page = MANY[name]
+    kv, seqs, q, table, kv_lens, start = _problem(1200 + d, lens, new, h, share, d, page, F16)
+    keep = [None] * len(lens)
+    for b, cols, bad in ((0, (0, 3, 7), kv.pages), (1, (2,), -5), (3, (0, 1), 1 << 30)):
+        keep[b] = np.ones(lens[b], bool)
+        for c in cols:
+            table[b, c] = bad
+            keep[b][c * page:(c + 1) * page] = False
+    more = torch.zeros(q.shape[0] + 5, *q.shape[1:], dtype=F16)
+    more[:-5] = q
+    for how in (dict(), dict(causal=False), dict(window=60)):
+        assert _takes(kv, more, table, **how) == "many_rows"
+        out, lse = torch.full_like(more, 3.0).cuda(), torch.full(more.shape[:2], 5.0, device="cuda")
+        kv.attend(more.cuda(), table, kv_lens, q_start=torch.from_numpy(start).cuda(), out=out, lse=lse, **how)
+        _check_each(out, lse, q, seqs, lens, start, F16, keep=keep, **how)
+        assert (out[-5:] == 3.0).all() and (lse[-5:] == 5.0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window", [0, 70])
+@pytest.mark.parametrize("n,new,h,share", [(900, 700, 4, 8), (400, 400, 2, 8), (400, 100, 64, 1)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_many_rows_nan_stays_where_it_is_seen(d, n, new, h, share, window):
+    """A NaN key or value reaches the rows that see its token and no other, bit for bit."""
+    kv, seqs, q, table, kv_lens, start = _problem(1300 + d + n, [n], [new], h, share, d, 64, F16)
+    q = q.cuda()
+    assert _takes(kv, q, table, ragged=False, window=window) == "many_rows"
+    clean, clean_lse = kv.attend(q, table, kv_lens, window=window, return_lse=True)
+    pos = n - new + torch.arange(new, device="cuda")
+    for at in (n - new + new // 2, n - new // 3 - 16):
+        seen = (pos >= at) & ((pos < at + window) if window else (pos >= 0))
+        for which in (0, 1):
+            kv2 = dsq.KVCache(h, d, kv.pages, 64, data=kv.data.clone())
+            k, v = (torch.from_numpy(x[at:at + 1]).half().cuda() for x in seqs[0])
+            (k, v)[which][0, :, 40] = float("nan")
+            kv2.append(k, v, torch.tensor([int(table[0, at // 64]) * 64 + at % 64], device="cuda"))
+            out, lse = kv2.attend(q, table, kv_lens, window=window, return_lse=True)
+            assert torch.equal(out[~seen], clean[~seen]) and torch.equal(lse[~seen], clean_lse[~seen])
+            assert torch.isnan(out[seen][..., 32:64]).all()
+            if which == 0:
+                assert torch.isnan(out[seen]).all() and torch.isnan(lse[seen]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_many_rows_a_query_of_nan_spoils_its_own_row_alone(d):
+    for dtype in (F16, BF16):
+        kv, seqs, q, table, kv_lens, start = _problem(1400 + d, [900], [500], 4, 8, d, 64, dtype)
+        assert _takes(kv, q, table, ragged=False) == "many_rows"
+        clean = kv.attend(q.cuda(), table, kv_lens)
+        q[250, 1, 5] = float("nan")
+        out = kv.attend(q.cuda(), table, kv_lens)
+        assert torch.isnan(out[250, 1]).all()
+        out[250, 1] = clean[250, 1]
+        assert torch.equal(out, clean)
+
+
+FEW = {  # for kv_split.cu: a job a CTA; dealt out, joined; sixteen rows at once
+    "short": ([333, 17, 0, 140], [1, 1, 1, 1], 4, 4, 64),
+    "dealt": ([5000, 31, 9000], [1, 1, 1], 2, 8, 64),
+    "drafts": ([3000, 700, 2, 900], [4, 1, 5, 3], 2, 4, 32),
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("rows,name", [("few_rows", n) for n in FEW] + [("many_rows", n) for n in ("short", "dealt", "halves")])
+def test_bits_repeat_whatever_the_workspace_held_and_on_two_streams(rows, name, d):
+    lens, new, h, share, page = (FEW if rows == "few_rows" else MANY)[name]
+    kv, seqs, q, table, kv_lens, start = _problem(1500 + d, lens, new, h, share, d, page, BF16)
+    assert _takes(kv, q, table) == rows
+    x, qs = q.cuda(), torch.from_numpy(start).cuda()
+    work = kv.attend_workspace(q.shape[0], q.shape[1], len(lens))
+    first = None
+    for fill in (0, 0xFF, 0x7C):
+        work.fill_(fill)
+        got = kv.attend(x, table, kv_lens, q_start=qs, return_lse=True, workspace=work)
+        first = first or got
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+    _check_each(*first, q, seqs, lens, start, BF16)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    results = []
+    for _ in range(4):
+        for s in streams:
+            results.append(kv.attend(x, table, kv_lens, q_start=qs, return_lse=True, stream=s))
+    torch.cuda.synchronize()
+    for got in results:
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lens,new,h,share", [([333, 20], [1, 1], 4, 2), ([700, 50, 0], [5, 3, 2], 2, 4),
+                                              ([500, 130], [500, 130], 2, 8), ([1200, 600], [300, 600], 3, 4)])
+def test_a_page_table_wider_than_the_sequences(lens, new, h, share, d):
+    """As a captured step has it, for any later length: columns of no page, and of
+    pages that are others'."""
+    kv, seqs, q, table, kv_lens, start = _problem(1600 + d, lens, new, h, share, d, 32, F16)
+    for fill in (-1, 0):
+        wide = torch.full((len(lens), 1000), fill, dtype=torch.int32, device="cuda")
+        for b, n in enumerate(lens):
+            wide[b, :-(-n // 32)] = table[b, :-(-n // 32)]
+        out, lse = kv.attend(q.cuda(), wide, kv_lens, q_start=torch.from_numpy(start).cuda(), return_lse=True)
+        _check_each(out, lse, q, seqs, lens, start, F16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_many_rows_strides_and_rows_left_alone(d):
+    """q_start left out; q a slice of a fused projection, out heads first."""
+    new, lens, h, share = 300, [450, 300, 304], 2, 4
+    kv, seqs, q, table, kv_lens, start = _problem(1700 + d, lens, [new] * 3, h, share, d, 32, BF16)
+    assert _takes(kv, q, table, ragged=False) == "many_rows"
+    fused = torch.zeros(3 * new, 12, d, dtype=BF16, device="cuda")
+    fused[:, 2:10] = q.cuda()
+    around = torch.full((9, 3 * new, d), 3.0, dtype=BF16, device="cuda")
+    kv.attend(fused[:, 2:10], table, kv_lens, out=around[:8].transpose(0, 1))
+    _check_each(around[:8].transpose(0, 1), None, q, seqs, lens, start, BF16)
+    assert (around[8] == 3.0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_many_rows_captured_calls_follow_their_buffers(d):
+    """A prompt's rows appended and attended over, captured once and replayed over
+    other rows, lengths and pages."""
+    rng = np.random.default_rng(d)
+    h, share, page, most, batch = 2, 8, 16, 256, 2
+    kv = dsq.KVCache(h, d, 64, page)
+    k, v = (torch.zeros(batch * most, h, d, dtype=F16, device="cuda") for _ in range(2))
+    q = torch.zeros(batch * most, h * share, d, dtype=F16, device="cuda")
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device="cuda")
+    slots = torch.full((batch * most,), -1, dtype=torch.int64, device="cuda")
+    table = torch.zeros(batch, 32, dtype=torch.int32, device="cuda")
+    lens, start = torch.zeros(batch, dtype=torch.int32, device="cuda"), torch.zeros(batch + 1, dtype=torch.int32, device="cuda")
+    work = kv.attend_workspace(q.shape[0], q.shape[1], batch)
+    assert _takes(kv, q, table) == "many_rows"
+
+    def step():
+        kv.append(k, v, slots)
+        kv.attend(q, table, lens, q_start=start, out=out, lse=lse, workspace=work)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for new in ([256, 256], [30, 200], [0, 1], [129, 255]):
+        x = torch.from_numpy(rng.standard_normal(tuple(q.shape))).half()
+        rows = [_rows(rng, batch * most, h, d).half() for _ in range(2)]
+        pages = rng.permutation(64).reshape(batch, 32)
+        at, seqs, where = 0, [], np.full(batch * most, -1)
+        for b, n in enumerate(new):
+            t = np.arange(n)
+            where[at:at + n] = pages[b, t // page] * page + t % page
+            seqs.append(tuple(_held(r[at:at + n]) for r in rows))
+            at += n
+        for to, what in ((k, rows[0]), (v, rows[1]), (q, x), (slots, torch.from_numpy(where)), (table, torch.from_numpy(pages)),
+                         (lens, torch.tensor(new)), (start, torch.tensor([0, new[0], sum(new)]))):
+            to.copy_(what)
+        out.fill_(3.0)
+        g.replay()
+        _check_each(out, lse, x, seqs, new, [0, new[0], sum(new)], F16)
+        assert (out[sum(new):] == 3.0).all()
