@@ -26,13 +26,13 @@ __host__ __device__ constexpr int kv_words(int D, int which) { return kKvTile * 
 // and mul = ceil(2^(31 + l) / d), n mul / 2^(31 + l) exceeds n / d by less than
 // n / 2^(31 + l) < 1 / d.
 struct KvDivisor {
-    uint32_t mul, shift, d;
+    uint32_t mul, shift;
     __device__ __forceinline__ int div(int n) const { return (int)(((uint64_t)(uint32_t)n * mul) >> shift); }
 };
 inline KvDivisor kv_divisor(int d) {
     uint32_t l = 0;
     while ((1ll << l) < d) l++;
-    return {(uint32_t)(((1ull << (31 + l)) + d - 1) / d), 31 + l, (uint32_t)d};
+    return {(uint32_t)(((1ull << (31 + l)) + d - 1) / d), 31 + l};
 }
 
 struct KvView {
@@ -145,6 +145,19 @@ struct KvOnce {
         return true;
     }
 };
+
+// SMs of a device, asked for once; 0 if CUDA does not say.
+inline int kv_sm_count(int device) {
+    static std::atomic<int> known[64];
+    int n = device < 64 ? known[device].load(std::memory_order_relaxed) : 0;
+    if (n) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (device < 64) known[device].store(n, std::memory_order_relaxed);
+    return n;
+}
 
 // Few query rows per sequence (kv_split.cu).
 size_t kv_split_workspace();

@@ -9,15 +9,7 @@ using namespace dsq;
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-
-int sm_count(int device) {
-    static std::atomic<int> known[64];
-    if (device < 64 && known[device].load(std::memory_order_relaxed)) return known[device].load(std::memory_order_relaxed);
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n < 1) n = 1;
-    if (device < 64) known[device].store(n, std::memory_order_relaxed);
-    return n;
-}
+constexpr int kMeasuredSms = 148;  // of the GPU that the estimates below were measured on
 
 // Rows of a job: query tokens of a sequence, on average, times the heads of a group.
 double rows_of(const dsq_kv_desc *d, const dsq_kv_queries *a) {
@@ -30,14 +22,14 @@ double rows_of(const dsq_kv_desc *d, const dsq_kv_queries *a) {
 // tokens and takes four units' time more for each tile of rows; kv_prompt.cu on
 // units of 256 rows (128 at 256 dimensions) x 128 tokens and three units' time
 // more for each piece, three quarters of the time for up to 128 rows.
-// Measured, fp16, causal, microseconds (kv_split / kv_prompt), of (sequences x
+// Measured on kMeasuredSms SMs, fp16, causal, microseconds (kv_split / kv_prompt), of (sequences x
 // kv heads, rows, tokens):
 //   128 dimensions: (8, 96, 4096) 21 / 26, (8, 96, 16384) 44 / 33,
 //     (64, 24, 4096) 35 / 40, (64, 96, 1024) 33 / 26, (64, 96, 256) 20 / 13,
 //     (512, 24, 256) 33 / 43, (512, 96, 256) 79 / 48
 //   64: (64, 48, 4096) 30 / 38, (64, 96, 256) 16 / 11, (512, 96, 256) 39 / 35
 //   256: (64, 16, 4096) 51 / 77, (64, 48, 1024) 47 / 34, (8, 96, 1024) 16 / 31
-bool many_rows(const dsq_kv_desc *d, const dsq_kv_queries *a) {
+bool many_rows(const dsq_kv_desc *d, const dsq_kv_queries *a, int sms) {
     const double each = a->batch ? (double)a->q_tokens / a->batch : 0.0, rows = rows_of(d, a);
     if (rows <= 8 || d->pages == 0) return false;
     const double jobs = (double)a->batch * d->kv_heads;
@@ -47,12 +39,12 @@ bool many_rows(const dsq_kv_desc *d, const dsq_kv_queries *a) {
     const bool wide = d->head_dim == 256;
     const double few_unit = d->head_dim == 64 ? 0.8e-3 : d->head_dim == 128 ? 1.36e-3 : 1.95e-3;
     const double few_tiles = jobs * ceil(rows / (wide ? 8 : 16));
-    const double few = (few_tiles <= 148 ? 8.0 : 12.0) + few_unit * few_tiles * (ceil(tokens / 32) + 4);
+    const double few = (few_tiles <= sms ? 8.0 : 12.0) + few_unit * ((double)kMeasuredSms / sms) * few_tiles * (ceil(tokens / 32) + 4);
     const double many_unit = (d->head_dim == 64 ? 2.0 : d->head_dim == 128 ? 2.7 : 3.7) * (rows <= 128 && !wide ? 0.75 : 1.0);
     const double many_tiles = jobs * ceil(rows / (wide ? 128 : 256)), units = ceil(tokens / 128);
-    const double many = many_tiles <= 148 && units <= 4
+    const double many = many_tiles <= sms && units <= 4
                             ? 7.0 + many_unit * (units + 1)
-                            : 12.0 + many_unit * fmax(fmin(units + 3, 7.0), many_tiles * (units + 3) / 148);
+                            : 12.0 + many_unit * fmax(fmin(units + 3, 7.0), many_tiles * (units + 3) / sms);
     return many < few;
 }
 
@@ -78,7 +70,9 @@ int check_shape(const dsq_kv_desc *d, const dsq_kv_queries *a) {
 
 extern "C" int dsq_kv_attend_kernel(const dsq_kv_desc *d, const dsq_kv_queries *a) {
     const int rc = check_shape(d, a);
-    return rc != DSQ_OK ? rc : many_rows(d, a) ? 1 : 0;
+    if (rc != DSQ_OK) return rc;
+    const int sms = kv_sm_count(d->device);
+    return many_rows(d, a, sms ? sms : kMeasuredSms) ? 1 : 0;
 }
 
 extern "C" int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_kv_queries *a, void *workspace,
@@ -127,8 +121,9 @@ extern "C" int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_
     k.page_table = a->page_table;
     k.kv_lens = a->kv_lens;
     k.q_start = a->q_start;
-    const int sms = sm_count(d->device);
-    return many_rows(d, a) ? launch_kv_prompt(k, d->head_dim, a->dtype, workspace, sms, (cudaStream_t)stream)
+    const int sms = kv_sm_count(d->device);
+    if (sms < 1) return DSQ_ERR_CUDA;
+    return many_rows(d, a, sms) ? launch_kv_prompt(k, d->head_dim, a->dtype, workspace, sms, (cudaStream_t)stream)
                            : launch_kv_split(k, d->head_dim, a->dtype, workspace, sms, (cudaStream_t)stream);
 }
 

@@ -350,7 +350,9 @@ extern "C" int dsq_kv_read(const dsq_kv_desc *d, const void *cache, const dsq_kv
     if (!guard.ok) return DSQ_ERR_CUDA;
     const KvView c = kv_view(d, cache);
     const cudaStream_t st = (cudaStream_t)stream;
-    const bool many = (double)tokens * d->kv_heads * d->head_dim / 8 >= 4.0 * 8 * 148 * kThreads;
+    const int sms = kv_sm_count(d->device);
+    if (sms < 1) return DSQ_ERR_CUDA;
+    const bool many = (double)tokens * d->kv_heads * d->head_dim / 8 >= 4.0 * 8 * sms * kThreads;
     if (d->head_dim == 64)
         return many ? launch_read<64, 4>(c, rows, slots, tokens, st) : launch_read<64, 1>(c, rows, slots, tokens, st);
     if (d->head_dim == 128)

@@ -518,8 +518,8 @@ DSQ_API int dsq_kv_attend(const dsq_kv_desc *d, const void *cache, const dsq_kv_
 
 /*
  * dsq_kv_attend_kernel -- which kernel such a call takes: 0, the one for few
- * rows; 1, the one for many.  Host-only; of `a` it reads the numbers and
- * whether q_start is NULL.  Returns that, or DSQ_ERR_INVALID_ARG or
+ * rows; 1, the one for many.  Host-only (without the device, as for a B200's
+ * 148 SMs); of `a` it reads the numbers and whether q_start is NULL.  Returns that, or DSQ_ERR_INVALID_ARG or
  * DSQ_ERR_UNSUPPORTED as dsq_kv_attend would.
  */
 DSQ_API int dsq_kv_attend_kernel(const dsq_kv_desc *d, const dsq_kv_queries *a);
