@@ -86,11 +86,20 @@ __device__ __forceinline__ uint32_t ends_of(uint4 raw) {
     return P::min_nan(ends, __shfl_xor_sync(kFull, ends, 2));
 }
 
-// x / s rounded to an integer, ties to even, as a float above 3 * 2^22.  One
-// Newton step on x times the rounded reciprocal gives the correctly rounded
-// quotient.  x (11 bits) over s (7 bits) against a border k + 1/2 (5 bits):
-// two numbers of 16 bits at most that are equal or 2^-16 apart, so it lies on
-// the same side as the exact one.  `most`: an integer not to be passed.
+// x / s rounded to an integer, ties to even, as a float above 3 * 2^22: the
+// quotient by Markstein's residual correction of x times the rounded
+// reciprocal.  (His theorem, IBM J. Res. Dev. 34, 1990, makes the result the
+// correctly rounded quotient where y is within an ulp of it and the residual is
+// exact; y may be two ulps and a bit off here, so what follows does without.)
+//   y = x inv (1 + e), |e| <= 2^-24, and inv = (1 + e') / s, |e'| <= 2^-24: y is
+//   less than 2^-22.9 of itself off.  x - y s is a multiple of the product of
+//   the last bits of y and of s (7 bits), fewer than 2^10 of them, so the first
+//   fused step is exact.  The second rounds x / s with an error of 2^-24 of the
+//   correction, 2^-46 of itself.  (An x far below s gives 0, underflow or not.)
+// x (11 bits) over s (7 bits) against a border k + 1/2 (5 bits): two numbers of
+// 16 bits at most, equal or 2^-16 apart.  Equal, the border is a float and the
+// one nearest to what is rounded; else the result lies on the exact quotient's
+// side of it.  `most`: an integer not to be passed.
 constexpr float kRound = 12582912.0f;
 __device__ __forceinline__ float rounded(float x, float s, float inv, float most) {
     const float y = x * inv;

@@ -17,10 +17,10 @@
 //                   one exceeds it by more than 2^8 in the numerator (then the
 //                   output so far is rescaled in tensor memory), writes the
 //                   numerators back as fp16 over the scores.
-//   warps 8-11      bring K and V: codes from global memory to registers a
-//                   unit ahead, unpacked exactly to fp16 (kv_device.h) into the
-//                   128-byte-swizzled tiles of a ring in shared memory.  Eight
-//                   dimensions come out as 0 4 1 5 2 6 3 7; the queries are
+//   warps 8-11      bring K and V: codes by cp.async into each warp's own
+//                   place in shared memory a unit ahead, unpacked from there
+//                   exactly to fp16 (kv_device.h) into the 128-byte-swizzled
+//                   tiles of a ring.  Eight dimensions come out as 0 4 1 5 2 6 3 7; the queries are
 //                   stored in that order, the output's columns renamed.
 //   warp 14         works out the run and its pieces, ahead of the others.
 //   warps 12, 13    issue the products of row tile 0, 1: S = Q K^T (K-major),
