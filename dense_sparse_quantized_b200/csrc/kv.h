@@ -107,7 +107,9 @@ inline bool kv_rows_apart(int64_t tokens, int64_t heads, int64_t token, int64_t 
 // The kernels are launched early, while the one before them in the stream still
 // runs (programmatic dependent launch): they touch no memory of the caller's
 // before kv_after_previous(), which waits until that one has ended, and let
-// the next one be launched as early.
+// the next one be launched as early.  No pointer to what an earlier kernel may
+// have written is __restrict__: with it a load counts as one of constant memory,
+// which the compiler is free to move up past the wait.
 __device__ __forceinline__ void kv_after_previous() {
     asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
 }

@@ -152,8 +152,8 @@ inline KvCarry *kv_carries(void *workspace) {
 // four heads of 7449 tokens: 22 us for the whole attention with one warp's loop
 // over them, 12 us so).
 template <int D, int R, int N, bool SHARED, typename T>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ KvAttend a, const float *__restrict__ parts,
-                                                   const KvCarry *__restrict__ carries) {
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ KvAttend a, const float *parts,
+                                                   const KvCarry *carries) {
     kv_after_previous();
     constexpr int E = D / 32, S = SHARED ? 8 : 1;  // elements of a lane; warps to a row
     static_assert(!SHARED || N == 1, "");
@@ -180,15 +180,23 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ KvAtt
 #pragma unroll(N == 1 ? 8 : 2)
     for (int i = mine; i <= c.more; i += S) {
         const size_t of = part(i);
+        float tops[N], sums[N];
+        float2 v[N][E / 2];
+#pragma unroll
+        for (int n = 0; n < N; n++) {  // all of a part's loads are under way together
+            tops[n] = ends[of + n];
+            sums[n] = ends[of + R + n];
+#pragma unroll
+            for (int e = 0; e < E; e += 2) v[n][e / 2] = *reinterpret_cast<const float2 *>(at + of + n * D + e);
+        }
 #pragma unroll
         for (int n = 0; n < N; n++) {
-            const float f = ex2(ends[of + n] - top[n]);
-            sum[n] += ends[of + R + n] * f;
+            const float f = ex2(tops[n] - top[n]);
+            sum[n] += sums[n] * f;
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
-                const float2 v = *reinterpret_cast<const float2 *>(at + of + n * D + e);
-                x[n][e] += v.x * f;
-                x[n][e + 1] += v.y * f;
+                x[n][e] += v[n][e / 2].x * f;
+                x[n][e + 1] += v[n][e / 2].y * f;
             }
         }
     }

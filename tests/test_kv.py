@@ -1168,3 +1168,75 @@ def test_many_rows_captured_calls_follow_their_buffers(d):
         g.replay()
         _check_each(out, lse, x, seqs, new, [0, new[0], sum(new)], F16)
         assert (out[sum(new):] == 3.0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("rows,name", [("few_rows", "dealt"), ("many_rows", "dealt")])
+def test_calls_that_follow_one_another_read_nothing_early(rows, name, d):
+    """append, attend, read and attend again, launched early behind one another on one
+    stream and one workspace, many times over: each call sees what the one before
+    it wrote."""
+    lens, new, h, share, page = (FEW if rows == "few_rows" else MANY)[name]
+    kv, seqs, q, table, kv_lens, start = _problem(1800 + d, lens, new, h, share, d, page, F16)
+    assert _takes(kv, q, table) == rows
+    qs = torch.from_numpy(start).cuda()
+    rng = np.random.default_rng(d)
+    sets = []
+    page0 = int(table[0, 0])
+    slots = torch.arange(page, device="cuda") + page0 * page
+    for i in range(2):   # two contents of the first page, two sets of queries
+        k, v = (_rows(rng, page, h, d).half().cuda() for _ in range(2))
+        sets.append((torch.randn(q.shape, generator=torch.Generator("cuda").manual_seed(i), device="cuda").half(), k, v))
+    work = kv.attend_workspace(q.shape[0], q.shape[1], len(lens))
+    want = []
+    for x, k, v in sets:
+        kv.append(k, v, slots)
+        torch.cuda.synchronize()
+        out, lse = kv.attend(x, table, kv_lens, q_start=qs, return_lse=True, workspace=work)
+        torch.cuda.synchronize()
+        want.append((out, lse, *kv.read(slots)))
+        torch.cuda.synchronize()
+    outs = [(torch.zeros_like(q, device="cuda"), torch.zeros(q.shape[:2], device="cuda"),
+             *(torch.zeros(page, h, d, dtype=F16, device="cuda") for _ in range(2))) for _ in range(20)]
+    torch.cuda.synchronize()
+    for i, (out, lse, k_out, v_out) in enumerate(outs):
+        x, k, v = sets[i % 2]
+        kv.append(k, v, slots)
+        kv.attend(x, table, kv_lens, q_start=qs, out=out, lse=lse, workspace=work)
+        kv.read(slots, k=k_out, v=v_out)
+    torch.cuda.synchronize()
+    for i, got in enumerate(outs):
+        assert all(torch.equal(g, w) for g, w in zip(got, want[i % 2])), i
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits,mode,batch", [(3, "affine", 1), (3, "affine", 2), (3, "affine", 16), (3, "lut", 1), (4, "lut", 1),
+                                             (4, "lut", 3), (4, "lut", 8), (2, "bitplane", 1), (3, "bitplane", 4), (14, "intgrid", 1)])
+def test_a_product_launched_early_behind_attention_reads_its_output(bits, mode, batch):
+    """Attention lets the product behind it start while it still runs; the product's
+    rows are the attention's all the same, bit for bit as after a synchronisation."""
+    import synth
+    h, heads, d, rows = 2, 8, 128, 512
+    p = synth.make_problem(rows, heads * d, bits, mode, 0.01, "uniform", 3, 1)
+    with dsq.Handle(dsq.pack_problem(p)) as mat:
+        n = 20000 // batch
+        kv, _, _, table, kv_lens, _ = _problem(1900, [n] * batch, [1] * batch, h, heads // h, d, 64, F16)
+        qs = [torch.randn(batch, heads, d, generator=torch.Generator("cuda").manual_seed(i), device="cuda").half() for i in range(2)]
+        work = kv.attend_workspace(batch, heads, batch)
+        want = []
+        for q in qs:
+            out = kv.attend(q, table, kv_lens, workspace=work)
+            torch.cuda.synchronize()
+            want.append(mat.gemv(out.view(batch, heads * d)))
+            torch.cuda.synchronize()
+        out = torch.zeros(batch, heads, d, dtype=F16, device="cuda")
+        ys = torch.zeros(20, batch, rows, dtype=F16, device="cuda")
+        torch.cuda.synchronize()
+        for i in range(20):
+            kv.attend(qs[i % 2], table, kv_lens, out=out, workspace=work)
+            mat.gemv(out.view(batch, heads * d), ys[i])
+        torch.cuda.synchronize()
+        for i in range(20):
+            assert torch.equal(ys[i], want[i % 2]), i
+        assert not torch.equal(want[0], want[1])
