@@ -1240,3 +1240,38 @@ def test_a_product_launched_early_behind_attention_reads_its_output(bits, mode, 
         for i in range(20):
             assert torch.equal(ys[i], want[i % 2]), i
         assert not torch.equal(want[0], want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [1, 3, 400])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attend_without_pages_or_columns(d, new):
+    """No cache memory, no column of the page table, no token of any sequence."""
+    q = torch.randn(2 * new, 8, d, device="cuda").half()
+    lens = torch.tensor([5, 900], dtype=torch.int32, device="cuda")
+    for pages, cols, n in ((0, 3, lens), (4, 0, lens), (0, 0, lens), (4, 3, lens * 0), (4, 3, -lens)):
+        kv = dsq.KVCache(2, d, pages, 16)
+        if pages:
+            kv.data.fill_(0xFF)
+        table = torch.zeros(2, cols, dtype=torch.int32, device="cuda")
+        for start in (None, torch.tensor([0, new, 2 * new], dtype=torch.int32, device="cuda")):
+            for causal in (True, False):
+                out, lse = kv.attend(q, table, n, q_start=start, causal=causal, out=torch.ones_like(q), return_lse=True)
+                assert not out.any() and torch.isneginf(lse).all()
+    kv = dsq.KVCache(2, d, 4, 16)   # no sequence, no row
+    none = kv.attend(q[:0], torch.zeros(0, 3, dtype=torch.int32, device="cuda"), lens[:0])
+    assert none.shape == (0, 8, d)
+    assert kv.attend(q[:0], torch.zeros(2, 3, dtype=torch.int32, device="cuda"), lens).shape == (0, 8, d)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [1, 5])
+def test_attend_one_page_for_all_and_queries_shared_by_heads(new):
+    """A page as large as the sequence, one kv head for 1500 query heads that are one
+    and the same row in memory."""
+    n, page, d = 3000, 4096, 64
+    kv, seqs, q, table, kv_lens, start = _problem(1950, [n], [new], 1, 1, d, page, BF16, extra=0)
+    heads = 1500
+    out, lse = kv.attend(q.cuda().expand(new, heads, d), table, kv_lens, return_lse=True)
+    # each within its bounds; not bit for bit alike, as the jobs' tokens are dealt out at different places
+    _check_each(out, lse, q.expand(new, heads, d), seqs, [n], start, BF16)
