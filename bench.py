@@ -49,8 +49,9 @@ def parse_args(argv=None):
     ap.add_argument("--config", default="c2")
     ap.add_argument("--batch", type=int, default=1)
     ap.add_argument("--impl", default="dsq", choices=["dsq", "reference"])
-    ap.add_argument("--op", default="gemv", choices=["gemv", "decompose"],
-                    help="decompose: time the on-device decomposition of the config's weights instead")
+    ap.add_argument("--op", default="gemv", choices=["gemv", "decompose", "kv"],
+                    help="decompose: time the on-device decomposition of the config's weights instead; "
+                         "kv: the key/value cache's cases of perf/operators.py (--config NAME,NAME or all)")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--e2e-steps", type=int, default=200)
     return ap.parse_args(argv)
@@ -565,6 +566,85 @@ def run_decompose(args):
     return 0
 
 
+def kv_states(bytes_per_pass: float, state_bytes: int, l2: int) -> int:
+    """States to rotate over so that what passes between two uses of one is more
+    than twice the L2, as far as 40 GB hold them."""
+    return max(2, min(math.ceil(2 * l2 / bytes_per_pass) + 1, 40 * 10**9 // max(1, state_bytes)))
+
+
+def run_kv(args):
+    """The cases of perf/operators.py on one GPU, through the library's calls.
+    Two times a case, over rotating states: a call among others (CUDA graphs of
+    calls back to back; each kernel starts early, while the call before it
+    ends), and a call apart (CUDA events around one call after a device-side
+    sleep: nothing overlaps it)."""
+    import torch
+    from perf import operators
+    operators.own = True
+    rank, world, local = dist_env()
+    torch.cuda.set_device(local)
+    l2 = torch.cuda.get_device_properties(local).L2_cache_size
+    peak, peak_src = measured_peaks()
+    names = None if args.config in ("all", "c2") else args.config.split(",")
+    cases = [c for c in operators.listed() if names is None or c["name"] in names]
+    if names is not None and len(cases) != len(names):
+        raise SystemExit(f"--config: names of perf/operators.py's listed cases, not {args.config}")
+    for case in cases:
+        work = operators.work(case)
+        torch.cuda.empty_cache()
+        before = torch.cuda.memory_allocated()
+        states = [operators.prepare(case, 1)]
+        n = kv_states(work["bytes"], torch.cuda.memory_allocated() - before, l2)
+        states += [operators.prepare(case, 1 + i) for i in range(1, n)]
+        stream = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            for i in range(max(3, args.warmup)):
+                operators.run(states[i % n])
+        stream.synchronize()
+        calls = n * max(1, 120 // n)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            for i in range(calls):
+                operators.run(states[i % n])
+        replays = max(3, min(args.steps // calls, 50))
+        marks = [torch.cuda.Event(enable_timing=True) for _ in range(replays + 1)]
+        apart = []
+        with ClockSampler(local) as clocks, torch.cuda.stream(stream):
+            g.replay()
+            for m in marks:
+                m.record(stream)
+                if m is not marks[-1]:
+                    g.replay()
+            stream.synchronize()
+            for i in range(60):
+                a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+                torch.cuda._sleep(200000)   # ~0.1 ms of device time
+                a.record(stream)
+                operators.run(states[i % n])
+                b.record(stream)
+                b.synchronize()
+                if i >= 10:
+                    apart.append(a.elapsed_time(b) * 1e3)
+        states[0]["kv"].check()     # raises if a kernel gave up a bounded wait
+        per = [a.elapsed_time(b) * 1e3 / calls for a, b in zip(marks, marks[1:])]
+        us, us_apart = statistics.median(per), statistics.median(apart)
+        gbs = work["bytes"] / us / 1e3
+        line = {"metric": "key/value cache operators: us per pass, GB/s on bytes read once and written once",
+                "value": gbs, "unit": "GB/s", "n_gpus": 1, "steps": replays * calls, "warmup": args.warmup,
+                "ms_per_step": us / 1e3, "us_per_call": us, "us_apart": us_apart, "tflops": work["flops"] / us / 1e6,
+                "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": case["dtype"], "data": "synthetic",
+                "config": {"workload": case["name"], **case, "algorithmic_bytes": work["bytes"], "flops": work["flops"],
+                           "l2": f"rotating {n} states ({n * work['bytes'] / 1e6:.0f} MB read and written, 2x L2 is {2 * l2 / 1e6:.0f} MB)",
+                           "timing": f"median of {replays} CUDA graph replays of {calls} calls back to back; apart: median of 50"},
+                "roofline": {"bound": "hbm", "achieved": gbs, "peak": peak, "unit": "GB/s", "frac": gbs / peak, "traffic": None,
+                             "peak_source": peak_src, "frac_apart": work["bytes"] / us_apart / 1e3 / peak},
+                "clocks": clocks.summary()}
+        print(json.dumps(line), flush=True)
+        del g, states
+    return 0
+
+
 def ctypes_workspace_bytes(dsq, M, N, bits, mode, nnz):
     import ctypes
     d = dsq.Desc(M, N, bits, dsq.MODE_LUT_ROW if mode == "lut" else dsq.MODE_AFFINE_G16, nnz)
@@ -580,6 +660,8 @@ def main(argv=None):
         return run_reference(args)
     if args.op == "decompose":
         return run_decompose(args)
+    if args.op == "kv":
+        return run_kv(args)
     return run_dsq(args)
 
 

@@ -119,3 +119,14 @@ def test_oracle_rate_threads_cover_every_row_once(monkeypatch):
     assert n == 1 and gbs > 0
     assert len(seen) == 4
     assert np.array_equal(np.sort(np.concatenate(seen)), np.arange(p.rows))
+
+
+def test_cache_cases_rotate_over_more_than_the_l2():
+    l2 = 126 * 10**6
+    from perf import operators
+    for case in operators.listed():
+        b = operators.work(case)["bytes"]
+        assert bench.kv_states(b, 10**6, l2) * b > 2 * l2
+    assert bench.kv_states(10**5, 10**9, l2) == 40      # what the memory holds
+    assert bench.kv_states(10**10, 10**11, l2) == 2
+    assert bench.parse_args(["--op", "kv", "--config", "token_long"]).op == "kv"
