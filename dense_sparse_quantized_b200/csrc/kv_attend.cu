@@ -29,6 +29,9 @@ double rows_of(const dsq_kv_desc *d, const dsq_kv_queries *a) {
 //     (512, 24, 256) 33 / 43, (512, 96, 256) 79 / 48
 //   64: (64, 48, 4096) 30 / 38, (64, 96, 256) 16 / 11, (512, 96, 256) 39 / 35
 //   256: (64, 16, 4096) 51 / 77, (64, 48, 1024) 47 / 34, (8, 96, 1024) 16 / 31
+// All with page tables as wide as the sequences are long.  The lengths are on
+// the device: a wider table is taken for longer sequences, and a batch that
+// mixes prompts with single tokens for one of average rows.
 bool many_rows(const dsq_kv_desc *d, const dsq_kv_queries *a, int sms) {
     const double each = a->batch ? (double)a->q_tokens / a->batch : 0.0, rows = rows_of(d, a);
     if (rows <= 8 || d->pages == 0) return false;

@@ -6,9 +6,10 @@
 // one 4-byte word of codes each, so a warp's accesses are whole 32-byte
 // sectors on both sides.  Four neighbouring threads share a group of 32.
 //
-// Measured on one B200: reading 65536 tokens of 8 heads of 128 to fp16, 344 MB,
-// takes 61 us, 5.6 TB/s (0.86 of a copy's rate): bound by HBM.  Writing 16384
-// such tokens of bf16, 86 MB, takes 27 us, 3.2 TB/s: bound by issue (80 %) and
+// Measured on one B200, among other calls (bench.py --op kv): reading 65536
+// tokens of 8 heads of 128 to fp16, 344 MB, takes 61 us, 5.6 TB/s (0.86 of a
+// copy's rate; 66 us apart): bound by HBM.  Writing 16384 such tokens of bf16, 86
+// MB, takes 27 of the 40 us of writing and reading back: bound by issue (80 %) and
 // the ALU pipe, about 20 instructions a value for quotient, rounding, clipping
 // and packing.  IEEE divisions and fp64 scales took 57 us for the same.
 #include "kv_device.h"

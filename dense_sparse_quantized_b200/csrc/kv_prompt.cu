@@ -36,20 +36,22 @@
 // a NaN numerator; which tokens these are, and pages that do not exist, goes
 // beside the tiles in `flags`.
 //
-// Measured on one B200: a prompt of 6000 tokens, 32 query heads on 8 kv heads of
-// 128, bf16, takes 355 us, 831 TFLOP/s of the scores that are seen (0.50 of a
-// burst bf16 product's rate).  A unit takes a pair about 4400 cycles: 1024 each
+// Measured on one B200, among other calls (bench.py --op kv): a prompt of 6000
+// tokens, 32 query heads on 8 kv heads of 128, bf16, takes 370 to 376 us, 784 to
+// 797 TFLOP/s of the scores that are seen (0.47 to 0.48 of a burst bf16 product's
+// rate; 385 to 390 us apart).  A unit takes a pair about 4400 cycles: 1024 each
 // for its two products (64 for each of 16 instructions, measured alone and
 // beside everything else), 1500 for 128 exponentials a thread (1024 at the
 // pipe's rate), 600 for the scores and their maximum, the rest waiting for one
-// another.  What the steps brought: products issued by one thread each from
+// another.  What the steps brought, in runs too short for the power cap: products issued by one thread each from
 // unrolled loops, not through local memory, 890 -> 764 us; loops rolled and
 // unpacking by cp.async from shared memory, 708 -> 621; a product warp for each
 // pair and numerators handed over by halves, 621 -> 527; pieces' own cost dealt
 // too, 527 -> 468; no 64-bit division, 474 -> 427; turns at the exponentials,
 // 444 -> 402 (in step, both pairs wait for the same pipe); pieces worked out by
 // a warp of its own, 402 -> 387; the first half's numerators handed over while the
-// second's are worked out, 387 -> 382; parts joined a row a warp, 382 -> 355.
+// second's are worked out, 387 -> 382; parts joined a row a warp, 382 -> 355
+// (355 us at 1965 MHz are the 376 at the 1867 of a longer run).
 //
 // Every mbarrier wait is bounded (ptx.h).  One that runs out sets the device's
 // status word, which dsq_kv_check reports, and ends its role; the others' waits

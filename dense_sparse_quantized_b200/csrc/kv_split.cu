@@ -34,14 +34,15 @@
 // 2^8 in the numerator (one vote a unit); until then numerators up to 2^15 are
 // as exact as ones up to 2^7, which they are at the maximum (kLift).
 //
-// Measured on one B200: four sequences of 100000 to 131072 tokens, 64 query
-// heads on 8 kv heads of 128, 558 MB of cache, take 129 us, 4.3 TB/s (0.66 of a
-// copy's rate); 48 uneven ones up to 4096, 115 MB, 43 us.  Bound by issue: about
+// Measured on one B200, among other calls (bench.py --op kv): four sequences of
+// 100000 to 131072 tokens, 64 query heads on 8 kv heads of 128, 558 MB of cache,
+// take 137 to 141 us, 4.0 TB/s (0.60 of a copy's rate; 147 to 157 us apart); 48
+// uneven ones up to 4096, 115 MB, 43 us (49 apart).  Bound by issue: about
 // 400 instructions a tile of 2304 bytes, 13 for every eight codes (3 for a pair
 // in both halves of a register, and a shift), at three quarters of the issue
 // rate inside the loop; about 8 us of a call go to finding the run, the first
-// loads and joining.  A loop with the ring's slots in variables took 150 us for
-// the first, partial results in rows (whose stores meet the same banks) 5 us
+// loads and joining.  A loop with the ring's slots in variables took a tenth more
+// for the first, partial results in rows (whose stores meet the same banks) 5 us
 // more, and a run found by every warp in 64-bit numbers 4 us more.
 #include <algorithm>
 

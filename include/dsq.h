@@ -505,9 +505,12 @@ typedef struct {
  * is more.
  * Two kernels, one of warp-level matrix instructions for few rows per kv head
  * and a tcgen05 one for many; a call takes the one that is estimated to be
- * faster, from its rows, its heads and the lengths that its pages allow.  Both
- * deal the batch's work out evenly, so one call may mix long and short
- * sequences.  One launch for few and short ones, else two.
+ * faster for sequences of average rows that fill the page table's width (or
+ * their window).  Both deal the batch's work out evenly, so one call may mix
+ * long and short sequences.  One launch for few jobs and a narrow table, else
+ * two.  The estimate does not know the lengths: where the table is much wider
+ * than the sequences, or prompts share a call with single tokens, it may take
+ * the slower kernel, and short contexts take the second launch.
  * Asynchronous; allocates nothing; the same inputs give the same bits.  A wait
  * that runs out inside the kernels is reported by dsq_kv_check.
  * Returns DSQ_OK, DSQ_ERR_INVALID_ARG, DSQ_ERR_UNSUPPORTED,
