@@ -59,12 +59,21 @@ class KVDesc(ctypes.Structure):
                 ("page_tokens", ctypes.c_int32), ("pages", ctypes.c_int32)]
 
 
-def _kv_desc(*values) -> KVDesc:
-    # ctypes takes a number's low 32 bits
-    values = tuple(int(v) for v in values)
-    if not all(-1 << 31 <= v < 1 << 31 for v in values):
-        raise ValueError(f"device, kv_heads, head_dim, page_tokens and pages must fit 32 bits: {values}")
-    return KVDesc(*values)
+def _kv_numbers(bits, **sizes):
+    """The sizes as ints; refused past ``bits``, whose low part ctypes would take."""
+    for name, v in sizes.items():
+        if not -1 << bits - 1 <= int(v) < 1 << bits - 1:
+            raise ValueError(f"{name} must fit {bits} bits, is {v}")
+    return [int(v) for v in sizes.values()]
+
+
+def _kv_desc(device, kv_heads, head_dim, page_tokens, pages) -> KVDesc:
+    return KVDesc(*_kv_numbers(32, device=device, kv_heads=kv_heads, head_dim=head_dim, page_tokens=page_tokens, pages=pages))
+
+
+def _kv_window(window):
+    """A window past every position is none."""
+    return window if 0 <= window < 1 << 31 else -1 if window < 0 else (1 << 31) - 1
 
 
 class KVRows(ctypes.Structure):
@@ -492,11 +501,10 @@ class KVCache:
         """Scratch for attend() calls of these sizes that follow one another;
         calls that may overlap need one each."""
         size = ctypes.c_size_t(0)
-        if not (-1 << 31 <= q_heads < 1 << 31 and -1 << 31 <= batch < 1 << 31 and -1 << 63 <= q_tokens < 1 << 63):
-            raise ValueError("q_heads and batch must fit 32 bits, q_tokens 64")
+        (n,), (heads, batch) = _kv_numbers(64, q_tokens=q_tokens), _kv_numbers(32, q_heads=q_heads, batch=batch)
         # the size is asked for with a q_start, which a query of it does not read:
         # any number of rows may be any number of sequences'
-        a = KVQueries(q_tokens=int(q_tokens), q_heads=int(q_heads), batch=int(batch), q_start=self._data or 256)
+        a = KVQueries(q_tokens=n, q_heads=heads, batch=batch, q_start=self._data or 256)
         rc = library().dsq_kv_attend(self._d, None, ctypes.byref(a), None, ctypes.byref(size), None)
         if rc != DSQ_ERR_BUFFER_TOO_SMALL:
             _check(rc, "dsq_kv_attend")
@@ -546,10 +554,8 @@ class KVCache:
             workspace = self.attend_workspace(n, heads, batch, stream)
         elif workspace.get_device() != self._index or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {device}")
-        if not 0 <= window < 1 << 31:  # ctypes would take its low 32 bits; one past every position is none
-            window = -1 if window < 0 else (1 << 31) - 1
         a = KVQueries(q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), qs[0], qs[1], os[0], os[1],
-                      n, dtype, heads, batch, columns, causal, window,
+                      n, dtype, heads, batch, columns, causal, _kv_window(window),
                       self.head_dim ** -0.5 if scale is None else scale, page_table.data_ptr(), kv_lens.data_ptr(),
                       None if q_start is None else q_start.data_ptr())
         size = ctypes.c_size_t(workspace.nbytes)
@@ -563,8 +569,9 @@ class KVCache:
                       window=0) -> str:
         """The kernel that attend() calls of these sizes take, "few_rows" or
         "many_rows" (dsq_kv_attend_kernel).  ragged: with a q_start."""
-        a = KVQueries(q_tokens=q_tokens, q_heads=q_heads, batch=batch, table_pages=table_pages, causal=causal,
-                      window=window, q_start=256 if ragged else None)
+        (n,), sizes = _kv_numbers(64, q_tokens=q_tokens), _kv_numbers(32, q_heads=q_heads, batch=batch, table_pages=table_pages)
+        a = KVQueries(q_tokens=n, q_heads=sizes[0], batch=sizes[1], table_pages=sizes[2], causal=causal,
+                      window=_kv_window(window), q_start=256 if ragged else None)
         which = self._lib.dsq_kv_attend_kernel(self._d, ctypes.byref(a))
         if which < 0:
             _check(which, "dsq_kv_attend_kernel")

@@ -9,7 +9,8 @@ S = scale * sum_i |q_i k_ti| (largest over the tokens), P = sum_t p_t |v_t|:
     part of themselves, as 2^-20 covers exp2, its argument's last bits and the
     other fp32 steps: 2 ((D + 8) 2^-23 S + 2^-20) P;
   numerators in fp16: 2^-11 of p_t, or 2^-25 of the running maximum's
-    numerator where that is more (subnormal): 2^-11 P + T 2^-25 max |v|;
+    numerator where that is more (subnormal): 2^-11 P + T 2^-25 max |v|
+    (2^-32, as the header has it, in the tests by kernel and by small numerators);
   the output's rounding: 2^-11 |out| (fp16), 2^-8 |out| (bf16), or 2^-25.
 The log-sum-exp: (D + 8) 2^-23 S + 2^-20 + 2^-22 |lse|.
 """
@@ -1275,3 +1276,17 @@ def test_attend_one_page_for_all_and_queries_shared_by_heads(new):
     out, lse = kv.attend(q.cuda().expand(new, heads, d), table, kv_lens, return_lse=True)
     # each within its bounds; not bit for bit alike, as the jobs' tokens are dealt out at different places
     _check_each(out, lse, q.expand(new, heads, d), seqs, [n], start, BF16)
+
+
+@pytest.mark.gpu
+def test_kernel_question_of_sizes_past_32_bits():
+    kv = dsq.KVCache(2, 64, 4, 16)
+    sizes = dict(q_tokens=400, q_heads=16, batch=1, table_pages=4)
+    assert kv.attend_kernel(**sizes, window=(1 << 32) + 1) == kv.attend_kernel(**sizes, window=(1 << 31) - 1)
+    for name, v in (("q_tokens", 1 << 64), ("q_heads", (1 << 32) + 16), ("batch", (1 << 32) + 1), ("table_pages", 1 << 32)):
+        with pytest.raises(ValueError):
+            kv.attend_kernel(**{**sizes, name: v})
+    for change in (dict(window=-1), dict(window=3, causal=False), dict(q_heads=15)):
+        with pytest.raises(dsq.DSQError) as e:
+            kv.attend_kernel(**{**sizes, **change})
+        assert e.value.status == BAD
